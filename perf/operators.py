@@ -235,7 +235,7 @@ def _own_exchange(s):
     T, k, E, D, t = c["tokens"], c["top_k"], c["experts"], c["cols"], c["dtype"]
     tg.tile_gemm_expert_sort(T, k, E, s["ids"], k, s["offsets"], s["entry_of_row"], s["row_of_entry"],
                              workspace=s["workspace"])
-    tg.tile_gemm_expert_gather(T, k, D, t, s["x"], D, s["entry_of_row"], s["rows"], D)
+    tg.tile_gemm_expert_gather(T, k, D, t, s["x"], D, s["row_of_entry"], s["rows"], D)
     tg.tile_gemm_expert_combine(T, k, D, t, s["y"], D, s["row_of_entry"], s["weights"], k, s["out"], D)
     out = dict(offsets=s["offsets"], entry_of_row=s["entry_of_row"], row_of_entry=s["row_of_entry"],
                rows=s["rows"], out=s["out"])
