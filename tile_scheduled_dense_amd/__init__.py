@@ -50,6 +50,13 @@ EXPORTED = ["tile_gemm", "tile_gemm_strided_batched", "tile_gemm_ex", "tile_gemm
             "tile_gemm_workspace_size", "tg_layout_eval", "tile_gemm_describe_layout", "tile_gemm_lds_offset",
             "tile_gemm_acc_coord", "tile_gemm_status_string", "tile_gemm_abi_version", "tile_gemm_packed_b_ld",
             "tile_gemm_packed_b_size", "tile_gemm_pack_b", "tile_gemm_ex_noalloc"]
+# every symbol include/tile_gemm_experts.h declares
+EXPORTED_EXPERTS = ["tile_gemm_experts_version", "tile_gemm_expert_sort_workspace_size", "tile_gemm_expert_sort",
+                    "tile_gemm_expert_gather", "tile_gemm_expert_combine", "tile_gemm_expert_combine_grad",
+                    "tile_gemm_grouped", "tile_gemm_grouped_wgrad", "tile_gemm_q4_packed_size", "tile_gemm_pack_q4",
+                    "tile_gemm_q4"]
+EXPERTS_VERSION = 1     # TILE_GEMM_EXPERTS_VERSION
+MAX_EXPERTS = 2048      # TILE_GEMM_MAX_EXPERTS
 
 
 class TileGemmError(RuntimeError):
@@ -155,8 +162,29 @@ def _lib():
     lib.tile_gemm_packed_b_size.restype = ci
     lib.tile_gemm_pack_b.argtypes = [i64, i64, i64, ci, vp, i64, i64, ci, vp, i64, vp]
     lib.tile_gemm_pack_b.restype = ci
+    _declare_experts(lib, i64, vp, ci)
     _lib_handle = lib
     return lib
+
+
+def _declare_experts(lib, i64, vp, ci):
+    """Argument types of the mixture-of-experts operators (include/tile_gemm_experts.h)."""
+    size = ctypes.POINTER(i64)
+    for name, args in {
+        "tile_gemm_experts_version": [],
+        "tile_gemm_expert_sort_workspace_size": [i64, i64, i64, size],
+        "tile_gemm_expert_sort": [i64, i64, i64, vp, i64, vp, vp, vp, vp, i64, vp],
+        "tile_gemm_expert_gather": [i64, i64, i64, ci, vp, i64, vp, vp, i64, vp],
+        "tile_gemm_expert_combine": [i64, i64, i64, ci, vp, i64, vp, vp, i64, vp, i64, vp],
+        "tile_gemm_expert_combine_grad": [i64, i64, i64, ci, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp],
+        "tile_gemm_grouped": [i64, i64, i64, i64, ci, vp, i64, vp, i64, i64, ci, vp, i64, ci, vp, vp],
+        "tile_gemm_grouped_wgrad": [i64, i64, i64, i64, ci, vp, i64, vp, i64, vp, i64, i64, ci, vp, vp],
+        "tile_gemm_q4_packed_size": [i64, i64, i64, i64, ci, size],
+        "tile_gemm_pack_q4": [i64, i64, i64, i64, ci, vp, i64, i64, vp, i64, i64, vp, i64, vp],
+        "tile_gemm_q4": [i64, i64, i64, i64, i64, ci, vp, i64, vp, vp, i64, ci, vp, vp],
+    }.items():
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ci
 
 
 def _addr(x) -> Optional[int]:
@@ -290,6 +318,102 @@ def tile_gemm_pack_b(batch, K, N, dtype, B, ldb, strideB, packed, packed_bytes=N
         packed_bytes = packed.numel() * packed.element_size() if hasattr(packed, "numel") else 0
     _check(_lib().tile_gemm_pack_b(batch, K, N, _dtype(dtype), _addr(B), ldb, strideB, int(transposed),
                                    _addr(packed), int(packed_bytes), _stream(stream)), "tile_gemm_pack_b")
+
+
+# ---- the operators of a mixture-of-experts layer (include/tile_gemm_experts.h) ----------
+def _bytes_of(x) -> int:
+    return x.numel() * x.element_size() if hasattr(x, "numel") else 0
+
+
+def experts_version() -> int:
+    return int(_lib().tile_gemm_experts_version())
+
+
+def tile_gemm_expert_sort_workspace_size(tokens, top_k, experts) -> int:
+    """Bytes of workspace tile_gemm_expert_sort needs (0: none)."""
+    n = ctypes.c_int64(0)
+    _check(_lib().tile_gemm_expert_sort_workspace_size(tokens, top_k, experts, ctypes.byref(n)),
+           "tile_gemm_expert_sort_workspace_size")
+    return int(n.value)
+
+
+def tile_gemm_expert_sort(tokens, top_k, experts, ids, ld_ids, offsets, entry_of_row, row_of_entry, workspace=None,
+                          workspace_bytes=None, stream=None) -> None:
+    """Sort the entries t * top_k + j by their expert ids[t][j] (int32; an id outside the experts: no
+    expert, sorted last).  Writes offsets (experts + 1) and the two inverse orders (tokens * top_k;
+    entries and rows without an expert complemented), all int32."""
+    if workspace_bytes is None:
+        workspace_bytes = _bytes_of(workspace)
+    _check(_lib().tile_gemm_expert_sort(tokens, top_k, experts, _addr(ids), ld_ids, _addr(offsets),
+                                        _addr(entry_of_row), _addr(row_of_entry), _addr(workspace), workspace_bytes,
+                                        _stream(stream)), "tile_gemm_expert_sort")
+
+
+def tile_gemm_expert_gather(tokens, top_k, cols, dtype, x, ldx, row_of_entry, rows, ldr, stream=None) -> None:
+    """rows[row of entry (t, j)] = x[t]; zeros in the rows of entries without an expert."""
+    _check(_lib().tile_gemm_expert_gather(tokens, top_k, cols, _dtype(dtype), _addr(x), ldx, _addr(row_of_entry),
+                                          _addr(rows), ldr, _stream(stream)), "tile_gemm_expert_gather")
+
+
+def tile_gemm_expert_combine(tokens, top_k, cols, dtype, y, ldy, row_of_entry, weights, ld_w, out, ldo,
+                             stream=None) -> None:
+    """out[t] = sum over j of weights[t][j] * y[row of entry (t, j)] (weights fp32; None: 1, the gradient of
+    the gather)."""
+    _check(_lib().tile_gemm_expert_combine(tokens, top_k, cols, _dtype(dtype), _addr(y), ldy, _addr(row_of_entry),
+                                           _addr(weights), ld_w, _addr(out), ldo, _stream(stream)),
+           "tile_gemm_expert_combine")
+
+
+def tile_gemm_expert_combine_grad(tokens, top_k, cols, dtype, d_out, ldo, y, ldy, row_of_entry, weights, ld_w, d_y,
+                                  ldd, d_w, ld_dw, stream=None) -> None:
+    """The gradient of combine with respect to y (d_y, by row) and the weights (d_w, fp32)."""
+    _check(_lib().tile_gemm_expert_combine_grad(tokens, top_k, cols, _dtype(dtype), _addr(d_out), ldo, _addr(y), ldy,
+                                                _addr(row_of_entry), _addr(weights), ld_w, _addr(d_y), ldd,
+                                                _addr(d_w), ld_dw, _stream(stream)), "tile_gemm_expert_combine_grad")
+
+
+def tile_gemm_grouped(experts, rows, N, K, dtype, A, lda, B, ldb, strideB, C, ldc, offsets, c_dtype="f32",
+                      transposed=0, stream=None) -> None:
+    """C[r] = A[r] . B[g] for the rows offsets[g] .. offsets[g + 1] of every expert g; B[g] is K x N, or
+    N x K with transposed=1.  offsets None: one expert with every row."""
+    _check(_lib().tile_gemm_grouped(experts, rows, N, K, _dtype(dtype), _addr(A), lda, _addr(B), ldb, strideB,
+                                    int(transposed), _addr(C), ldc, _dtype(c_dtype), _addr(offsets),
+                                    _stream(stream)), "tile_gemm_grouped")
+
+
+def tile_gemm_grouped_wgrad(experts, rows, M, N, dtype, A, lda, D, ldd, C, ldc, strideC, offsets, c_dtype="f32",
+                            stream=None) -> None:
+    """C[g] = A[rows of g]^T . D[rows of g], M x N, for every expert g: the gradient of the grouped product
+    with respect to B."""
+    _check(_lib().tile_gemm_grouped_wgrad(experts, rows, M, N, _dtype(dtype), _addr(A), lda, _addr(D), ldd, _addr(C),
+                                          ldc, strideC, _dtype(c_dtype), _addr(offsets), _stream(stream)),
+           "tile_gemm_grouped_wgrad")
+
+
+def tile_gemm_q4_packed_size(experts, N, K, group, dtype) -> int:
+    n = ctypes.c_int64(0)
+    _check(_lib().tile_gemm_q4_packed_size(experts, N, K, group, _dtype(dtype), ctypes.byref(n)),
+           "tile_gemm_q4_packed_size")
+    return int(n.value)
+
+
+def tile_gemm_pack_q4(experts, N, K, group, dtype, codes, ld_codes, stride_codes, scales, ld_scales, stride_scales,
+                      packed, packed_bytes=None, stream=None) -> None:
+    """Lay 4-bit codes (two a byte along K, the lower four bits first; weight = (code - 8) * scale) and their
+    scales (of dtype, one per `group` k) out for tile_gemm_q4, once."""
+    if packed_bytes is None:
+        packed_bytes = _bytes_of(packed)
+    _check(_lib().tile_gemm_pack_q4(experts, N, K, group, _dtype(dtype), _addr(codes), ld_codes, stride_codes,
+                                    _addr(scales), ld_scales, stride_scales, _addr(packed), packed_bytes,
+                                    _stream(stream)), "tile_gemm_pack_q4")
+
+
+def tile_gemm_q4(experts, rows, N, K, group, dtype, A, lda, packed, C, ldc, offsets=None, c_dtype="f32",
+                 stream=None) -> None:
+    """C[r] = A[r] . W[g]^T for the rows of every expert g, W packed by tile_gemm_pack_q4.  offsets None: one
+    expert with every row."""
+    _check(_lib().tile_gemm_q4(experts, rows, N, K, group, _dtype(dtype), _addr(A), lda, _addr(packed), _addr(C),
+                               ldc, _dtype(c_dtype), _addr(offsets), _stream(stream)), "tile_gemm_q4")
 
 
 def make_layout(shape, shard, replica=(), offset=None, swizzle=None) -> Layout:

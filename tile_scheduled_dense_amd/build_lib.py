@@ -13,10 +13,12 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libtile_gemm.so")
-# the C ABI and planning, the layout introspection, and one translation unit per
-# input type for the GEMM kernels (compiled in parallel, then linked)
+# the C ABIs and planning, the layout introspection, and one translation unit per
+# input type for the GEMM kernels and for the expert products (compiled in
+# parallel, then linked)
 SOURCES = [os.path.join(CSRC, f) for f in ("tile_gemm.hip", "layout.hip", "launch_bf16.hip", "launch_f16.hip",
-                                           "launch_f32.hip")]
+                                           "launch_f32.hip", "experts.hip", "experts_bf16.hip", "experts_f16.hip",
+                                           "experts_f32.hip")]
 BUILD_DIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,74 @@
+// experts_kernels.hpp -- instantiations and launches of the expert products'
+// kernels (experts.hpp), included by one translation unit per input type.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "experts.hpp"
+#include "ranges.hpp"
+
+namespace tg {
+namespace {
+
+inline tg_status launched() { return hipGetLastError() == hipSuccess ? TG_OK : TG_ERR_LAUNCH; }
+
+// Waves that split K: enough for two stages each, eight at most.
+template <int DT, bool TRANS, int MT>
+tg_status launch_stream(const GroupedParams &p, hipStream_t s) {
+    using S = StreamShape<DT, TRANS>;
+    const int64_t stages = cdiv(p.K, S::K);
+    const int waves = stages >= 16 ? 8 : (stages >= 8 ? 4 : 2);
+    const dim3 grid((unsigned)cdiv(p.N, S::COLS), (unsigned)p.experts + 1);
+    hipLaunchKernelGGL((grouped_stream_kernel<DT, TRANS, MT>), grid, dim3(64 * waves), waves * S::FRAGS * 1024, s, p);
+    return launched();
+}
+
+template <int DT, int GROUP, int MT>
+tg_status launch_q4_as(const Q4Params &p, hipStream_t s) {
+    const int waves = p.k_blocks >= 32 && MT < 4 ? 16 : (p.k_blocks >= 16 ? 8 : (p.k_blocks >= 4 ? 4 : 1));
+    const dim3 grid((unsigned)p.n_tiles, (unsigned)p.experts + 1);
+    hipLaunchKernelGGL((q4_kernel<DT, GROUP, MT>), grid, dim3(64 * waves), waves * MT * 1024, s, p);
+    return launched();
+}
+
+// row tiles of 16 taken together: by the rows an expert has on average
+template <int DT, int GROUP>
+tg_status launch_q4_group(const Q4Params &p, hipStream_t s) {
+    const int64_t mean = cdiv(p.rows, p.experts);
+    if (mean <= 16) return launch_q4_as<DT, GROUP, 1>(p, s);
+    if (mean <= 32) return launch_q4_as<DT, GROUP, 2>(p, s);
+    return launch_q4_as<DT, GROUP, 4>(p, s);
+}
+
+template <int DT, bool TRANS>
+tg_status launch_grouped_as(const GroupedParams &p, hipStream_t s) {
+    const int64_t mean = cdiv(p.rows, p.experts);
+    if (mean <= 16) return launch_stream<DT, TRANS, 1>(p, s);
+    return launch_stream<DT, TRANS, 2>(p, s);
+}
+
+}  // namespace
+
+template <int DT>
+tg_status launch_grouped(const GroupedParams &p, bool transposed, hipStream_t s) {
+    return transposed ? launch_grouped_as<DT, true>(p, s) : launch_grouped_as<DT, false>(p, s);
+}
+
+template <int DT>
+tg_status launch_wgrad(const GroupedParams &p, hipStream_t s) {
+    const int64_t blocks = cdiv((int64_t)p.experts * p.M * p.N, 256);
+    hipLaunchKernelGGL((wgrad_small_kernel<DT>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, p);
+    return launched();
+}
+
+template <int DT>
+tg_status launch_q4(const Q4Params &p, int group, hipStream_t s) {
+    switch (group) {
+        case 32: return launch_q4_group<DT, 32>(p, s);
+        case 64: return launch_q4_group<DT, 64>(p, s);
+        case 128: return launch_q4_group<DT, 128>(p, s);
+    }
+    return TG_ERR_INTERNAL;
+}
+
+}  // namespace tg

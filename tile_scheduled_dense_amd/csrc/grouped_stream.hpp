@@ -1,0 +1,270 @@
+// grouped_stream.hpp -- expert products with few rows an expert: C[r] = A[r] .
+// B[g], bound by the bytes of the experts' weights.
+//
+// The weights go from HBM straight to registers, every byte once (per 16 * MT
+// rows), and no LDS lies between: at a few rows a weight is used by a single
+// matrix instruction.  A workgroup takes a strip of columns of one expert, its
+// waves split K stage by stage, and their sums are added in LDS in wave order.
+// The weights are the matrix instruction's first operand and the tokens its
+// second, so that a lane holds neighbouring columns of one row of C.
+//
+// A stage is eight 16-byte loads a lane (8 KiB a wave), twice in flight:
+//  * B as stored (n contiguous): lane l = 16 g + c loads, of 16-bit types, the
+//    rows k = 8 g .. 8 g + 7 at the columns 8 c .. 8 c + 7, an 8 x 8 square that
+//    it transposes in registers: fragment j is column 8 c + j.  128 columns by 32
+//    k.  fp32 needs no transpose: of 16 k, rows 4 g .. 4 g + 3 at columns 4 c ..
+//    4 c + 3; element j of row e feeds instruction e of fragment j.  64 by 32.
+//  * B transposed (k contiguous): a load is a fragment, row n = 16 j + c, a
+//    16-byte chunk of k at lane group g.  32 columns by 128 k (fp32: 64 k).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "expert_rows.hpp"
+
+namespace tg {
+
+struct GroupedParams {
+    const char *A, *B;
+    char *C;
+    const int32_t *offsets;
+    int64_t lda, ldb, ldc, sB, sC;      // sC: wgrad only
+    int experts, rows;
+    int M, N, K;                         // wgrad: C[g] is M x N (K unused); grouped: rows x N over K
+    int c_f32;
+};
+
+template <int DT, bool TRANS>
+struct StreamShape {
+    static constexpr int E = DT == DT_F32 ? 4 : 2, PER = 16 / E;
+    static constexpr int FRAGS = TRANS ? 2 : PER;                    // column fragments of 16
+    static constexpr int COLS = 16 * FRAGS;
+    static constexpr int K = TRANS ? 16 * E == 64 ? 64 : 128 : 32;   // k of a stage
+    static constexpr int A_LOADS = K / (4 * PER);                    // 16-byte loads of a row of A
+};
+
+template <int DT, bool TRANS>
+struct StreamB {
+    using S = StreamShape<DT, TRANS>;
+    u32x4 q[8];
+    // the stage at k0; FULL: all its columns and k exist
+    template <bool FULL>
+    __device__ __forceinline__ void load(const char *B, int64_t ldb, int n_left, int k_left, int lane) {
+        const rsrc_t r = make_rsrc(B);
+        const int g = lane / 16, c = lane % 16, ld = (int)ldb;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            int k, n, left;      // first element, elements there along the contiguous axis
+            if constexpr (TRANS) {
+                n = 16 * (i / 4) + c;
+                k = 4 * S::PER * (i % 4) + S::PER * g;
+                left = n < n_left ? k_left - k : 0;
+            } else {
+                n = S::PER * c;
+                k = DT == DT_F32 ? 16 * (i / 4) + 4 * g + i % 4 : 8 * g + i;
+                left = k < k_left ? n_left - n : 0;
+            }
+            const int at = (TRANS ? n * ld + k : k * ld + n) * S::E;
+            if constexpr (FULL) {
+                // one lane offset for every load, the rest scalar
+                const int i0 = (TRANS ? c * ld + S::PER * g : (DT == DT_F32 ? 4 : 8) * g * ld + S::PER * c) * S::E;
+                const int step = TRANS ? 16 * (i / 4) * ld + 4 * S::PER * (i % 4)
+                                       : (DT == DT_F32 ? 16 * (i / 4) + i % 4 : i) * ld;
+                q[i] = bload16(r, i0, step * S::E);
+            }
+            else {
+                // one chunk's single elements at a time, their addresses made here: neither
+                // the elements' registers nor the addresses of all are held together
+                int here = left > 0 ? at : kOutOfRange;
+                asm volatile("" : "+v"(here));
+                q[i] = bload16_n<S::E>(r, here, 0, left < 0 ? 0 : left);
+                asm volatile("" : "+v"(q[i]) : : "memory");
+            }
+        }
+    }
+};
+
+// rows of A: A_LOADS chunks of row tile i's row of this lane
+template <int DT, bool TRANS, int MT>
+struct StreamA {
+    using S = StreamShape<DT, TRANS>;
+    u32x4 a[MT][S::A_LOADS];
+    template <bool FULL>
+    __device__ __forceinline__ void load(const char *A, int64_t lda, int rows, int k_left, int lane) {
+        const rsrc_t r = make_rsrc(A);
+        const int g = lane / 16;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int row = 16 * i + lane % 16;
+#pragma unroll
+            for (int s = 0; s < S::A_LOADS; ++s) {
+                const int k = 4 * S::PER * s + S::PER * g;
+                const int at = row < rows ? (row * (int)lda + k) * S::E : kOutOfRange;
+                const int left = row < rows ? k_left - k : 0;
+                if constexpr (FULL) a[i][s] = bload16(r, at, 0);
+                else {
+                    int here = at;
+                    asm volatile("" : "+v"(here));
+                    a[i][s] = bload16_n<S::E>(r, here, 0, left < 0 ? 0 : left);
+                    asm volatile("" : "+v"(a[i][s]) : : "memory");
+                }
+            }
+        }
+    }
+};
+
+template <int DT, bool TRANS, int MT>
+__device__ __forceinline__ void stream_mma(const StreamB<DT, TRANS> &b, const StreamA<DT, TRANS, MT> &a,
+                                           f32x4 (&acc)[MT][StreamShape<DT, TRANS>::FRAGS]) {
+    using S = StreamShape<DT, TRANS>;
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+        for (int s = 0; s < S::A_LOADS; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < S::FRAGS; ++j) {
+                    const uint32_t w = TRANS ? b.q[4 * j + s][e] : b.q[4 * s + e][j];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        const uint32_t x = a.a[i][s][e];
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, w),
+                                                                        __builtin_bit_cast(float, x), acc[i][j], 0, 0, 0);
+                    }
+                }
+    } else if constexpr (TRANS) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) mfma_chunk<DT>(b.q[4 * j + s], a.a[i][s], acc[i][j]);
+    } else {
+        u32x4 f[8];
+        transpose_square<2>(b.q, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) mfma_chunk<DT>(f[j], a.a[i][0], acc[i][j]);
+    }
+}
+
+// grid: column strips x (experts + 1); the last takes the rows without an expert.
+template <int DT, bool TRANS, int MT>
+__global__ __launch_bounds__(512) void grouped_stream_kernel(GroupedParams p) {
+    using S = StreamShape<DT, TRANS>;
+    extern __shared__ f32x4 stream_lds[];           // [waves][FRAGS][64]
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    const int e = blockIdx.y, n0 = blockIdx.x * S::COLS;
+    const RowSpan span = rows_of(p.offsets, e, p.experts, p.rows);
+    const int n_left = p.N - n0;
+    const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
+    const int stages = e == p.experts ? 0 : (p.K + S::K - 1) / S::K;
+    const char *B = p.B + (e == p.experts ? 0 : (int64_t)e * p.sB) * S::E + (TRANS ? n0 * p.ldb : (int64_t)n0) * S::E;
+    const int64_t b_step = (TRANS ? (int64_t)S::K : S::K * p.ldb) * S::E;
+    for (int r0 = span.lo; r0 < span.hi; r0 += 16 * MT) {
+        const int rows = span.hi - r0 < 16 * MT ? span.hi - r0 : 16 * MT;
+        const char *A = p.A + (int64_t)r0 * p.lda * S::E;
+        f32x4 acc[MT][S::FRAGS];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < S::FRAGS; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        auto fetch = [&](int s, StreamB<DT, TRANS> &b, StreamA<DT, TRANS, MT> &a, auto full) {
+            constexpr bool FULL = decltype(full)::value;
+            const int k_left = p.K - s * S::K;
+            b.template load<FULL>(B + s * b_step, p.ldb, n_left, k_left, lane);
+            a.template load<FULL>(A + (int64_t)s * S::K * S::E, p.lda, rows, k_left, lane);
+        };
+        // whole stages, the next one's loads in flight during the current one's
+        // products; then those that N or K cuts, one at a time
+        const int whole = n_left < S::COLS || stages == 0 ? 0 : p.K / S::K;
+        int s = wave;
+        if (s < whole) {
+            const std::true_type full;
+            StreamB<DT, TRANS> b0, b1;
+            StreamA<DT, TRANS, MT> a0, a1;
+            fetch(s, b0, a0, full);
+            for (;;) {
+                s += waves;
+                const bool more = s < whole;
+                if (more) fetch(s, b1, a1, full);
+                __builtin_amdgcn_sched_barrier(0);
+                stream_mma<DT, TRANS, MT>(b0, a0, acc);
+                if (!more) break;
+                b0 = b1;
+                a0 = a1;
+            }
+        }
+        for (; s < stages; s += waves) {
+            StreamB<DT, TRANS> b;
+            StreamA<DT, TRANS, MT> a;
+            fetch(s, b, a, std::false_type{});
+            stream_mma<DT, TRANS, MT>(b, a, acc);
+        }
+        for (int i = 0; i < MT; ++i) {
+            if (16 * i >= rows) break;
+#pragma unroll
+            for (int j = 0; j < S::FRAGS; ++j) {
+                f32x4 v = acc[0][j];
+#pragma unroll
+                for (int m = 1; m < MT; ++m)
+                    if (m == i) v = acc[m][j];
+                stream_lds[(wave * S::FRAGS + j) * 64 + lane] = v;
+            }
+            __syncthreads();
+            // wave w sums and stores value w, w + waves, ... of the tile's four: the FRAGS
+            // columns of a value are neighbours (B as stored), the four values of a
+            // fragment are (B transposed)
+            const int r = r0 + 16 * i + lane % 16, g = lane / 16;
+            if constexpr (TRANS) {
+                for (int j = wave; j < S::FRAGS; j += waves) {
+                    f32x4 v = stream_lds[j * 64 + lane];
+                    for (int w = 1; w < waves; ++w) v += stream_lds[(w * S::FRAGS + j) * 64 + lane];
+                    const int n = 16 * j + 4 * g;
+                    if (r < span.hi && n < n_left)
+                        store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, v);
+                }
+            } else {
+                for (int q = wave; q < S::FRAGS; q += waves) {      // (value, four fragments)
+                    const int v = q / (S::FRAGS / 4), j0 = 4 * (q % (S::FRAGS / 4));
+                    f32x4 x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float *at = reinterpret_cast<const float *>(stream_lds + (j0 + j) * 64 + lane) + v;
+                        float y = at[0];
+                        for (int w = 1; w < waves; ++w) y += at[w * S::FRAGS * 256];
+                        x[j] = y;
+                    }
+                    const int n = S::PER * (4 * g + v) + j0;
+                    if (r < span.hi && n < n_left)
+                        store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, x);
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// C[g] = A[rows of g]^T . D[rows of g], one output a thread: for extents below
+// one 16-byte chunk, where there is no tile to fill.
+template <int DT>
+__global__ __launch_bounds__(256) void wgrad_small_kernel(GroupedParams p) {
+    typedef typename ElemOf<DT>::type T;
+    const int64_t per = (int64_t)p.M * p.N, total = per * p.experts;
+    const T *A = reinterpret_cast<const T *>(p.A), *D = reinterpret_cast<const T *>(p.B);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int g = (int)(i / per), m = (int)(i % per / p.N), n = (int)(i % p.N);
+        const RowSpan span = rows_of(p.offsets, g, p.experts, p.rows);
+        float sum = 0.0f;
+        for (int r = span.lo; r < span.hi; ++r)
+            sum = __builtin_fmaf((float)A[(int64_t)r * p.lda + m], (float)D[(int64_t)r * p.ldb + n], sum);
+        const int64_t at = (int64_t)g * p.sC + (int64_t)m * p.ldc + n;
+        if (DT == DT_F32 || p.c_f32) reinterpret_cast<float *>(p.C)[at] = sum;
+        else reinterpret_cast<T *>(p.C)[at] = (T)sum;
+    }
+}
+
+}  // namespace tg

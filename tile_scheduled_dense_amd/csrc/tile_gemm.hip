@@ -11,6 +11,7 @@
 
 #include "launch.hpp"
 #include "pack.hpp"
+#include "ranges.hpp"
 #include "splitk.hpp"
 #include "tile_gemm.h"
 
@@ -106,8 +107,6 @@ CfgDims cfg_dims(int config, tg_dtype dtype) {
         default: return {0, 0, 0, 0, 0, 0, 0};
     }
 }
-
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The 256 x 256 partition of one M x N problem: main tile rows and columns,
 // and the thin-remainder strips beside them (an N tail of at most 64 columns
@@ -276,7 +275,6 @@ struct Plan {
     int64_t b_offset = 0;              // workspace bytes before the B copy (the A copy)
 };
 
-inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // lda, ldb: the call's (or, for the plan queries, the assumed) leading
 // dimensions of A and B; a_aligned: A itself starts on a 16-byte boundary;
@@ -610,20 +608,6 @@ tg_status make_plan(int64_t batch, int64_t M, int64_t N, int64_t K, tg_dtype dty
     }
     return TG_OK;
 }
-
-// Byte extent [lo, hi) touched by a strided-batched row-major operand.
-struct Range {
-    uintptr_t lo, hi;
-};
-
-Range span(const void *p, int64_t batch, int64_t rows, int64_t cols, int64_t ld, int64_t stride, int esz) {
-    if (batch == 0 || rows == 0 || cols == 0) return {0, 0};
-    const uintptr_t base = reinterpret_cast<uintptr_t>(p);
-    const int64_t last = (batch - 1) * stride + (rows - 1) * ld + cols;   // one past the last element
-    return {base, base + static_cast<uintptr_t>(last) * esz};
-}
-
-bool overlaps(Range a, Range b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
 
 tg_status validate(int64_t batch, int64_t M, int64_t N, int64_t K, tg_dtype dtype,
                    const void *A, int64_t lda, int64_t sA, const void *B, int64_t ldb, int64_t sB,
@@ -979,6 +963,8 @@ int64_t plan_ld(const tg_options *opt, bool a) {
 }
 
 }  // namespace
+
+tg_status tg::device_ok() { return current_device_ok(); }
 
 extern "C" {
 
