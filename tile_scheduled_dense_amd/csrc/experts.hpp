@@ -6,7 +6,7 @@
 
 #include <hip/hip_runtime.h>
 
-#include "grouped_stream.hpp"
+#include "grouped_ring.hpp"
 #include "q4.hpp"
 #include "tile_gemm.h"
 

@@ -40,9 +40,40 @@ tg_status launch_q4_group(const Q4Params &p, hipStream_t s) {
     return launch_q4_as<DT, GROUP, 4>(p, s);
 }
 
+template <int DT> using Tile256 = RingCfg<DT, 256, 256, 2, 2, 16>;
+template <int DT> using Tile128 = RingCfg<DT, 128, 128, 2, 2, 16>;
+
+// the most tile rows that `groups` groups of `rows` rows together can have
+inline int64_t most_tiles(int64_t rows, int64_t groups, int64_t bm) {
+    const int64_t parts = rows < groups ? rows : groups;
+    return (rows + parts * (bm - 1)) / bm;
+}
+
+template <class C, bool B_KS, bool PIPE>
+tg_status launch_tiles(const GroupedParams &p, hipStream_t s) {
+    const int64_t grid = most_tiles(p.rows, p.experts + 1, C::BM) * cdiv(p.N, C::BN);
+    if (grid > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((grouped_tile_kernel<C, B_KS, PIPE>), dim3((unsigned)grid), dim3(C::THREADS), 0, s, p);
+    return launched();
+}
+
+template <class C, bool PIPE>
+tg_status launch_wgrad_tiles(const GroupedParams &p, hipStream_t s) {
+    const int64_t tiles = cdiv(p.M, C::BM) * cdiv(p.N, C::BN), grid = p.experts * cdiv(tiles, 8) * 8;
+    if (grid > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((wgrad_tile_kernel<C, PIPE>), dim3((unsigned)grid), dim3(C::THREADS), 0, s, p);
+    return launched();
+}
+
 template <int DT, bool TRANS>
 tg_status launch_grouped_as(const GroupedParams &p, hipStream_t s) {
     const int64_t mean = cdiv(p.rows, p.experts);
+    // an N below a chunk is not for the tiles (grouped_ring.hpp)
+    if (mean > 32 && p.N >= 8) {
+        const int64_t tiles = cdiv(p.rows, 256) * cdiv(p.N, 256);
+        if (tiles >= 200) return launch_tiles<Tile256<DT>, !TRANS, true>(p, s);
+        return launch_tiles<Tile128<DT>, !TRANS, false>(p, s);
+    }
     if (mean <= 16) return launch_stream<DT, TRANS, 1>(p, s);
     return launch_stream<DT, TRANS, 2>(p, s);
 }
@@ -56,6 +87,11 @@ tg_status launch_grouped(const GroupedParams &p, bool transposed, hipStream_t s)
 
 template <int DT>
 tg_status launch_wgrad(const GroupedParams &p, hipStream_t s) {
+    if (p.M >= 8 && p.N >= 8) {
+        const int64_t tiles = p.experts * cdiv(p.M, 256) * cdiv(p.N, 256);
+        if (tiles >= 200) return launch_wgrad_tiles<Tile256<DT>, true>(p, s);
+        return launch_wgrad_tiles<Tile128<DT>, false>(p, s);
+    }
     const int64_t blocks = cdiv((int64_t)p.experts * p.M * p.N, 256);
     hipLaunchKernelGGL((wgrad_small_kernel<DT>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, p);
     return launched();

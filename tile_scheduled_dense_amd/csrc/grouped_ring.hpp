@@ -1,0 +1,430 @@
+// grouped_ring.hpp -- expert products with many rows an expert, and their
+// gradients, on block tiles and the LDS ring of gemm_ring.hpp: one workgroup a
+// tile of one expert, K tiles copied straight from memory to LDS a few ahead,
+// one barrier per K tile, 16x16x32 (fp32: 16x16x4) matrix instructions.
+//
+// Three forms, by which axis each operand holds contiguous:
+//   C[r] = A[r] . B[g]             A along k,  B along n   (NN)
+//   C[r] = A[r] . B[g]^T           both along k            (NT)
+//   C[g] = A[rows]^T . D[rows]     A along m, D along n; k is the expert's rows  (TN)
+// An operand contiguous along k is staged as rows of 64 bytes and read by
+// ds_read_b128; one contiguous along its own extent as 32 k rows and read by
+// the transposing ds_read_b64_tr_b16 (fp32: ds_read_b32 per step): the two
+// staged tiles of tile_config.hpp, either of them for either operand.
+//
+// The extents' fringe: a row or column chunk past the end is fetched from past
+// the resource, which reads 0.  A chunk that the end cuts brings what lies
+// behind, in the same matrix (the host keeps extents below one chunk away), and
+// only feeds outputs that are not stored.  The last K tile goes through registers
+// with element-exact zeros in both operands, so that a NaN behind K meets none.
+//
+// B's fragments are the matrix instruction's first operand and A's the second:
+// a lane then holds four neighbouring columns of one row of C, so that C is
+// stored 8 or 16 bytes at a time.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_ring.hpp"
+#include "grouped_stream.hpp"
+
+namespace tg {
+
+template <class C> struct SwapCfg;
+template <int DT, int BM, int BN, int WM, int WN, int MT>
+struct SwapCfg<RingCfg<DT, BM, BN, WM, WN, MT>> {
+    using type = RingCfg<DT, BN, BM, WN, WM, MT>;
+};
+
+// One operand of a tile.  V: a configuration whose A tile (contiguous along k)
+// or B tile (KS: along the extent) is this operand's.  T: its MFMA tiles per wave.
+template <class V, bool KS, int T>
+struct RingOperand {
+    using CP = RingCopy<V, SWZ_XOR, KS ? 1 : 0>;
+    static constexpr int E = V::ELEM, CHUNK = V::CHUNK, BK = V::BK, PER = CP::PER, REGION = CP::REGION;
+    static constexpr int SHIFT = (CP::GMAX - 1) * 1024;      // a group's resource base sits this far below
+    static constexpr int BASES = KS ? T : 1;                 // registers of fragment read addresses
+    static constexpr int PIECES = KS ? (V::DT == DT_F32 ? 4 : 2) : 1;
+    // a fragment's largest distance from its base: the last row tile, the last piece
+    static constexpr int REACH = KS ? 4 * V::B_ROW_BYTES : (T - 1) * 16 * V::A_ROW_BYTES;
+    static_assert(V::MT == 16 && V::KSTEPS == 1, "one fragment read step per K tile");
+
+    const char *base;
+    int ld, left;               // left: rows or columns from the tile's first to the extent's end
+    int lane, wave;
+    uint32_t lds;
+    int x[PER], k[PER], voff[PER];
+    uint32_t rd[BASES];
+    i32x4 rs;
+    uint64_t step;              // bytes per K tile
+
+    // base: the tile's first element; w: the wave's first row or column in the tile
+    __device__ __forceinline__ void init(const char *base_, int64_t ld_, int left_, int w, uint32_t lds_, int lane_,
+                                         int wave_) {
+        base = reinterpret_cast<const char *>(uniform_u64(reinterpret_cast<uint64_t>(base_)));
+        ld = (int)ld_;
+        left = left_;
+        lane = lane_;
+        wave = wave_;
+        lds = lds_;
+        step = (uint64_t)(KS ? BK * ld_ * E : BK * E);
+        rs = rsrc_words_u(reinterpret_cast<uint64_t>(base) - SHIFT, 0x7fffffff);
+#pragma unroll
+        for (int d = 0; d < PER; ++d) {
+            if constexpr (KS) ring_b_source<V>(CP::block(d, wave), lane, SWZ_XOR, k[d], x[d]);
+            else ring_a_source<V>(CP::block(d, wave), lane, SWZ_XOR, x[d], k[d]);
+            const int off = x[d] < left ? (KS ? k[d] * ld + x[d] : x[d] * ld + k[d]) * E : kOutOfRange;
+            voff[d] = off + SHIFT - 1024 * CP::pos(d);
+        }
+        const int grp = lane / 16, in = lane % 16;
+#pragma unroll
+        for (int j = 0; j < BASES; ++j) {
+            if constexpr (!KS) rd[j] = lds + ring_a_byte<V>(w + in, grp, SWZ_XOR);
+            else if constexpr (V::DT == DT_F32) rd[j] = lds + ring_b_byte<V>(4 * grp, w + 16 * j + in, SWZ_XOR);
+            else rd[j] = lds + ring_b_byte<V>(8 * grp + in / 4, w + 16 * j + 4 * (in % 4), SWZ_XOR);
+            // keeps the base whole: a split-off constant would not fit the DS offset
+            asm("" : "+v"(rd[j]));
+        }
+    }
+
+    // this wave's copies of the next K tile into LDS copy `stage`
+    __device__ __forceinline__ void copy(int stage) {
+        constexpr int G0 = CP::Q < 4 ? CP::Q : 4;
+        static_assert(CP::Q <= 4 && !CP::SHARED, "one group of copies per wave");
+        copy_group_to_lds<G0>(rs, lds + stage * REGION + CP::block(0, wave) * 1024, &voff[0]);
+        const uint64_t a = (((uint64_t)(uint32_t)rs.y << 32) | (uint32_t)rs.x) + step;
+        rs.x = (int)(uint32_t)a;
+        rs.y = (int)(uint32_t)(a >> 32);
+    }
+
+    // the K tile at k0, of which k < K exist, through registers, zeros past the ends
+    __device__ __forceinline__ void tail_load(int64_t k0, int K, u32x4 *tail) const {
+        const rsrc_t r = make_rsrc(base + (KS ? k0 * ld : k0) * E);
+#pragma unroll
+        for (int d = 0; d < PER; ++d) {
+            const int k_left = K - (int)k0 - k[d], x_left = left - x[d];
+            const int run = KS ? x_left : k_left, other = KS ? k_left : x_left;
+            const int n = other <= 0 || run <= 0 ? 0 : (run < CHUNK ? run : CHUNK);
+            tail[d] = bload16_n<E>(r, n > 0 ? (KS ? k[d] * ld + x[d] : x[d] * ld + k[d]) * E : 0, 0, n);
+        }
+    }
+    __device__ __forceinline__ void tail_store(int stage, const u32x4 *tail) const {
+#pragma unroll
+        for (int d = 0; d < PER; ++d) {
+            const uint32_t at = lds + stage * REGION + CP::block(d, wave) * 1024 + 16 * lane;
+            *(__attribute__((address_space(3))) u32x4 *)(uintptr_t)at = tail[d];
+        }
+    }
+
+    // piece q of fragment i from LDS copy `stage`
+    __device__ __forceinline__ void read(int stage, int i, int q, u32x4 &f) const {
+        if constexpr (!KS) {
+            const uint32_t at = rd[0] + stage * REGION + i * 16 * V::A_ROW_BYTES;
+            f = *(const __attribute__((address_space(3))) u32x4 *)(uintptr_t)at;
+        } else if constexpr (V::DT == DT_F32) {
+            const uint32_t at = rd[i] + stage * REGION + q * V::B_ROW_BYTES;
+            f[q] = *(const __attribute__((address_space(3))) uint32_t *)(uintptr_t)at;
+        } else {
+            const uint32_t at = rd[i] + stage * REGION + q * 4 * V::B_ROW_BYTES;
+            const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                          (__attribute__((address_space(3))) v4i16 *)(uintptr_t)at));
+            if (q == 0) {
+                f.x = v.x;
+                f.y = v.y;
+            } else {
+                f.z = v.x;
+                f.w = v.y;
+            }
+        }
+    }
+};
+
+template <class C, bool A_KS, bool B_KS, int STAGES>
+struct GroupedTile {
+    using CT = typename SwapCfg<C>::type;
+    using OA = RingOperand<typename std::conditional<A_KS, CT, C>::type, A_KS, C::TM>;
+    using OB = RingOperand<typename std::conditional<B_KS, C, CT>::type, B_KS, C::TN>;
+    static constexpr int COPIES = OA::PER + OB::PER;
+    static constexpr int LDS = STAGES * (OA::REGION + OB::REGION);
+    static constexpr int READS = C::TM * OA::PIECES + C::TN * OB::PIECES;
+    static constexpr int NMFMA = C::MFMA_PER_READ * C::TM * C::TN;
+    static_assert(READS <= NMFMA, "one fragment read per MFMA at most");
+    // a read's distance from its base, the LDS copy included, is the 16-bit immediate of a DS instruction
+    static_assert((STAGES - 1) * OA::REGION + OA::REACH < 65536 && (STAGES - 1) * OB::REGION + OB::REACH < 65536,
+                  "DS offsets");
+
+    OA a;
+    OB b;
+    AccTiles<C> acc;
+    int K, nk, ndma;            // ndma: K tiles copied straight to LDS (all but the last)
+    int wave, lane;
+    u32x4 tail[COPIES];
+
+    __device__ __forceinline__ void init(const char *A, int64_t lda, int m_left, const char *B, int64_t ldb, int n_left,
+                                         int K_, char *smem) {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        K = K_;
+        nk = (K + C::BK - 1) / C::BK;
+        ndma = nk > 0 ? nk - 1 : 0;
+        const uint32_t lds0 = lds_address(smem);
+        b.init(B, ldb, n_left, (wave % C::WAVES_N) * C::WTN, lds0, lane, wave);
+        a.init(A, lda, m_left, (wave / C::WAVES_N) * C::WTM, lds0 + STAGES * OB::REGION, lane, wave);
+        acc.zero();
+    }
+    __device__ __forceinline__ void copy(int stage) {
+        a.copy(stage);
+        b.copy(stage);
+    }
+    __device__ __forceinline__ void tail_load() {
+        const int64_t k0 = (int64_t)(nk - 1) * C::BK;
+        a.tail_load(k0, K, &tail[0]);
+        b.tail_load(k0, K, &tail[OA::PER]);
+    }
+    // Wait until this wave's share of tile t is in LDS copy `stage`, at most AHEAD
+    // later tiles being in flight; the last tile is stored from its registers.
+    template <int AHEAD>
+    __device__ __forceinline__ void land(int t, int stage) {
+        if (t < ndma) {
+            const int later = ndma - 1 - t;
+            if (AHEAD >= 3 && later >= 3) wait_vmcnt<3 * COPIES>();
+            else if (AHEAD >= 2 && later >= 2) wait_vmcnt<2 * COPIES>();
+            else if (AHEAD >= 1 && later >= 1) wait_vmcnt<COPIES>();
+            else wait_vmcnt<0>();
+        } else {
+            wait_vmcnt<0>();
+            a.tail_store(stage, &tail[0]);
+            b.tail_store(stage, &tail[OA::PER]);
+        }
+        wait_lds();
+    }
+    __device__ __forceinline__ void read_piece(int stage, int r, u32x4 (&fa)[C::TM], u32x4 (&fb)[C::TN]) const {
+        constexpr int NA = C::TM * OA::PIECES;
+        if (r < NA) a.read(stage, r / OA::PIECES, r % OA::PIECES, fa[r / OA::PIECES]);
+        else b.read(stage, (r - NA) / OB::PIECES, (r - NA) % OB::PIECES, fb[(r - NA) / OB::PIECES]);
+    }
+    // MFMA q of a K tile (step e outermost: an accumulator's are TM x TN apart)
+    template <bool FIRST, int q>
+    __device__ __forceinline__ void mma(const u32x4 (&fa)[C::TM], const u32x4 (&fb)[C::TN]) {
+        constexpr int e = q / (C::TM * C::TN), i = (q / C::TN) % C::TM, j = q % C::TN;
+        acc.template mma<FIRST && e == 0>(i, j, fb[j], fa[i], e);
+    }
+
+    // All waves in step: wait for tile kt, one barrier, copy tile kt + STAGES - 1
+    // into the copy just released, multiply tile kt.
+    __device__ __forceinline__ void run_ring() {
+        if (nk == 0) return;
+        tail_load();
+#pragma unroll
+        for (int t = 0; t < STAGES - 1; ++t)
+            if (t < ndma) copy(t);
+        int cur = 0, nxt = STAGES - 1;
+        auto step = [&](int kt, auto first) {
+            land<STAGES - 2>(kt, cur);
+            block_barrier();
+            if (kt + STAGES - 1 < ndma) copy(nxt);
+            u32x4 fa[C::TM], fb[C::TN];
+#pragma unroll
+            for (int r = 0; r < READS; ++r) read_piece(cur, r, fa, fb);
+            static_for<0, NMFMA, 1>([&](auto q) { mma<decltype(first)::value, decltype(q)::value>(fa, fb); });
+            cur = cur + 1 == STAGES ? 0 : cur + 1;
+            nxt = nxt + 1 == STAGES ? 0 : nxt + 1;
+        };
+        step(0, std::true_type{});
+        for (int kt = 1; kt < nk; ++kt) step(kt, std::false_type{});
+        acc.settle();
+    }
+
+    // The software pipeline of gemm_ring.hpp (one wave per SIMD, a K tile's
+    // fragments in registers, twice): multiply tile t from (fa, fb) while tile
+    // t + 1 is read into (na, nb) and tile t + STAGES copied into tile t's copy.
+    template <bool STEADY, bool FIRST = false>
+    __device__ __forceinline__ void iter(int t, int cur, int next, u32x4 (&fa)[C::TM], u32x4 (&fb)[C::TN],
+                                         u32x4 (&na)[C::TM], u32x4 (&nb)[C::TN]) {
+        const bool more = STEADY || t + 1 < nk;
+        if (STEADY) wait_vmcnt<(STAGES - 2) * COPIES>();
+        else if (more) land<STAGES - 2>(t + 1, next);
+        wait_lds();
+        __builtin_amdgcn_sched_barrier(0);
+        block_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (STEADY) {
+            static_for<0, NMFMA, 1>([&](auto qc) {
+                constexpr int q = decltype(qc)::value;
+                mma<FIRST, q>(fa, fb);
+                if constexpr (q < READS) read_piece(next, q, na, nb);
+                if constexpr (q == NMFMA / 4 - 1) a.copy(cur);
+                if constexpr (q == 3 * NMFMA / 4 - 1) b.copy(cur);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        } else {
+            if (more) {
+#pragma unroll
+                for (int r = 0; r < READS; ++r) read_piece(next, r, na, nb);
+            }
+            if (t + STAGES < ndma) copy(cur);
+            static_for<0, NMFMA, 1>([&](auto q) { mma<FIRST, decltype(q)::value>(fa, fb); });
+        }
+    }
+    __device__ __forceinline__ void run_pipe() {
+        static_assert(STAGES == 4, "four tiles per trip cycle the LDS copies");
+        if (nk == 0) return;
+        // with at most STAGES copied tiles the last one is landed by the prologue or
+        // the first iteration: load it before any copy
+        const bool early = ndma <= STAGES;
+        if (early) tail_load();
+#pragma unroll
+        for (int t = 0; t < STAGES; ++t)
+            if (t < ndma) copy(t);
+        land<STAGES - 1>(0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        block_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 a0[C::TM], b0[C::TN], a1[C::TM], b1[C::TN];
+#pragma unroll
+        for (int r = 0; r < READS; ++r) read_piece(0, r, a0, b0);
+        if (STAGES < ndma) iter<true, true>(0, 0, 1, a0, b0, a1, b1);
+        else iter<false, true>(0, 0, 1, a0, b0, a1, b1);
+        int t = 1;
+        for (; t + 3 + STAGES < ndma; t += 4) {
+            iter<true>(t, 1, 2, a1, b1, a0, b0);
+            iter<true>(t + 1, 2, 3, a0, b0, a1, b1);
+            iter<true>(t + 2, 3, 0, a1, b1, a0, b0);
+            iter<true>(t + 3, 0, 1, a0, b0, a1, b1);
+        }
+        int cur = t % STAGES;
+        // the last tile's loads are younger than some copies, which only makes a wait longer
+        if (!early) tail_load();
+        for (; t + 1 < nk; t += 2) {
+            const int c1 = (cur + 1) % STAGES, c2 = (cur + 2) % STAGES;
+            iter<false>(t, cur, c1, a1, b1, a0, b0);
+            iter<false>(t + 1, c1, c2, a0, b0, a1, b1);
+            cur = c2;
+        }
+        if (t < nk) iter<false>(t, cur, (cur + 1) % STAGES, a1, b1, a0, b0);
+        acc.settle();
+    }
+
+    // C's tile: rows m < m_left, columns n < n_left, from its first element
+    __device__ __forceinline__ void store(char *Cp, int64_t at, int64_t ldc, int m_left, int n_left, bool c_f32,
+                                          bool wide) const {
+        const int m = (wave / C::WAVES_N) * C::WTM + lane % 16, n = (wave % C::WAVES_N) * C::WTN + 4 * (lane / 16);
+        static_for<0, C::TM, 1>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            if (m + 16 * i < m_left) {
+                const int64_t row = at + (int64_t)(m + 16 * i) * ldc;
+                static_for<0, C::TN, 1>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    const f32x4 v = {acc.get(i, j, 0), acc.get(i, j, 1), acc.get(i, j, 2), acc.get(i, j, 3)};
+                    if (n + 16 * j < n_left)
+                        store4<C::DT>(Cp, row + n + 16 * j, n_left - n - 16 * j, c_f32, wide, v);
+                });
+            }
+        });
+    }
+};
+
+// ---- which tile a workgroup takes ------------------------------------------------------
+// Products over rows: every group (expert, or the rows without one) has
+// ceil(rows / BM) tile rows; only the device knows how many.  The grid holds the
+// most there can be; each wave sums the groups' tile rows, 64 a step, and the
+// workgroups past the total end at once.  Ids are dealt to the XCDs in
+// contiguous runs, walked in groups of group_m tile rows, as the dense kernel's.
+struct RowTile {
+    int g, lo, rows, m0, tn;      // rows: from m0 to the group's end
+};
+
+__device__ __forceinline__ int wave_inclusive(int v, int lane) {
+    for (int d = 1; d < 64; d *= 2) {
+        const int up = __shfl_up(v, d);
+        if (lane >= d) v += up;
+    }
+    return v;
+}
+
+__device__ __forceinline__ bool row_tile(const GroupedParams &p, int BM, int tiles_n, RowTile &t) {
+    const int lane = threadIdx.x & 63;
+    const int groups = p.experts + 1;
+    RowSpan s = {0, 0};
+    int mine = 0, incl = 0;
+    auto look = [&](int base) {
+        s = base + lane < groups ? rows_of(p.offsets, base + lane, p.experts, p.rows) : RowSpan{0, 0};
+        mine = (s.hi - s.lo + BM - 1) / BM;
+        incl = wave_inclusive(mine, lane);
+        return __builtin_amdgcn_readlane(incl, 63);
+    };
+    int total_m = 0;
+    for (int base = 0; base < groups; base += 64) total_m += look(base);
+    const uint32_t total = (uint32_t)total_m * (uint32_t)tiles_n;
+    if (blockIdx.x >= total) return false;
+    const uint32_t per = total / 8, rem = total % 8, x = blockIdx.x % 8;
+    const uint32_t id = x * per + (x < rem ? x : rem) + blockIdx.x / 8;
+    const uint32_t gm = 8, group = id / (gm * tiles_n), first = group * gm;
+    const uint32_t rows = (uint32_t)total_m - first < gm ? (uint32_t)total_m - first : gm;
+    const uint32_t in = id - group * gm * tiles_n;
+    const int tm = (int)(first + in % rows);
+    t.tn = (int)(in / rows);
+    int before = 0;
+    for (int base = 0; base < groups; base += 64) {
+        const int here = groups <= 64 ? total_m : look(base);
+        if (tm < before + here) {
+            const int l = __builtin_ctzll(__ballot(before + incl > tm));
+            t.g = base + l;
+            t.lo = __builtin_amdgcn_readlane(s.lo, l);
+            t.m0 = (tm - before - __builtin_amdgcn_readlane(incl - mine, l)) * BM;
+            t.rows = __builtin_amdgcn_readlane(s.hi, l) - t.lo - t.m0;
+            return true;
+        }
+        before += here;
+    }
+    return false;
+}
+
+template <class C, bool B_KS, bool PIPE>
+__global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void grouped_tile_kernel(GroupedParams p) {
+    using Tile = GroupedTile<C, false, B_KS, 4>;
+    __shared__ __attribute__((aligned(1024))) char smem[Tile::LDS];
+    RowTile t;
+    if (!row_tile(p, C::BM, (p.N + C::BN - 1) / C::BN, t)) return;
+    const bool dead = t.g == p.experts;
+    const int n0 = t.tn * C::BN;
+    const char *A = p.A + (int64_t)(t.lo + t.m0) * p.lda * C::ELEM;
+    const char *B = p.B + ((dead ? 0 : (int64_t)t.g * p.sB) + (B_KS ? (int64_t)n0 : n0 * p.ldb)) * C::ELEM;
+    Tile tile;
+    tile.init(A, p.lda, t.rows, B, p.ldb, p.N - n0, dead ? 0 : p.K, smem);
+    if constexpr (PIPE) tile.run_pipe();
+    else tile.run_ring();
+    const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
+    tile.store(p.C, (int64_t)(t.lo + t.m0) * p.ldc + n0, p.ldc, t.rows, p.N - n0, p.c_f32, wide);
+}
+
+// The gradient with respect to B: experts x tiles_m x tiles_n tiles, whose work
+// goes with their expert's rows.  Every expert's tiles are dealt to all eight XCDs,
+// a contiguous run each, expert after expert: an XCD of its own for a popular
+// expert would work on alone.
+template <class C, bool PIPE>
+__global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void wgrad_tile_kernel(GroupedParams p) {
+    using Tile = GroupedTile<C, true, true, 4>;
+    __shared__ __attribute__((aligned(1024))) char smem[Tile::LDS];
+    const uint32_t tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN, tiles = tiles_m * tiles_n;
+    const uint32_t run = (tiles + 7) / 8;
+    const int g = (int)(blockIdx.x / (8 * run));
+    const uint32_t in = blockIdx.x % (8 * run), id = in % 8 * run + in / 8;
+    if (id >= tiles) return;
+    const uint32_t gm = 8, group = id / (gm * tiles_n), first = group * gm;
+    const uint32_t rows = tiles_m - first < gm ? tiles_m - first : gm;
+    const uint32_t at = id - group * gm * tiles_n;
+    const int m0 = (int)(first + at % rows) * C::BM, n0 = (int)(at / rows) * C::BN;
+    const RowSpan s = rows_of(p.offsets, g, p.experts, p.rows);
+    const int lo = __builtin_amdgcn_readfirstlane(s.lo), K = __builtin_amdgcn_readfirstlane(s.hi) - lo;
+    Tile tile;
+    tile.init(p.A + ((int64_t)lo * p.lda + m0) * C::ELEM, p.lda, p.M - m0, p.B + ((int64_t)lo * p.ldb + n0) * C::ELEM,
+              p.ldb, p.N - n0, K, smem);
+    if constexpr (PIPE) tile.run_pipe();
+    else tile.run_ring();
+    const bool wide = p.ldc % 4 == 0 && p.sC % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
+    tile.store(p.C, (int64_t)g * p.sC + (int64_t)m0 * p.ldc + n0, p.ldc, p.M - m0, p.N - n0, p.c_f32, wide);
+}
+
+}  // namespace tg
