@@ -200,6 +200,10 @@ def _addr(x) -> Optional[int]:
 def _stream(s) -> int:
     if s is None:
         import torch
+        if torch.cuda.is_initialized():
+            # the same handle as torch.cuda.current_stream().cuda_stream, without making a
+            # Stream object: 0.3 us a call against 3.5
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return int(torch.cuda.current_stream().cuda_stream) if torch.cuda.is_available() else 0
     if isinstance(s, int):
         return s
