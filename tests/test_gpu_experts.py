@@ -282,6 +282,41 @@ def test_wgrad(dt, experts, rows, spare, active, N, K, pad, skew, out):
             ref.check(got, want, rows, absum, o)
 
 
+@pytest.mark.parametrize("form", ["nn", "nt", "tn"])
+@pytest.mark.parametrize("dt,experts,rows,spare,N,K,pad", [
+    # enough tiles for the largest ones, their pieces and a part-filled last round
+    ("bf16", 5, 6500, 70, 2600, 200, 0), ("f16", 3, 7001, 0, 2307, 129, 1), ("f32", 6, 6400, 1, 2568, 72, 0),
+    ("bf16", 80, 9000, 0, 2048, 64, 0),
+], ids=lambda v: str(v))
+def test_products_of_many_tiles(dt, experts, rows, spare, N, K, pad, form):
+    offsets = offsets_of(sizes_of(experts, rows, experts - 1, seed=rows))
+    off = torch.tensor(offsets, dtype=torch.int32).cuda()
+    total = rows + spare
+    if form == "tn":
+        M, N, total = 2 * K + 1600, N, total // 4
+        offsets = [o // 4 for o in offsets]
+        off = torch.tensor(offsets, dtype=torch.int32).cuda()
+        experts = min(experts, 6)
+        offsets, off = offsets[:experts + 1], off[:experts + 1]
+        A, D = ints(total, M, dtype=dt, low=-1, high=2, seed=1), ints(total, N, dtype=dt, low=-1, high=2, seed=2)
+        A[offsets[-1]:] = float("nan")
+        want, _ = ref.wgrad(A, D, offsets)
+        (Ad, lda), (Dd, ldd) = strided(A, pad), strided(D, pad)
+        C = Out(M, N, torch.float32, pad, batch=experts)
+        tg.tile_gemm_grouped_wgrad(experts, total, M, N, dt, Ad, lda, Dd, ldd, C.t, C.ld, C.stride, off)
+    else:
+        A, B = ints(total, K, dtype=dt, low=-1, high=2, seed=1), ints(experts, K, N, dtype=dt, low=-1, high=2, seed=2)
+        A[offsets[-1]:] = float("nan")
+        want, _ = ref.grouped(A, B, offsets, total)
+        if form == "nt":
+            B = B.transpose(1, 2).contiguous()
+        (Ad, lda), (Bd, ldb) = strided(A, pad), strided(B, pad)
+        C = Out(total, N, torch.float32, pad)
+        tg.tile_gemm_grouped(experts, total, N, K, dt, Ad, lda, Bd, ldb, B.shape[1] * ldb, C.t, C.ld, off,
+                             transposed=int(form == "nt"))
+    assert torch.equal(C.get().double(), want)
+
+
 def test_grouped_nan_stays_in_its_row_and_column():
     """A NaN or an infinity in one row of A reaches that row alone; in one column of B, that column of its expert."""
     for dt in ("bf16", "f32"):

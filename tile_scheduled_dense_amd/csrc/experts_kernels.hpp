@@ -42,6 +42,7 @@ tg_status launch_q4_group(const Q4Params &p, hipStream_t s) {
 
 template <int DT> using Tile256 = RingCfg<DT, 256, 256, 2, 2, 16>;
 template <int DT> using Tile128 = RingCfg<DT, 128, 128, 2, 2, 16>;
+using Tile64F32 = RingCfg<DT_F32, 64, 64, 2, 2, 16>;
 
 // the most tile rows that `groups` groups of `rows` rows together can have
 inline int64_t most_tiles(int64_t rows, int64_t groups, int64_t bm) {
@@ -49,11 +50,16 @@ inline int64_t most_tiles(int64_t rows, int64_t groups, int64_t bm) {
     return (rows + parts * (bm - 1)) / bm;
 }
 
-template <class C, bool B_KS, bool PIPE>
+// P: the pieces' configuration (C itself: none).  The grid is the most there can
+// be: whole tiles, three more pieces for each tile that is split, and a row of
+// pieces for every group.
+template <class C, class P, bool B_KS, bool PIPE>
 tg_status launch_tiles(const GroupedParams &p, hipStream_t s) {
-    const int64_t grid = most_tiles(p.rows, p.experts + 1, C::BM) * cdiv(p.N, C::BN);
+    int64_t grid = most_tiles(p.rows, p.experts + 1, C::BM) * cdiv(p.N, C::BN);
+    if (!std::is_same<C, P>::value)
+        grid += 3 * kSplitRound + (p.rows < p.experts + 1 ? p.rows : p.experts + 1) * cdiv(p.N, P::BN);
     if (grid > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((grouped_tile_kernel<C, B_KS, PIPE>), dim3((unsigned)grid), dim3(C::THREADS), 0, s, p);
+    hipLaunchKernelGGL((grouped_tile_kernel<C, P, B_KS, PIPE>), dim3((unsigned)grid), dim3(C::THREADS), 0, s, p);
     return launched();
 }
 
@@ -71,8 +77,11 @@ tg_status launch_grouped_as(const GroupedParams &p, hipStream_t s) {
     // an N below a chunk is not for the tiles (grouped_ring.hpp)
     if (mean > 32 && p.N >= 8) {
         const int64_t tiles = cdiv(p.rows, 256) * cdiv(p.N, 256);
-        if (tiles >= 200) return launch_tiles<Tile256<DT>, !TRANS, true>(p, s);
-        return launch_tiles<Tile128<DT>, !TRANS, false>(p, s);
+        if (tiles >= 200) return launch_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true>(p, s);
+        if constexpr (DT == DT_F32) {
+            if (cdiv(p.rows, 128) * cdiv(p.N, 128) < 512) return launch_tiles<Tile64F32, Tile64F32, !TRANS, false>(p, s);
+        }
+        return launch_tiles<Tile128<DT>, Tile128<DT>, !TRANS, false>(p, s);
     }
     if (mean <= 16) return launch_stream<DT, TRANS, 1>(p, s);
     return launch_stream<DT, TRANS, 2>(p, s);
@@ -90,6 +99,9 @@ tg_status launch_wgrad(const GroupedParams &p, hipStream_t s) {
     if (p.M >= 8 && p.N >= 8) {
         const int64_t tiles = p.experts * cdiv(p.M, 256) * cdiv(p.N, 256);
         if (tiles >= 200) return launch_wgrad_tiles<Tile256<DT>, true>(p, s);
+        if constexpr (DT == DT_F32) {
+            if (p.experts * cdiv(p.M, 128) * cdiv(p.N, 128) < 512) return launch_wgrad_tiles<Tile64F32, false>(p, s);
+        }
         return launch_wgrad_tiles<Tile128<DT>, false>(p, s);
     }
     const int64_t blocks = cdiv((int64_t)p.experts * p.M * p.N, 256);

@@ -15,8 +15,9 @@
 // The extents' fringe: a row or column chunk past the end is fetched from past
 // the resource, which reads 0.  A chunk that the end cuts brings what lies
 // behind, in the same matrix (the host keeps extents below one chunk away), and
-// only feeds outputs that are not stored.  The last K tile goes through registers
-// with element-exact zeros in both operands, so that a NaN behind K meets none.
+// only feeds outputs that are not stored.  A last K tile that K cuts (or whose
+// last chunk would pass a matrix's end) goes through registers with element-exact
+// zeros in both operands, so that a NaN behind K meets none.
 //
 // B's fragments are the matrix instruction's first operand and A's the second:
 // a lane then holds four neighbouring columns of one row of C, so that C is
@@ -157,7 +158,7 @@ struct GroupedTile {
     OA a;
     OB b;
     AccTiles<C> acc;
-    int K, nk, ndma;            // ndma: K tiles copied straight to LDS (all but the last)
+    int K, nk, ndma;            // ndma: K tiles copied straight to LDS (all, or all but the last)
     int wave, lane;
     u32x4 tail[COPIES];
 
@@ -167,7 +168,9 @@ struct GroupedTile {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         K = K_;
         nk = (K + C::BK - 1) / C::BK;
-        ndma = nk > 0 ? nk - 1 : 0;
+        const bool whole = K % C::BK == 0 && (!A_KS || m_left >= C::BM || m_left % C::CHUNK == 0) &&
+                           (!B_KS || n_left >= C::BN || n_left % C::CHUNK == 0);
+        ndma = whole || nk == 0 ? nk : nk - 1;
         const uint32_t lds0 = lds_address(smem);
         b.init(B, ldb, n_left, (wave % C::WAVES_N) * C::WTN, lds0, lane, wave);
         a.init(A, lda, m_left, (wave / C::WAVES_N) * C::WTM, lds0 + STAGES * OB::REGION, lane, wave);
@@ -215,7 +218,7 @@ struct GroupedTile {
     // into the copy just released, multiply tile kt.
     __device__ __forceinline__ void run_ring() {
         if (nk == 0) return;
-        tail_load();
+        if (ndma < nk) tail_load();
 #pragma unroll
         for (int t = 0; t < STAGES - 1; ++t)
             if (t < ndma) copy(t);
@@ -239,6 +242,7 @@ struct GroupedTile {
     // The software pipeline of gemm_ring.hpp (one wave per SIMD, a K tile's
     // fragments in registers, twice): multiply tile t from (fa, fb) while tile
     // t + 1 is read into (na, nb) and tile t + STAGES copied into tile t's copy.
+    // STEADY: both exist; else both are conditional.
     template <bool STEADY, bool FIRST = false>
     __device__ __forceinline__ void iter(int t, int cur, int next, u32x4 (&fa)[C::TM], u32x4 (&fb)[C::TN],
                                          u32x4 (&na)[C::TM], u32x4 (&nb)[C::TN]) {
@@ -270,9 +274,9 @@ struct GroupedTile {
     __device__ __forceinline__ void run_pipe() {
         static_assert(STAGES == 4, "four tiles per trip cycle the LDS copies");
         if (nk == 0) return;
-        // with at most STAGES copied tiles the last one is landed by the prologue or
-        // the first iteration: load it before any copy
-        const bool early = ndma <= STAGES;
+        // a last tile that goes through registers: with at most STAGES copied tiles it is
+        // landed by the prologue or the first iteration, and loaded before any copy
+        const bool cut = ndma < nk, early = cut && ndma <= STAGES;
         if (early) tail_load();
 #pragma unroll
         for (int t = 0; t < STAGES; ++t)
@@ -295,7 +299,7 @@ struct GroupedTile {
         }
         int cur = t % STAGES;
         // the last tile's loads are younger than some copies, which only makes a wait longer
-        if (!early) tail_load();
+        if (cut && !early) tail_load();
         for (; t + 1 < nk; t += 2) {
             const int c1 = (cur + 1) % STAGES, c2 = (cur + 2) % STAGES;
             iter<false>(t, cur, c1, a1, b1, a0, b0);
@@ -326,13 +330,22 @@ struct GroupedTile {
 };
 
 // ---- which tile a workgroup takes ------------------------------------------------------
-// Products over rows: every group (expert, or the rows without one) has
-// ceil(rows / BM) tile rows; only the device knows how many.  The grid holds the
-// most there can be; each wave sums the groups' tile rows, 64 a step, and the
-// workgroups past the total end at once.  Ids are dealt to the XCDs in
-// contiguous runs, walked in groups of group_m tile rows, as the dense kernel's.
+// Products over rows: only the device knows every group's (an expert's, or the
+// rows' without one) rows.  The grid holds the most work there can be; each wave
+// sums the groups' tile rows, 64 groups a step, and workgroups past the total
+// end at once.
+//
+// A kernel of 256 x 256 tiles has pieces of 128 x 128 too, for what would leave
+// the GPU half idle: a group's last tile row when it has at most 128 rows, and
+// the tiles past the last whole round of 256 when there are at most kSplitRound,
+// as four pieces each.
+//
+// Ids are dealt to the XCDs in contiguous runs, walked in groups of 8 tile rows.
+constexpr uint32_t kRound = 256, kSplitRound = 128;
+
 struct RowTile {
-    int g, lo, rows, m0, tn;      // rows: from m0 to the group's end
+    bool piece;
+    int g, lo, rows, m0, n0;      // rows: from m0 to the group's end
 };
 
 __device__ __forceinline__ int wave_inclusive(int v, int lane) {
@@ -343,60 +356,125 @@ __device__ __forceinline__ int wave_inclusive(int v, int lane) {
     return v;
 }
 
-__device__ __forceinline__ bool row_tile(const GroupedParams &p, int BM, int tiles_n, RowTile &t) {
+// id-th of n, so that the ids that one XCD receives (id % 8) are a contiguous run
+__device__ __forceinline__ uint32_t xcd_run(uint32_t id, uint32_t n) {
+    const uint32_t per = n / 8, rem = n % 8, x = id % 8;
+    return x * per + (x < rem ? x : rem) + id / 8;
+}
+
+// tile id of rows x cols tiles, by columns within groups of 8 tile rows
+__device__ __forceinline__ void grouped_order(uint32_t id, uint32_t rows, uint32_t cols, int &tm, int &tn) {
+    const uint32_t group = id / (8 * cols), first = group * 8;
+    const uint32_t here = rows - first < 8 ? rows - first : 8;
+    const uint32_t in = id - first * cols;
+    tm = (int)(first + in % here);
+    tn = (int)(in / here);
+}
+
+// BM: 256 with pieces of 128 (PIECES), or a tile of BM x BN alone.
+template <int BM, int BN, bool PIECES>
+__device__ __forceinline__ bool row_tile(const GroupedParams &p, RowTile &t) {
     const int lane = threadIdx.x & 63;
     const int groups = p.experts + 1;
+    const uint32_t tiles_n = (p.N + BN - 1) / BN;
     RowSpan s = {0, 0};
-    int mine = 0, incl = 0;
+    int big = 0, small = 0, big_incl = 0, small_incl = 0;
     auto look = [&](int base) {
         s = base + lane < groups ? rows_of(p.offsets, base + lane, p.experts, p.rows) : RowSpan{0, 0};
-        mine = (s.hi - s.lo + BM - 1) / BM;
-        incl = wave_inclusive(mine, lane);
-        return __builtin_amdgcn_readlane(incl, 63);
+        const int n = s.hi - s.lo, rest = n % BM;
+        if (PIECES) {
+            big = n / BM + (rest > BM / 2);
+            small = rest > 0 && rest <= BM / 2;
+            small_incl = wave_inclusive(small, lane);
+        } else {
+            big = (n + BM - 1) / BM;
+        }
+        big_incl = wave_inclusive(big, lane);
     };
-    int total_m = 0;
-    for (int base = 0; base < groups; base += 64) total_m += look(base);
-    const uint32_t total = (uint32_t)total_m * (uint32_t)tiles_n;
-    if (blockIdx.x >= total) return false;
-    const uint32_t per = total / 8, rem = total % 8, x = blockIdx.x % 8;
-    const uint32_t id = x * per + (x < rem ? x : rem) + blockIdx.x / 8;
-    const uint32_t gm = 8, group = id / (gm * tiles_n), first = group * gm;
-    const uint32_t rows = (uint32_t)total_m - first < gm ? (uint32_t)total_m - first : gm;
-    const uint32_t in = id - group * gm * tiles_n;
-    const int tm = (int)(first + in % rows);
-    t.tn = (int)(in / rows);
+    uint32_t total_b = 0, total_s = 0;
+    for (int base = 0; base < groups; base += 64) {
+        look(base);
+        total_b += __builtin_amdgcn_readlane(big_incl, 63);
+        if (PIECES) total_s += __builtin_amdgcn_readlane(small_incl, 63);
+    }
+    const uint32_t tiles = total_b * tiles_n, left = PIECES ? tiles % kRound : 0;
+    const uint32_t whole = PIECES && left <= kSplitRound ? tiles - left : tiles;   // tiles taken as they are
+    uint32_t id = blockIdx.x;
+    int row;              // which tile row, among the big ones or the small ones
+    int half_m = 0;       // a piece's place in a split tile's rows
+    bool of_small = false;
+    t.piece = false;
+    if (id < whole) {
+        int tn;
+        grouped_order(xcd_run(id, whole), total_b, tiles_n, row, tn);
+        t.n0 = tn * BN;
+    } else {
+        if (!PIECES) return false;
+        id -= whole;
+        t.piece = true;
+        int tn;
+        if (id < 4 * (tiles - whole)) {
+            grouped_order(whole + id / 4, total_b, tiles_n, row, tn);
+            half_m = id / 2 % 2;
+            t.n0 = tn * BN + (int)(id % 2) * (BN / 2);
+        } else {
+            id -= 4 * (tiles - whole);
+            const uint32_t pieces_n = (p.N + BN / 2 - 1) / (BN / 2);
+            if (id >= total_s * pieces_n) return false;
+            of_small = true;
+            row = (int)(id / pieces_n);
+            t.n0 = (int)(id % pieces_n) * (BN / 2);
+        }
+        if (t.n0 >= p.N) return false;
+    }
     int before = 0;
     for (int base = 0; base < groups; base += 64) {
-        const int here = groups <= 64 ? total_m : look(base);
-        if (tm < before + here) {
-            const int l = __builtin_ctzll(__ballot(before + incl > tm));
+        if (groups > 64) look(base);
+        const int incl = of_small ? small_incl : big_incl, mine = of_small ? small : big;
+        const int here = __builtin_amdgcn_readlane(incl, 63);
+        if (row < before + here) {
+            const int l = __builtin_ctzll(__ballot(before + incl > row));
+            const int first = before + __builtin_amdgcn_readlane(incl - mine, l);
             t.g = base + l;
             t.lo = __builtin_amdgcn_readlane(s.lo, l);
-            t.m0 = (tm - before - __builtin_amdgcn_readlane(incl - mine, l)) * BM;
-            t.rows = __builtin_amdgcn_readlane(s.hi, l) - t.lo - t.m0;
-            return true;
+            const int n = __builtin_amdgcn_readlane(s.hi, l) - t.lo;
+            t.m0 = of_small ? n / BM * BM : (row - first) * BM + half_m * (BM / 2);
+            t.rows = n - t.m0;
+            return t.rows > 0;
         }
         before += here;
     }
     return false;
 }
 
-template <class C, bool B_KS, bool PIPE>
-__global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void grouped_tile_kernel(GroupedParams p) {
-    using Tile = GroupedTile<C, false, B_KS, 4>;
-    __shared__ __attribute__((aligned(1024))) char smem[Tile::LDS];
-    RowTile t;
-    if (!row_tile(p, C::BM, (p.N + C::BN - 1) / C::BN, t)) return;
-    const bool dead = t.g == p.experts;
-    const int n0 = t.tn * C::BN;
-    const char *A = p.A + (int64_t)(t.lo + t.m0) * p.lda * C::ELEM;
-    const char *B = p.B + ((dead ? 0 : (int64_t)t.g * p.sB) + (B_KS ? (int64_t)n0 : n0 * p.ldb)) * C::ELEM;
-    Tile tile;
-    tile.init(A, p.lda, t.rows, B, p.ldb, p.N - n0, dead ? 0 : p.K, smem);
+template <class C, bool A_KS, bool B_KS, bool PIPE>
+__device__ __forceinline__ void run_tile_of(const GroupedParams &p, char *smem, const char *A, int64_t lda, int m_left,
+                                            const char *B, int n_left, int K, int64_t c_at, bool wide) {
+    GroupedTile<C, A_KS, B_KS, 4> tile;
+    tile.init(A, lda, m_left, B, p.ldb, n_left, K, smem);
     if constexpr (PIPE) tile.run_pipe();
     else tile.run_ring();
+    tile.store(p.C, c_at, p.ldc, m_left, n_left, p.c_f32, wide);
+}
+
+// P: the configuration of the pieces (C itself: none).
+template <class C, class P, bool B_KS, bool PIPE>
+__global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void grouped_tile_kernel(GroupedParams p) {
+    constexpr bool PIECES = !std::is_same<C, P>::value;
+    static_assert(!PIECES || (P::BM * 2 == C::BM && P::BN * 2 == C::BN && P::THREADS == C::THREADS), "quarters");
+    __shared__ __attribute__((aligned(1024))) char smem[GroupedTile<C, false, B_KS, 4>::LDS];
+    RowTile t;
+    if (!row_tile<C::BM, C::BN, PIECES>(p, t)) return;
+    const bool dead = t.g == p.experts;
+    const int64_t row = t.lo + t.m0;
+    const char *A = p.A + row * p.lda * C::ELEM;
+    const char *B = p.B + ((dead ? 0 : (int64_t)t.g * p.sB) + (B_KS ? (int64_t)t.n0 : t.n0 * p.ldb)) * C::ELEM;
     const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
-    tile.store(p.C, (int64_t)(t.lo + t.m0) * p.ldc + n0, p.ldc, t.rows, p.N - n0, p.c_f32, wide);
+    const int K = dead ? 0 : p.K;
+    if (PIECES && t.piece)
+        run_tile_of<P, false, B_KS, PIPE>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0, wide);
+    else
+        run_tile_of<C, false, B_KS, PIPE>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0, wide);
 }
 
 // The gradient with respect to B: experts x tiles_m x tiles_n tiles, whose work
@@ -405,26 +483,21 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void grouped_tile_kernel(
 // expert would work on alone.
 template <class C, bool PIPE>
 __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void wgrad_tile_kernel(GroupedParams p) {
-    using Tile = GroupedTile<C, true, true, 4>;
-    __shared__ __attribute__((aligned(1024))) char smem[Tile::LDS];
+    __shared__ __attribute__((aligned(1024))) char smem[GroupedTile<C, true, true, 4>::LDS];
     const uint32_t tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN, tiles = tiles_m * tiles_n;
     const uint32_t run = (tiles + 7) / 8;
     const int g = (int)(blockIdx.x / (8 * run));
     const uint32_t in = blockIdx.x % (8 * run), id = in % 8 * run + in / 8;
     if (id >= tiles) return;
-    const uint32_t gm = 8, group = id / (gm * tiles_n), first = group * gm;
-    const uint32_t rows = tiles_m - first < gm ? tiles_m - first : gm;
-    const uint32_t at = id - group * gm * tiles_n;
-    const int m0 = (int)(first + at % rows) * C::BM, n0 = (int)(at / rows) * C::BN;
+    int tm, tn;
+    grouped_order(id, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * C::BM, n0 = tn * C::BN;
     const RowSpan s = rows_of(p.offsets, g, p.experts, p.rows);
     const int lo = __builtin_amdgcn_readfirstlane(s.lo), K = __builtin_amdgcn_readfirstlane(s.hi) - lo;
-    Tile tile;
-    tile.init(p.A + ((int64_t)lo * p.lda + m0) * C::ELEM, p.lda, p.M - m0, p.B + ((int64_t)lo * p.ldb + n0) * C::ELEM,
-              p.ldb, p.N - n0, K, smem);
-    if constexpr (PIPE) tile.run_pipe();
-    else tile.run_ring();
     const bool wide = p.ldc % 4 == 0 && p.sC % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
-    tile.store(p.C, (int64_t)g * p.sC + (int64_t)m0 * p.ldc + n0, p.ldc, p.M - m0, p.N - n0, p.c_f32, wide);
+    run_tile_of<C, true, true, PIPE>(p, smem, p.A + ((int64_t)lo * p.lda + m0) * C::ELEM, p.lda, p.M - m0,
+                                     p.B + ((int64_t)lo * p.ldb + n0) * C::ELEM, p.N - n0, K,
+                                     (int64_t)g * p.sC + (int64_t)m0 * p.ldc + n0, wide);
 }
 
 }  // namespace tg
