@@ -310,19 +310,69 @@ struct GroupedTile {
         acc.settle();
     }
 
-    // C's tile: rows m < m_left, columns n < n_left, from its first element
-    __device__ __forceinline__ void store(char *Cp, int64_t at, int64_t ldc, int m_left, int n_left, bool c_f32,
-                                          bool wide) const {
-        const int m = (wave / C::WAVES_N) * C::WTM + lane % 16, n = (wave % C::WAVES_N) * C::WTN + 4 * (lane / 16);
+    // C's tile: rows m < m_left, columns n < n_left, from its element `at`.
+    // A whole tile on 16-byte rows takes straight-line code, without a test between
+    // stores: 16 bytes a lane.  Of a 16-bit C a lane holds 8 bytes of each fragment, so
+    // neighbouring fragments trade halves between lane groups (v_permlane16_swap:
+    // the odd rows of 16 lanes of one register against the even ones of the other),
+    // and a store writes 64 bytes of each row.
+    __device__ __forceinline__ void store(char *Cp, int64_t at, int64_t ldc, int m_left, int n_left, bool c_f32) const {
+        typedef typename ElemOf<C::DT>::type T;
+        const int g = lane / 16, m = (wave / C::WAVES_N) * C::WTM + lane % 16, n = (wave % C::WAVES_N) * C::WTN;
+        const bool f32 = C::DT == DT_F32 || c_f32;
+        const int size = f32 ? 4 : 2;
+        char *first = Cp + at * size;
+        const bool wide = ldc * size % 16 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
+        if (wide && m_left >= C::BM && n_left >= C::BN) {
+            char *row = first + ((int64_t)m * ldc + n) * size;
+            const int64_t step = 16 * ldc * size;
+            if (f32) {
+                row += 16 * g;
+                static_for<0, C::TM, 1>([&](auto ic) {
+                    constexpr int i = decltype(ic)::value;
+                    static_for<0, C::TN, 1>([&](auto jc) {
+                        constexpr int j = decltype(jc)::value;
+                        *reinterpret_cast<f32x4 *>(row + 64 * j) =
+                            f32x4{acc.get(i, j, 0), acc.get(i, j, 1), acc.get(i, j, 2), acc.get(i, j, 3)};
+                    });
+                    row += step;
+                });
+            } else if constexpr (C::DT != DT_F32 && C::TN % 2 == 0) {
+                typedef T t2 __attribute__((ext_vector_type(2)));
+                // after the trade lane groups 0 and 2 hold columns 0-7 and 8-15 of the even
+                // fragment, groups 1 and 3 those of the odd one
+                row += 16 * (g / 2) + 32 * (g % 2);
+                static_for<0, C::TM, 1>([&](auto ic) {
+                    constexpr int i = decltype(ic)::value;
+                    static_for<0, C::TN, 2>([&](auto jc) {
+                        constexpr int j = decltype(jc)::value;
+                        u32x4 v;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const t2 even = {(T)acc.get(i, j, 2 * h), (T)acc.get(i, j, 2 * h + 1)};
+                            const t2 odd = {(T)acc.get(i, j + 1, 2 * h), (T)acc.get(i, j + 1, 2 * h + 1)};
+                            const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, even),
+                                                                            __builtin_bit_cast(uint32_t, odd), false, false);
+                            v[h] = r[0];
+                            v[2 + h] = r[1];
+                        }
+                        *reinterpret_cast<u32x4 *>(row + 32 * j) = v;
+                    });
+                    row += step;
+                });
+            }
+            return;
+        }
+        const bool wide4 = ldc % 4 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
         static_for<0, C::TM, 1>([&](auto ic) {
             constexpr int i = decltype(ic)::value;
             if (m + 16 * i < m_left) {
-                const int64_t row = at + (int64_t)(m + 16 * i) * ldc;
+                const int64_t row = at + (int64_t)(m + 16 * i) * ldc + n + 4 * g;
                 static_for<0, C::TN, 1>([&](auto jc) {
                     constexpr int j = decltype(jc)::value;
                     const f32x4 v = {acc.get(i, j, 0), acc.get(i, j, 1), acc.get(i, j, 2), acc.get(i, j, 3)};
-                    if (n + 16 * j < n_left)
-                        store4<C::DT>(Cp, row + n + 16 * j, n_left - n - 16 * j, c_f32, wide, v);
+                    const int left = n_left - n - 4 * g - 16 * j;
+                    if (left > 0) store4<C::DT>(Cp, row + 16 * j, left, c_f32, wide4, v);
                 });
             }
         });
@@ -449,12 +499,12 @@ __device__ __forceinline__ bool row_tile(const GroupedParams &p, RowTile &t) {
 
 template <class C, bool A_KS, bool B_KS, bool PIPE>
 __device__ __forceinline__ void run_tile_of(const GroupedParams &p, char *smem, const char *A, int64_t lda, int m_left,
-                                            const char *B, int n_left, int K, int64_t c_at, bool wide) {
+                                            const char *B, int n_left, int K, int64_t c_at) {
     GroupedTile<C, A_KS, B_KS, 4> tile;
     tile.init(A, lda, m_left, B, p.ldb, n_left, K, smem);
     if constexpr (PIPE) tile.run_pipe();
     else tile.run_ring();
-    tile.store(p.C, c_at, p.ldc, m_left, n_left, p.c_f32, wide);
+    tile.store(p.C, c_at, p.ldc, m_left, n_left, p.c_f32);
 }
 
 // P: the configuration of the pieces (C itself: none).
@@ -469,12 +519,11 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void grouped_tile_kernel(
     const int64_t row = t.lo + t.m0;
     const char *A = p.A + row * p.lda * C::ELEM;
     const char *B = p.B + ((dead ? 0 : (int64_t)t.g * p.sB) + (B_KS ? (int64_t)t.n0 : t.n0 * p.ldb)) * C::ELEM;
-    const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
     const int K = dead ? 0 : p.K;
     if (PIECES && t.piece)
-        run_tile_of<P, false, B_KS, PIPE>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0, wide);
+        run_tile_of<P, false, B_KS, PIPE>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0);
     else
-        run_tile_of<C, false, B_KS, PIPE>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0, wide);
+        run_tile_of<C, false, B_KS, PIPE>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0);
 }
 
 // The gradient with respect to B: experts x tiles_m x tiles_n tiles, whose work
@@ -494,10 +543,9 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void wgrad_tile_kernel(Gr
     const int m0 = tm * C::BM, n0 = tn * C::BN;
     const RowSpan s = rows_of(p.offsets, g, p.experts, p.rows);
     const int lo = __builtin_amdgcn_readfirstlane(s.lo), K = __builtin_amdgcn_readfirstlane(s.hi) - lo;
-    const bool wide = p.ldc % 4 == 0 && p.sC % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
     run_tile_of<C, true, true, PIPE>(p, smem, p.A + ((int64_t)lo * p.lda + m0) * C::ELEM, p.lda, p.M - m0,
                                      p.B + ((int64_t)lo * p.ldb + n0) * C::ELEM, p.N - n0, K,
-                                     (int64_t)g * p.sC + (int64_t)m0 * p.ldc + n0, wide);
+                                     (int64_t)g * p.sC + (int64_t)m0 * p.ldc + n0);
 }
 
 }  // namespace tg
