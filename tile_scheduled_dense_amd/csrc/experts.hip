@@ -230,6 +230,11 @@ tg_status product_arguments(int64_t experts, int64_t rows, int64_t N, int64_t K,
     return TG_OK;
 }
 
+// whether operands and result together exceed the last-level cache (GroupedParams::past)
+bool past_caches(int64_t operand_bytes, int64_t result_bytes) {
+    return operand_bytes + result_bytes > (int64_t(256) << 20);
+}
+
 // A block's tile of an operand (256 rows of ld elements at most) is addressed
 // in 31 bits from its first element.
 bool tile_fits(int64_t ld, int esz) { return ld <= kMaxExtent && (256 * ld + 4096) * esz < (int64_t(1) << 31) - 65536; }
@@ -268,6 +273,7 @@ tg_status grouped(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype 
     p.N = (int)N;
     p.K = (int)K;
     p.c_f32 = c_dtype == TG_F32;
+    p.past = past_caches((rows * K + experts * N * K) * esz, rows * N * csz);
     hipStream_t s = static_cast<hipStream_t>(stream);
     switch (dtype) {
         case TG_F32: return launch_grouped<DT_F32>(p, transposed != 0, s);
@@ -309,6 +315,7 @@ tg_status wgrad(int64_t experts, int64_t rows, int64_t M, int64_t N, tg_dtype dt
     p.M = (int)M;
     p.N = (int)N;
     p.c_f32 = c_dtype == TG_F32;
+    p.past = past_caches(rows * (M + N) * esz, experts * M * N * csz);
     hipStream_t s = static_cast<hipStream_t>(stream);
     switch (dtype) {
         case TG_F32: return launch_wgrad<DT_F32>(p, s);

@@ -312,55 +312,88 @@ struct GroupedTile {
 
     // C's tile: rows m < m_left, columns n < n_left, from its element `at`.
     // A whole tile on 16-byte rows takes straight-line code, without a test between
-    // stores: 16 bytes a lane.  Of a 16-bit C a lane holds 8 bytes of each fragment, so
-    // neighbouring fragments trade halves between lane groups (v_permlane16_swap:
-    // the odd rows of 16 lanes of one register against the even ones of the other),
-    // and a store writes 64 bytes of each row.
-    __device__ __forceinline__ void store(char *Cp, int64_t at, int64_t ldc, int m_left, int n_left, bool c_f32) const {
+    // stores, that writes 128 bytes of each of eight rows at a time, whole cache lines
+    // where C's rows are aligned to them (64 or 32 bytes a row cost up to 40% more).  Of a
+    // 16-bit C a lane holds 8 bytes of each fragment, so neighbouring fragments trade
+    // halves between lane groups first (v_permlane16_swap: the odd rows of 16 lanes of
+    // one register against the even ones of the other).  Then two 64-byte neighbours P,
+    // Q of 16 rows trade their halves of 8 rows (a rotation by 8 lanes).
+    __device__ __forceinline__ static void trade_rows(const u32x4 &P, const u32x4 &Q, u32x4 &low, u32x4 &high) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            // row_ror:8, written to lanes 8-15 (banks 2, 3) or 0-7 (banks 0, 1) of each 16
+            low[c] = __builtin_amdgcn_update_dpp((int)P[c], (int)Q[c], 0x128, 0xf, 0xc, false);
+            high[c] = __builtin_amdgcn_update_dpp((int)Q[c], (int)P[c], 0x128, 0xf, 0x3, false);
+        }
+    }
+    // fragments j, j + 1 of row tile i in 16 bits: 16 bytes of lane group 0, 2 are columns
+    // 0-7, 8-15 of the even fragment, of 1, 3 those of the odd one
+    template <int i, int j>
+    __device__ __forceinline__ u32x4 pair16() const {
+        typedef typename ElemOf<C::DT>::type t2 __attribute__((ext_vector_type(2)));
         typedef typename ElemOf<C::DT>::type T;
+        u32x4 v;
+        static_for<0, 2, 1>([&](auto hc) {
+            constexpr int h = decltype(hc)::value;
+            const t2 even = {(T)acc.get(i, j, 2 * h), (T)acc.get(i, j, 2 * h + 1)};
+            const t2 odd = {(T)acc.get(i, j + 1, 2 * h), (T)acc.get(i, j + 1, 2 * h + 1)};
+            const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, even),
+                                                            __builtin_bit_cast(uint32_t, odd), false, false);
+            v[h] = r[0];
+            v[2 + h] = r[1];
+        });
+        return v;
+    }
+    template <int i, int j>
+    __device__ __forceinline__ u32x4 quad32() const {
+        return __builtin_bit_cast(u32x4, f32x4{acc.get(i, j, 0), acc.get(i, j, 1), acc.get(i, j, 2), acc.get(i, j, 3)});
+    }
+    // PAST: with the non-temporal hint (GroupedParams::past)
+    template <bool PAST>
+    __device__ __forceinline__ static void put(char *at, const u32x4 &v) {
+        if constexpr (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(at));
+        else *reinterpret_cast<u32x4 *>(at) = v;
+    }
+    template <bool F32, bool PAST>
+    __device__ __forceinline__ void store_whole(char *row, int64_t half) const {
+        static_for<0, C::TM, 1>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            if constexpr (F32) {
+                static_for<0, C::TN, 2>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    u32x4 low, high;
+                    trade_rows(quad32<i, j>(), quad32<i, j + 1>(), low, high);
+                    put<PAST>(row + 64 * j, low);
+                    put<PAST>(row + 64 * j + half, high);
+                });
+            } else if constexpr (C::DT != DT_F32) {
+                static_for<0, C::TN, 4>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    u32x4 low, high;
+                    trade_rows(pair16<i, j>(), pair16<i, j + 2>(), low, high);
+                    put<PAST>(row + 32 * j, low);
+                    put<PAST>(row + 32 * j + half, high);
+                });
+            }
+            row += 2 * half;
+        });
+    }
+    __device__ __forceinline__ void store(char *Cp, int64_t at, int64_t ldc, int m_left, int n_left, bool c_f32,
+                                          bool past) const {
         const int g = lane / 16, m = (wave / C::WAVES_N) * C::WTM + lane % 16, n = (wave % C::WAVES_N) * C::WTN;
         const bool f32 = C::DT == DT_F32 || c_f32;
         const int size = f32 ? 4 : 2;
         char *first = Cp + at * size;
         const bool wide = ldc * size % 16 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
         if (wide && m_left >= C::BM && n_left >= C::BN) {
-            char *row = first + ((int64_t)m * ldc + n) * size;
-            const int64_t step = 16 * ldc * size;
-            if (f32) {
-                row += 16 * g;
-                static_for<0, C::TM, 1>([&](auto ic) {
-                    constexpr int i = decltype(ic)::value;
-                    static_for<0, C::TN, 1>([&](auto jc) {
-                        constexpr int j = decltype(jc)::value;
-                        *reinterpret_cast<f32x4 *>(row + 64 * j) =
-                            f32x4{acc.get(i, j, 0), acc.get(i, j, 1), acc.get(i, j, 2), acc.get(i, j, 3)};
-                    });
-                    row += step;
-                });
-            } else if constexpr (C::DT != DT_F32 && C::TN % 2 == 0) {
-                typedef T t2 __attribute__((ext_vector_type(2)));
-                // after the trade lane groups 0 and 2 hold columns 0-7 and 8-15 of the even
-                // fragment, groups 1 and 3 those of the odd one
-                row += 16 * (g / 2) + 32 * (g % 2);
-                static_for<0, C::TM, 1>([&](auto ic) {
-                    constexpr int i = decltype(ic)::value;
-                    static_for<0, C::TN, 2>([&](auto jc) {
-                        constexpr int j = decltype(jc)::value;
-                        u32x4 v;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const t2 even = {(T)acc.get(i, j, 2 * h), (T)acc.get(i, j, 2 * h + 1)};
-                            const t2 odd = {(T)acc.get(i, j + 1, 2 * h), (T)acc.get(i, j + 1, 2 * h + 1)};
-                            const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, even),
-                                                                            __builtin_bit_cast(uint32_t, odd), false, false);
-                            v[h] = r[0];
-                            v[2 + h] = r[1];
-                        }
-                        *reinterpret_cast<u32x4 *>(row + 32 * j) = v;
-                    });
-                    row += step;
-                });
-            }
+            const int rm = (wave / C::WAVES_N) * C::WTM + lane % 8;
+            char *row = first + ((int64_t)rm * ldc + n) * size + 64 * (lane % 16 / 8);
+            const int64_t half = 8 * ldc * size;
+            row += f32 ? 16 * g : 16 * (g / 2) + 32 * (g % 2);
+            if (f32 && past) store_whole<true, true>(row, half);
+            else if (f32) store_whole<true, false>(row, half);
+            else if (past) store_whole<false, true>(row, half);
+            else store_whole<false, false>(row, half);
             return;
         }
         const bool wide4 = ldc % 4 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
@@ -504,7 +537,7 @@ __device__ __forceinline__ void run_tile_of(const GroupedParams &p, char *smem, 
     tile.init(A, lda, m_left, B, p.ldb, n_left, K, smem);
     if constexpr (PIPE) tile.run_pipe();
     else tile.run_ring();
-    tile.store(p.C, c_at, p.ldc, m_left, n_left, p.c_f32);
+    tile.store(p.C, c_at, p.ldc, m_left, n_left, p.c_f32, p.past);
 }
 
 // P: the configuration of the pieces (C itself: none).

@@ -33,6 +33,12 @@ struct GroupedParams {
     int experts, rows;
     int M, N, K;                         // wgrad: C[g] is M x N (K unused); grouped: rows x N over K
     int c_f32;
+    // C stored past the caches: set where operands and result together exceed the
+    // 256 MiB last-level cache, in which a result would then drive out operands that
+    // other workgroups still read (16384 x 4096 x 2048 bf16 over 8 experts: forward 245 ->
+    // 229 us, the gradients 245 -> 234 and 249 -> 222; where all of it fits, the hint costs:
+    // 8192 x 8192 x 2048 for one expert 211 -> 213 us).
+    int past;
 };
 
 template <int DT, bool TRANS>
