@@ -23,21 +23,38 @@ tg_status launch_stream(const GroupedParams &p, hipStream_t s) {
     return launched();
 }
 
-template <int DT, int GROUP, int MT>
-tg_status launch_q4_as(const Q4Params &p, hipStream_t s) {
-    const int waves = p.k_blocks >= 32 && MT < 4 ? 16 : (p.k_blocks >= 16 ? 8 : (p.k_blocks >= 4 ? 4 : 1));
-    const dim3 grid((unsigned)p.n_tiles, (unsigned)p.experts + 1);
-    hipLaunchKernelGGL((q4_kernel<DT, GROUP, MT>), grid, dim3(64 * waves), waves * MT * 1024, s, p);
+template <int DT, int GROUP, int MT, int NT>
+tg_status launch_q4_as(const Q4Params &p, int64_t chunks, hipStream_t s) {
+    // waves that split K: more while they have four blocks each and there are not yet
+    // 4096 (a wave costs 0.6 ns to start: 64 experts of 2048 x 2048, 24 of them with
+    // rows, take 15 us in workgroups of 2 waves, 17 of 4, 27 of 8)
+    const int64_t strips = cdiv(p.n_tiles, NT);
+    int waves = 1;
+    while (waves < q4_waves<DT, MT>() && waves * 4 <= p.k_blocks && (waves < 2 || strips * p.experts * waves < 4096))
+        waves *= 2;
+    const unsigned lds = waves * Q4Rows<DT, MT>::LDS * 16;
+    const dim3 grid((unsigned)strips, (unsigned)p.experts + 1, (unsigned)cdiv(chunks, MT));
+    hipLaunchKernelGGL((q4_kernel<DT, GROUP, MT, NT>), grid, dim3(64 * waves), lds, s, p);
     return launched();
 }
 
-// row tiles of 16 taken together: by the rows an expert has on average
+// Row tiles (MT) and n tiles (NT) of a workgroup: more of either reads the codes or
+// the activations less often, as long as there are workgroups for the 256 CUs.
+// fp32 takes one of each, in as many workgroups: two row tiles leave room for half the
+// waves, whose latency then shows (37 rows, 1001 x 4100: 12 us against 28).
+// chunks: row tiles that an expert has on average.
 template <int DT, int GROUP>
 tg_status launch_q4_group(const Q4Params &p, hipStream_t s) {
-    const int64_t mean = cdiv(p.rows, p.experts);
-    if (mean <= 16) return launch_q4_as<DT, GROUP, 1>(p, s);
-    if (mean <= 32) return launch_q4_as<DT, GROUP, 2>(p, s);
-    return launch_q4_as<DT, GROUP, 4>(p, s);
+    const int64_t chunks = cdiv(cdiv(p.rows, p.experts), 16) < 64 ? cdiv(cdiv(p.rows, p.experts), 16) : 64;
+    const int64_t strips = (int64_t)p.n_tiles * p.experts;
+    if constexpr (DT == DT_F32) {
+        return launch_q4_as<DT, GROUP, 1, 1>(p, chunks, s);
+    } else {
+        if (chunks > 2 && strips * cdiv(chunks, 4) >= 256) return launch_q4_as<DT, GROUP, 4, 1>(p, chunks, s);
+        if (chunks > 1 && strips * cdiv(chunks, 2) >= 256) return launch_q4_as<DT, GROUP, 2, 1>(p, chunks, s);
+        if (strips * chunks >= 512) return launch_q4_as<DT, GROUP, 1, 2>(p, chunks, s);
+        return launch_q4_as<DT, GROUP, 1, 1>(p, chunks, s);
+    }
 }
 
 template <int DT> using Tile256 = RingCfg<DT, 256, 256, 2, 2, 16>;

@@ -22,8 +22,9 @@ namespace tg {
 // 32 s + 8 (l / 16) .. + 7: the lane's operand of the 16x16x32 matrix
 // instruction of k step s (fp32: eight 16x16x4 instructions, element e of every
 // lane to instruction e).  Blocks of one n tile follow each other along k, n
-// tiles and then experts outside.  The scales come after all codes, 16 n
-// together: [expert][n tile][group][16].  Past N and K: weight 0, scale 0.
+// tiles and then experts outside.  The scales come after all codes, a block's
+// together: [expert][n tile][block][n / 4 of 4][group of the block][n % 4], so that a
+// lane finds those of its four outputs side by side.  Past N and K: weight 0, scale 0.
 constexpr int kQ4N = 16, kQ4K = 128;
 
 struct Q4Shape {
@@ -42,13 +43,14 @@ inline Q4Shape q4_shape(int64_t experts, int64_t N, int64_t K, int64_t group, in
 
 // Where element e (0 .. 7) of a lane's eight sits in its word, and how it is
 // stored, is chosen for the cheapest way back to the input type:
-//  * f16: code e in bits 4 (e / 2) + 16 (e % 2), as it is: a shift and a mask
-//    give two codes in the low bits of two halves, or-ing 0x6400 makes them
-//    1024 + code exactly, and a packed subtraction of 1032 ends it: 11
-//    instructions for eight.
+//  * f16: code e in bits 4 (e / 2) + 16 (e % 2), as it is: a mask leaves two codes in
+//    the low four or the next four bits of two halves, or-ing 0x6400 makes them 1024 +
+//    code or 1024 + 16 code exactly, and a packed subtraction of 1032, or a
+//    multiplication by 1 / 16 less 72, ends it: 9 instructions for eight.
 //  * bf16, f32: code e in bits 4 e, its top bit turned, which makes it the
-//    two's complement of code - 8; v_cvt_off_f32_i4 turns one into fp32 (value
-//    / 16, exactly) in one instruction.  The factor 16 goes into the group's fma.
+//    two's complement of code - 8; v_cvt_off_f32_i4 turns four bits into fp32 (value /
+//    16, exactly).  The factor 16 is applied to the finished sum: 15 instructions for
+//    eight bf16.
 template <int DT>
 TG_HD int q4_bit(int e) { return DT == DT_F16 ? 4 * (e / 2) + 16 * (e % 2) : 4 * e; }
 template <int DT>
@@ -87,20 +89,34 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t *__restrict_
     const int64_t count = experts * s.n_tiles * s.groups * kQ4N;
     const int64_t groups_in = (K + group - 1) / group;
     for (int64_t i = first; i < count; i += step) {
-        const int64_t q = i / kQ4N % s.groups, tile = i / kQ4N / s.groups;
-        const int64_t n = tile % s.n_tiles * kQ4N + i % kQ4N, g = tile / s.n_tiles;
+        const int per = kQ4K / group;                       // groups of a block
+        const int64_t block = i / (kQ4N * per), in = i % (kQ4N * per), tile = block / s.k_blocks;
+        const int64_t q = block % s.k_blocks * per + in / 4 % per;
+        const int64_t n = tile % s.n_tiles * kQ4N + in / (4 * per) * 4 + in % 4, g = tile / s.n_tiles;
         out[i] = n < N && q < groups_in ? scales[g * stride_scales + n * ld_scales + q] : (T)0.0f;
     }
 }
 
 // Eight codes of a word as a matrix operand: 16 bytes (16-bit types), or eight
-// floats.  Q4_UNIT is what one unit of the operand stands for.
+// floats.  Q4Unit is what one unit of the operand stands for.
 template <int DT> struct Q4Unit { static constexpr float value = 16.0f; };
 template <> struct Q4Unit<DT_F16> { static constexpr float value = 1.0f; };
 
 __device__ __forceinline__ void q4_floats(uint32_t w, float (&f)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __builtin_amdgcn_cvt_off_f32_i4((int)(w >> (4 * e)));
+    // v_cvt_off_f32_i4 reads the low four bits of its source, whose upper half or top
+    // byte the instruction selects itself: three shifts for eight codes.  The empty asm
+    // keeps a shift of a shift apart.
+    uint32_t x = w >> 4;
+    asm("" : "+v"(x));
+    auto cvt = [](uint32_t v) { return __builtin_amdgcn_cvt_off_f32_i4((int)v); };
+    f[0] = cvt(w);
+    f[1] = cvt(x);
+    f[2] = cvt(w >> 8);
+    f[3] = cvt(x >> 8);
+    f[4] = cvt(w >> 16);
+    f[5] = cvt(x >> 16);
+    f[6] = cvt(w >> 24);
+    f[7] = cvt(x >> 24);
 }
 template <int DT>
 __device__ __forceinline__ u32x4 q4_operand(uint32_t w) {
@@ -108,9 +124,18 @@ __device__ __forceinline__ u32x4 q4_operand(uint32_t w) {
     if constexpr (DT == DT_F16) {
         typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
         const f16x2 off = {(_Float16)1032.0f, (_Float16)1032.0f};
+        const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f}, off16 = {(_Float16)72.0f, (_Float16)72.0f};
+        // one v_and_or_b32 each: a literal at most would fit the instruction, so the
+        // two are kept in registers
+        uint32_t low = 0x000f000fu, high = 0x00f000f0u, one = 0x64006400u;
+        asm("" : "+s"(low), "+s"(high), "+v"(one));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, ((w >> (4 * i)) & 0x000f000fu) | 0x64006400u) - off);
+        for (int i = 0; i < 4; i += 2) {
+            const uint32_t x = i == 0 ? w : w >> 8;
+            v[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, (x & low) | one) - off);
+            v[i + 1] = __builtin_bit_cast(
+                uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (x & high) | one), sixteenth, -off16));
+        }
     } else {
         float f[8];
         q4_floats(w, f);
@@ -133,107 +158,229 @@ struct Q4Params {
     int c_f32;                      // C is fp32 (else the input type)
 };
 
-// A workgroup takes one n tile of one expert; its waves split K (blocks w,
-// w + W, ...) and add their sums in LDS, wave by wave in order.  Weights are the
+// A workgroup takes NT neighbouring n tiles of one expert; its waves split K
+// (blocks w, w + W, ...) and add their sums in LDS, in wave order.  Weights are the
 // matrix instruction's first operand, so lane l holds C[row l % 16][n 4 (l / 16)
 // .. + 3]: four neighbours in a row of C, one store.  MT row tiles of 16 at a
-// time; more rows take further passes over the codes (from L2).
-template <int DT, int GROUP, int MT>
-__global__ __launch_bounds__(MT == 4 ? 512 : 1024) void q4_kernel(Q4Params p) {
+// time; further ones go to gridDim.z workgroups in turn, each reading the codes
+// again (from cache).
+//
+// The codes, scales and activations of the next block are in flight while a block
+// is multiplied.  Activations are loaded as they lie, 256 bytes of a row by 16
+// lanes (fp32: 512 by 32), and cross to the lanes that need them through LDS of
+// the wave's own, in 16-byte units whose place in a row is XORed with the row so
+// that 16 rows meet distinct banks.  Loaded by those lanes instead, an instruction
+// touched 16 rows for 64 bytes each, rows that lie a power of two apart fell on
+// one cache channel, and 16 rows cost more than the codes (8192 x 8192 f16).
+template <int DT, int MT>
+struct Q4Rows {
     typedef typename ElemOf<DT>::type T;
-    constexpr int E = (int)sizeof(T);
-    constexpr int PIECES = DT == DT_F32 ? 2 : 1;    // 16-byte loads for a lane's eight k of a row
-    constexpr int PER = 16 / E;
-    extern __shared__ f32x4 q4_lds[];                // [waves][MT][64]
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // the same in every lane of a wave
-    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-    const int g = blockIdx.y, tile = blockIdx.x;
-    const RowSpan span = rows_of(p.offsets, g, p.experts, p.rows);
-    const int n0 = tile * kQ4N + 4 * (lane / 16);
-    const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
-    const bool dead = g == p.experts || p.K == 0;    // zeros
-    const int64_t at = (int64_t)g * p.n_tiles + tile;
-    const u32x4 *codes = reinterpret_cast<const u32x4 *>(p.codes) + at * p.k_blocks * 64 + lane;
-    const T *scales = reinterpret_cast<const T *>(p.scales) + at * p.groups * kQ4N + 4 * (lane / 16);
-    for (int r0 = span.lo; r0 < span.hi; r0 += 16 * MT) {
-        f32x4 acc[MT];
+    static constexpr int E = (int)sizeof(T), PER = 16 / E;
+    static constexpr int ROW = kQ4K / PER;             // 16-byte units of a block's row: 16 or 32
+    static constexpr int RPI = 64 / ROW;               // rows of a load: 4 or 2
+    static constexpr int LOADS = 16 / RPI;             // loads of a row tile
+    static constexpr int PIECES = DT == DT_F32 ? 2 : 1;    // units of a lane's eight k
+    static constexpr int LDS = MT * 16 * ROW;          // units of a wave's region
+
+    rsrc_t ra;
+    int voff, lda, rows, K, lane;
+    u32x4 *lds;
+    __device__ __forceinline__ void init(const char *A, int64_t lda_, int rows_, int K_, int lane_, u32x4 *lds_) {
+        ra = make_rsrc(A);
+        lda = (int)lda_;
+        rows = rows_;
+        K = K_;
+        lane = lane_;
+        lds = lds_;
+        voff = (lane / ROW * lda + lane % ROW * PER) * E;
+        // rows that are never loaded
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
-        if (!dead) {
-            const int rows = span.hi - r0 < 16 * MT ? span.hi - r0 : 16 * MT;
-            const rsrc_t ra = make_rsrc(p.A + (int64_t)r0 * p.lda * E);
-            int voff[MT];
+        for (int i = 0; i < MT * LOADS; ++i)
+            if (i * RPI >= rows) lds[i * 64 + lane] = u32x4{0, 0, 0, 0};
+    }
+    // TAIL: K ends in the block (past it +0, so that a NaN behind a row's end meets no weight)
+    template <bool TAIL>
+    __device__ __forceinline__ void load(int kb, int i, u32x4 (&a)[LOADS]) const {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int r = 16 * i + lane % 16;
-                voff[i] = r < rows ? (int)(r * (int)p.lda + 8 * (lane / 16)) * E : kOutOfRange;
+        for (int d = 0; d < LOADS; ++d) {
+            const int r0 = 16 * i + RPI * d;
+            if (r0 >= rows) continue;
+            const int soff = (r0 * lda + kb * kQ4K) * E;
+            const bool in = r0 + lane / ROW < rows;
+            if constexpr (TAIL) {
+                const int left = K - (kb * kQ4K + lane % ROW * PER);
+                a[d] = bload16_n<E>(ra, voff, soff, in && left > 0 ? left : 0);
+            } else {
+                a[d] = bload16(ra, in ? voff : kOutOfRange, soff);
             }
-            // one block of 128 k; TAIL: K ends in it (A past K is +0, so that a NaN
-            // behind a row's end meets no weight)
-            auto block = [&](int kb, auto tail) {
-                constexpr bool TAIL = decltype(tail)::value;
-                const u32x4 w = codes[(int64_t)kb * 64];
-                f32x4 sum[MT];
+        }
+    }
+    __device__ __forceinline__ void stage(int i, const u32x4 (&a)[LOADS]) const {
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int k0 = kb * kQ4K + 32 * s;
-                    u32x4 a[MT][PIECES];
+        for (int d = 0; d < LOADS; ++d) {
+            const int r = RPI * d + lane / ROW;
+            if (16 * i + RPI * d < rows) lds[(16 * i + r) * ROW + (lane % ROW ^ r)] = a[d];
+        }
+    }
+    // unit h of this lane's eight k of step s, row lane % 16 of tile i
+    __device__ __forceinline__ u32x4 read(int i, int s, int h) const {
+        const int r = lane % 16, unit = 4 * PIECES * s + PIECES * (lane / 16) + h;
+        return lds[(16 * i + r) * ROW + (unit ^ r)];
+    }
+};
+
+template <int DT, int GROUP, int MT, int NT>
+struct Q4Block {
+    using Rows = Q4Rows<DT, MT>;
+    typedef typename ElemOf<DT>::type T;
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    static constexpr int SCALES = kQ4K / GROUP;
+    // held ahead where that is at most 64 registers a block
+    static constexpr bool A_AHEAD = MT * Rows::LOADS <= 8;
+    u32x4 w[NT];
+    t4 q[NT][SCALES];           // loaded together
+    u32x4 a[A_AHEAD ? MT : 1][Rows::LOADS];
+
+    template <bool TAIL>
+    __device__ __forceinline__ void load(const u32x4 *const (&codes)[NT], const T *const (&scales)[NT], const Rows &rows,
+                                         int kb) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            w[t] = codes[t][(int64_t)kb * 64];
+            const t4 *from = reinterpret_cast<const t4 *>(scales[t] + (int64_t)kb * (SCALES * kQ4N));
+#pragma unroll
+            for (int g = 0; g < SCALES; ++g) q[t][g] = from[g];
+        }
+        if constexpr (A_AHEAD) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) rows.template load<TAIL>(kb, i, a[i]);
+        }
+    }
+    template <bool TAIL>
+    __device__ __forceinline__ void multiply(const Rows &rows, int kb, f32x4 (&acc)[NT][MT]) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            if constexpr (!A_AHEAD) rows.template load<TAIL>(kb, i, a[0]);
+            rows.stage(i, a[A_AHEAD ? i : 0]);
+        }
+        f32x4 sum[NT][MT];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            u32x4 x[MT][Rows::PIECES];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < Rows::PIECES; ++h) x[i][h] = rows.read(i, s, h);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (32 * s % GROUP == 0) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) sum[t][i] = f32x4{0, 0, 0, 0};
+                }
+                if constexpr (DT == DT_F32) {
+                    float f[8];
+                    q4_floats(w[t][s], f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            const uint32_t y = x[i][e / 4][e % 4];
+                            sum[t][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[e], __builtin_bit_cast(float, y), sum[t][i],
+                                                                             0, 0, 0);
+                        }
+                } else {
+                    const u32x4 b = q4_operand<DT>(w[t][s]);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) mfma_chunk<DT>(b, x[i][0], sum[t][i]);
+                }
+                if ((32 * s + 32) % GROUP == 0) {
+                    const t4 c = q[t][32 * s / GROUP];
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
-                        for (int h = 0; h < PIECES; ++h) {
-                            if constexpr (TAIL) {
-                                const int left = p.K - (k0 + 8 * (lane / 16) + PER * h);
-                                a[i][h] = bload16_n<E>(ra, voff[i] + 16 * h, k0 * E,
-                                                       left < 0 || voff[i] == kOutOfRange ? 0 : left);
-                            } else {
-                                a[i][h] = bload16(ra, voff[i] + 16 * h, k0 * E);
-                            }
-                        }
-                    if (32 * s % GROUP == 0) {
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) sum[i] = f32x4{0, 0, 0, 0};
-                    }
-                    if constexpr (DT == DT_F32) {
-                        float f[8];
-                        q4_floats(w[s], f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-#pragma unroll
-                            for (int i = 0; i < MT; ++i) {
-                                const uint32_t x = a[i][e / 4][e % 4];
-                                sum[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[e], __builtin_bit_cast(float, x), sum[i],
-                                                                              0, 0, 0);
-                            }
-                    } else {
-                        const u32x4 b = q4_operand<DT>(w[s]);
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) mfma_chunk<DT>(b, a[i][0], sum[i]);
-                    }
-                    if ((32 * s + 32) % GROUP == 0) {
-                        typedef T t4 __attribute__((ext_vector_type(4)));
-                        const t4 q = *reinterpret_cast<const t4 *>(scales + (int64_t)(k0 / GROUP) * kQ4N);
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                acc[i][v] = __builtin_fmaf((float)q[v], Q4Unit<DT>::value * sum[i][v], acc[i][v]);
-                    }
+                        for (int v = 0; v < 4; ++v)
+                            acc[t][i][v] = __builtin_fmaf((float)c[v], sum[t][i][v], acc[t][i][v]);
                 }
-            };
+            }
+        }
+    }
+};
+
+// Waves of a workgroup at most: their LDS regions are 64 KiB together.
+template <int DT, int MT>
+constexpr int q4_waves() {
+    const int fit = 65536 / (Q4Rows<DT, MT>::LDS * 16);
+    return fit < 8 ? fit : 8;
+}
+
+template <int DT, int GROUP, int MT, int NT>
+__global__ __launch_bounds__(512) void q4_kernel(Q4Params p) {
+    using Block = Q4Block<DT, GROUP, MT, NT>;
+    using Rows = Q4Rows<DT, MT>;
+    typedef typename Block::T T;
+    extern __shared__ u32x4 q4_lds[];                // [waves][Rows::LDS], then the sums [waves][NT * MT][64]
+    static_assert(Rows::LDS >= NT * MT * 64, "the sums fit the waves' regions");
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // the same in every lane of a wave
+    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
+    const int g = blockIdx.y, tile = blockIdx.x * NT;
+    const RowSpan span = rows_of(p.offsets, g, p.experts, p.rows);
+    const bool dead = g == p.experts || p.K == 0;    // zeros
+    const int n0 = tile * kQ4N + 4 * (lane / 16);
+    const u32x4 *codes[NT];
+    const T *scales[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        // past the last tile: the last one again, for columns that are not stored
+        const int64_t at = (int64_t)g * p.n_tiles + (tile + t < p.n_tiles ? tile + t : p.n_tiles - 1);
+        codes[t] = reinterpret_cast<const u32x4 *>(p.codes) + at * p.k_blocks * 64 + lane;
+        scales[t] = reinterpret_cast<const T *>(p.scales) + at * p.groups * kQ4N + 4 * (kQ4K / GROUP) * (lane / 16);
+    }
+    for (int r0 = span.lo + 16 * MT * (int)blockIdx.z; r0 < span.hi; r0 += 16 * MT * (int)gridDim.z) {
+        f32x4 acc[NT][MT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[t][i] = f32x4{0, 0, 0, 0};
+        if (!dead) {
+            Rows rows;
+            const int count = __builtin_amdgcn_readfirstlane(span.hi - r0 < 16 * MT ? span.hi - r0 : 16 * MT);
+            rows.init(p.A + (int64_t)r0 * p.lda * Rows::E, p.lda, count, p.K, lane, q4_lds + wave * Rows::LDS);
             const int full = p.K / kQ4K;
             int kb = wave;
-            for (; kb < full; kb += waves) block(kb, std::false_type{});
-            if (kb < p.k_blocks) block(kb, std::true_type{});
+            if (kb < full) {
+                Block b, n;
+                b.template load<false>(codes, scales, rows, kb);
+                for (;;) {
+                    if (kb + waves < full) n.template load<false>(codes, scales, rows, kb + waves);
+                    b.template multiply<false>(rows, kb, acc);
+                    kb += waves;
+                    if (kb >= full) break;
+                    if (kb + waves < full) b.template load<false>(codes, scales, rows, kb + waves);
+                    n.template multiply<false>(rows, kb, acc);
+                    kb += waves;
+                    if (kb >= full) break;
+                }
+            }
+            if (kb < p.k_blocks) {
+                Block b;
+                b.template load<true>(codes, scales, rows, kb);
+                b.template multiply<true>(rows, kb, acc);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) q4_lds[(wave * MT + i) * 64 + lane] = acc[i];
         __syncthreads();
-        for (int i = wave; i < MT; i += waves) {
-            f32x4 v = q4_lds[i * 64 + lane];
-            for (int w = 1; w < waves; ++w) v += q4_lds[(w * MT + i) * 64 + lane];
-            const int r = r0 + 16 * i + lane % 16;
-            if (r < span.hi && n0 < p.N) store4<DT>(p.C, (int64_t)r * p.ldc + n0, p.N - n0, p.c_f32, wide, v);
+        f32x4 *sums = reinterpret_cast<f32x4 *>(q4_lds);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) sums[((wave * NT + t) * MT + i) * 64 + lane] = acc[t][i];
+        __syncthreads();
+        for (int q = wave; q < NT * MT; q += waves) {
+            f32x4 v = sums[q * 64 + lane];
+            for (int w = 1; w < waves; ++w) v += sums[(w * NT * MT + q) * 64 + lane];
+            const int r = r0 + 16 * (q % MT) + lane % 16, n = n0 + 16 * (q / MT);
+            v *= Q4Unit<DT>::value;
+            if (r < span.hi && n < p.N) store4<DT>(p.C, (int64_t)r * p.ldc + n, p.N - n, p.c_f32, wide, v);
         }
         __syncthreads();
     }
