@@ -172,6 +172,38 @@ def test_exchange(dt, tokens, top_k, experts, cols, dropped, pad):
     ref.check(d_w.get(), want_w, cols, abs_w, "f32")
 
 
+@pytest.mark.parametrize("dt,cols", [("bf16", 2048), ("f32", 1023)])
+def test_exchange_of_much_data(dt, cols):
+    """More bytes than the caches hold (results are then stored past them); the same on the GPU in 64 bits."""
+    T, k, E = 6001, 3, 8
+    ids = routing(T, k, E, 0.1, 5).cuda()
+    n = T * k
+    offsets, entry, row = (torch.empty(m, dtype=torch.int32, device="cuda") for m in (E + 1, n, n))
+    ws = torch.empty(tg.tile_gemm_expert_sort_workspace_size(T, k, E) // 4, dtype=torch.int32, device="cuda")
+    tg.tile_gemm_expert_sort(T, k, E, ids, k, offsets, entry, row, workspace=ws)
+    x, y, d = (normal(m, cols, dtype=dt, seed=i).cuda() for i, m in enumerate((T, n, T)))
+    w = torch.rand(T, k, generator=torch.Generator().manual_seed(1)).cuda()
+    rows, out, d_y, d_w = Out(n, cols, TYPES[dt]), Out(T, cols, TYPES[dt]), Out(n, cols, TYPES[dt]), Out(T, k, torch.float32)
+    tg.tile_gemm_expert_gather(T, k, cols, dt, x, cols, row, rows.t, cols)
+    tg.tile_gemm_expert_combine(T, k, cols, dt, y, cols, row, w, k, out.t, cols)
+    tg.tile_gemm_expert_combine_grad(T, k, cols, dt, d, cols, y, cols, row, w, k, d_y.t, cols, d_w.t, k)
+    at = row.long().reshape(T, k)
+    has = at >= 0
+    at = torch.where(has, at, ~at)
+    token = torch.arange(T, device="cuda")[:, None].expand(T, k)
+    want = torch.zeros(n, cols, dtype=x.dtype, device="cuda")
+    want[at[has]] = x[token[has]]
+    assert torch.equal(rows.get(), want.cpu())
+    f = torch.where(has, w, 0).double()
+    picked = torch.where(has[..., None], y[at].double(), 0)
+    ref.check(out.get(), (picked * f[..., None]).sum(1).cpu(), k, (picked.abs() * f[..., None]).sum(1).cpu(), dt)
+    want = torch.zeros(n, cols, dtype=torch.float64, device="cuda")
+    want[at.reshape(-1)] = (d.double()[:, None, :] * f[..., None]).reshape(n, cols)
+    ref.check(d_y.get(), want.cpu(), 1, want.abs().cpu(), dt)
+    prod = picked * d.double()[:, None, :]
+    ref.check(d_w.get(), prod.sum(2).cpu(), cols, prod.abs().sum(2).cpu(), "f32")
+
+
 def test_combine_gradient_against_differences():
     """<d_out, combine(w, y)> is linear in w and in y: a central difference of any step is its gradient."""
     T, k, D = 12, 3, 40
@@ -315,6 +347,30 @@ def test_products_of_many_tiles(dt, experts, rows, spare, N, K, pad, form):
         tg.tile_gemm_grouped(experts, total, N, K, dt, Ad, lda, Bd, ldb, B.shape[1] * ldb, C.t, C.ld, off,
                              transposed=int(form == "nt"))
     assert torch.equal(C.get().double(), want)
+
+
+@pytest.mark.parametrize("dt,out", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+def test_products_larger_than_the_caches(dt, out):
+    """Results stored past the caches, whole numbers against products in 64 bits on the GPU."""
+    E, R, N, K = 3, 17000, 8192, 64
+    offsets = [0, 5000, 5100, R]
+    off = torch.tensor(offsets, dtype=torch.int32).cuda()
+    A, B = ints(R, K, dtype=dt, low=-1, high=2, seed=1).cuda(), ints(E, K, N, dtype=dt, low=-1, high=2, seed=2).cuda()
+    C = torch.full((R, N), float("nan"), dtype=TYPES[out], device="cuda")
+    tg.tile_gemm_grouped(E, R, N, K, dt, A, K, B, N, K * N, C, N, off, c_dtype=out)
+    for g in range(E):
+        lo, hi = offsets[g], offsets[g + 1]
+        assert torch.equal(C[lo:hi].double(), A[lo:hi].double() @ B[g].double())
+    C = torch.full((40, 1200, 3000), float("nan"), dtype=torch.float32, device="cuda")
+    sizes = [13 * (g % 5) for g in range(40)]
+    offsets = offsets_of(sizes)
+    R = offsets[-1]
+    A, D = ints(R, 1200, dtype=dt, low=-1, high=2, seed=3).cuda(), ints(R, 3000, dtype=dt, low=-1, high=2, seed=4).cuda()
+    tg.tile_gemm_grouped_wgrad(40, R, 1200, 3000, dt, A, 1200, D, 3000, C, 3000, 1200 * 3000,
+                               torch.tensor(offsets, dtype=torch.int32).cuda())
+    for g in range(40):
+        lo, hi = offsets[g], offsets[g + 1]
+        assert torch.equal(C[g].double(), A[lo:hi].double().t().contiguous() @ D[lo:hi].double())
 
 
 def test_grouped_nan_stays_in_its_row_and_column():

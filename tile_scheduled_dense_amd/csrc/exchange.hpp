@@ -33,10 +33,13 @@ struct Row {
             if (e < left) v[e] = row[c * PER + e];
         return __builtin_bit_cast(u32x4, v);
     }
+    // PAST: with the non-temporal hint
+    template <bool PAST = false>
     __device__ __forceinline__ static void store(T *row, int64_t c, int64_t cols, u32x4 x) {
         const int64_t left = cols - c * PER;
         if (left >= PER) {
-            *reinterpret_cast<u32x4_any *>(row + c * PER) = x;
+            if constexpr (PAST) __builtin_nontemporal_store(x, reinterpret_cast<u32x4_any *>(row + c * PER));
+            else *reinterpret_cast<u32x4_any *>(row + c * PER) = x;
             return;
         }
         const vec v = __builtin_bit_cast(vec, x);
@@ -63,12 +66,14 @@ struct Row {
 // takes 64 consecutive entries at a time; the lanes that share a key find each
 // other with one ballot per key bit, a lane's rank among them is a population
 // count, and the wave's own histogram in LDS carries the ranks from one 64 to
-// the next: no atomics, so the order is the entries'.  Waves of a block are
-// joined by a scan over their histograms; blocks by the counts of
-// sort_count_kernel, which every block of sort_place_kernel sums for itself (at
-// most kSortBlocks counts a key, one load of a lane each).
+// the next, so the order is the entries'.  Waves of a block are joined by a scan
+// over their histograms.  Blocks are joined by the counts of sort_count_kernel,
+// which every block of sort_place_kernel sums for itself, one load of a lane each.
+// No atomics.  (Every block counting all entries for itself, in LDS atomics and one
+// launch, took 19 us for 16384 entries of 8 experts, against 11 in two launches.)
 // Bound by latency: 16384 entries are 64 KiB.
 constexpr int kSortBlocks = 64;
+constexpr int kSortOnce = 4;       // steps a wave at most for one block to take them all
 // waves of a sorting block: their histograms are waves * (experts + 1) ints of LDS, 32 KiB at most
 inline int sort_waves(int64_t experts) { return experts < 512 ? 16 : 4; }
 
@@ -76,21 +81,13 @@ struct SortShape {
     int waves, iters;      // a wave takes iters * 64 consecutive entries
     int64_t blocks;
 };
-// One block as long as its waves take at most kSortOnce steps each (one launch
-// in place of two), else at most kSortBlocks blocks.
-constexpr int kSortOnce = 4;
 inline SortShape sort_shape(int64_t n, int64_t experts) {
     SortShape s;
     s.waves = sort_waves(experts);
     const int64_t step = s.waves * 64;
     const int64_t steps = (n + step - 1) / step;
-    if (steps <= kSortOnce) {
-        s.iters = steps > 1 ? (int)steps : 1;
-        s.blocks = 1;
-        return s;
-    }
-    s.iters = (int)((steps + kSortBlocks - 1) / kSortBlocks);
-    s.blocks = (n + step * s.iters - 1) / (step * s.iters);
+    s.iters = (int)(steps <= kSortOnce ? (steps > 1 ? steps : 1) : (steps + kSortBlocks - 1) / kSortBlocks);
+    s.blocks = n > step * s.iters ? (n + step * s.iters - 1) / (step * s.iters) : 1;
     return s;
 }
 
@@ -102,8 +99,12 @@ struct SortParams {
 };
 
 __device__ __forceinline__ int sort_key(const SortParams &p, int entry) {
-    const int t = entry / p.top_k;
-    const int id = p.ids[(int64_t)t * p.ld_ids + (entry - t * p.top_k)];
+    int64_t at = entry;
+    if (p.ld_ids != p.top_k) {
+        const int t = entry / p.top_k;
+        at = (int64_t)t * p.ld_ids + (entry - t * p.top_k);
+    }
+    const int id = p.ids[at];
     return (uint32_t)id < (uint32_t)p.experts ? id : p.experts;
 }
 
@@ -117,16 +118,15 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits, uint64_t active)
     return m;
 }
 
-// the wave's histogram of its entries (leaders add; one key has one leader a step)
-__device__ __forceinline__ void sort_histogram(const SortParams &p, int first, int lane, volatile int *hist) {
-    for (int i = 0; i < p.iters; ++i) {
-        const int entry = first + i * 64 + lane;
-        const bool in = entry < p.n;
-        const int key = in ? sort_key(p, entry) : p.experts;
-        const uint64_t m = same_key(key, p.bits, __ballot(in));
-        if (in && __builtin_ctzll(m) == lane) hist[key] = hist[key] + __popcll(m);
-        __builtin_amdgcn_wave_barrier();
-    }
+// One step of a wave: 64 entries into its histogram (a key has one leader among
+// them); returns this lane's rank among the wave's entries of its key so far.
+__device__ __forceinline__ int sort_step(int key, bool in, int bits, int lane, volatile int *hist) {
+    const uint64_t m = same_key(key, bits, __ballot(in));
+    const int seen = in ? hist[key] : 0;
+    __builtin_amdgcn_wave_barrier();
+    if (in && __builtin_ctzll(m) == lane) hist[key] = seen + __popcll(m);
+    __builtin_amdgcn_wave_barrier();
+    return seen + __popcll(m & ((1ull << lane) - 1));
 }
 
 static __global__ __launch_bounds__(1024) void sort_count_kernel(SortParams p) {
@@ -134,7 +134,12 @@ static __global__ __launch_bounds__(1024) void sort_count_kernel(SortParams p) {
     const int keys = p.experts + 1, wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = blockDim.x >> 6;
     for (int i = threadIdx.x; i < waves * keys; i += blockDim.x) sort_lds[i] = 0;
     __syncthreads();
-    sort_histogram(p, (blockIdx.x * waves + wave) * p.iters * 64, lane, sort_lds + wave * keys);
+    const int first = (blockIdx.x * waves + wave) * p.iters * 64;
+    for (int i = 0; i < p.iters; ++i) {
+        const int entry = first + i * 64 + lane;
+        const bool in = entry < p.n;
+        sort_step(in ? sort_key(p, entry) : p.experts, in, p.bits, lane, sort_lds + wave * keys);
+    }
     __syncthreads();
     for (int k = threadIdx.x; k < keys; k += blockDim.x) {
         int sum = 0;
@@ -143,6 +148,9 @@ static __global__ __launch_bounds__(1024) void sort_count_kernel(SortParams p) {
     }
 }
 
+// KEPT: a wave's steps are at most that many, their keys and ranks kept in
+// registers (0: any number, found again for the second pass).
+template <int KEPT>
 static __global__ __launch_bounds__(1024) void sort_place_kernel(SortParams p) {
     extern __shared__ int sort_lds[];
     __shared__ int wave_sum[16];
@@ -150,10 +158,28 @@ static __global__ __launch_bounds__(1024) void sort_place_kernel(SortParams p) {
     int *hist = sort_lds;                     // [waves][keys]
     int *total = sort_lds + waves * keys;     // [keys]: entries of the key, then its first row
     int *before = total + keys;               // [keys]: those in earlier blocks
-    for (int i = threadIdx.x; i < waves * keys; i += blockDim.x) hist[i] = 0;
+    for (int i = threadIdx.x; i < (waves + 2) * keys; i += blockDim.x) hist[i] = 0;
     __syncthreads();
     const int first = (blockIdx.x * waves + wave) * p.iters * 64;
-    sort_histogram(p, first, lane, hist + wave * keys);
+    volatile int *mine_hist = hist + wave * keys;
+    int kept_key[KEPT ? KEPT : 1], kept_rank[KEPT ? KEPT : 1];
+    if constexpr (KEPT > 0) {
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i) {
+            const int entry = first + i * 64 + lane;
+            kept_key[i] = i < p.iters && entry < p.n ? sort_key(p, entry) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i)
+            if (i < p.iters)
+                kept_rank[i] = sort_step(kept_key[i] < 0 ? p.experts : kept_key[i], kept_key[i] >= 0, p.bits, lane, mine_hist);
+    } else {
+        for (int i = 0; i < p.iters; ++i) {
+            const int entry = first + i * 64 + lane;
+            const bool in = entry < p.n;
+            sort_step(in ? sort_key(p, entry) : p.experts, in, p.bits, lane, mine_hist);
+        }
+    }
     if (p.blocks > 1) {
         // groups of `span` lanes take a key each, a lane a block's count
         int span = 1;
@@ -162,7 +188,7 @@ static __global__ __launch_bounds__(1024) void sort_place_kernel(SortParams p) {
         for (int k0 = wave * per; k0 < keys; k0 += waves * per) {
             const int k = k0 + sub;
             int c = 0;
-            if (k < keys && blk < p.blocks) c = p.counts[k * p.blocks + blk];
+            if (k < keys && blk < p.blocks && blk != (int)blockIdx.x) c = p.counts[k * p.blocks + blk];
             int b = blk < (int)blockIdx.x ? c : 0;
             for (int d = 1; d < span; d *= 2) {
                 c += __shfl_xor(c, d);
@@ -175,7 +201,7 @@ static __global__ __launch_bounds__(1024) void sort_place_kernel(SortParams p) {
         }
     }
     __syncthreads();
-    // a key's waves in order: exclusive sums over the histograms
+    // a key's waves in order: exclusive sums over the histograms; total: this block's too
     for (int k = threadIdx.x; k < keys; k += blockDim.x) {
         int sum = 0;
         for (int w = 0; w < waves; ++w) {
@@ -183,10 +209,7 @@ static __global__ __launch_bounds__(1024) void sort_place_kernel(SortParams p) {
             hist[w * keys + k] = sum;
             sum += c;
         }
-        if (p.blocks == 1) {
-            total[k] = sum;
-            before[k] = 0;
-        }
+        total[k] += sum;
     }
     __syncthreads();
     // the first row of every key: an exclusive sum over the totals, `share` keys a thread
@@ -215,36 +238,51 @@ static __global__ __launch_bounds__(1024) void sort_place_kernel(SortParams p) {
         }
     }
     __syncthreads();
-    volatile int *mine_hist = hist + wave * keys;
-    for (int i = 0; i < p.iters; ++i) {
-        const int entry = first + i * 64 + lane;
-        const bool in = entry < p.n;
-        const int key = in ? sort_key(p, entry) : p.experts;
-        const uint64_t m = same_key(key, p.bits, __ballot(in));
-        const int seen = in ? mine_hist[key] : 0;
-        __builtin_amdgcn_wave_barrier();
-        if (in) {
-            const int row = total[key] + before[key] + seen + __popcll(m & ((1ull << lane) - 1));
-            p.entry_of_row[row] = key < p.experts ? entry : ~entry;
-            p.row_of_entry[entry] = key < p.experts ? row : ~row;
-            if (__builtin_ctzll(m) == lane) mine_hist[key] = seen + __popcll(m);
+    auto place = [&](int entry, int key, int rank) {
+        const int row = total[key] + before[key] + rank;
+        p.entry_of_row[row] = key < p.experts ? entry : ~entry;
+        p.row_of_entry[entry] = key < p.experts ? row : ~row;
+    };
+    if constexpr (KEPT > 0) {
+#pragma unroll
+        for (int i = 0; i < KEPT; ++i)
+            if (kept_key[i] >= 0)
+                place(first + i * 64 + lane, kept_key[i], mine_hist[kept_key[i]] + kept_rank[i]);
+    } else {
+        for (int i = 0; i < p.iters; ++i) {
+            const int entry = first + i * 64 + lane;
+            const bool in = entry < p.n;
+            const int key = in ? sort_key(p, entry) : p.experts;
+            const int rank = sort_step(key, in, p.bits, lane, mine_hist);   // on from the earlier waves'
+            if (in) place(entry, key, rank);
         }
-        __builtin_amdgcn_wave_barrier();
     }
 }
 
 // ---- rows ---------------------------------------------------------------------------
 // `group` threads (64, 128 or 256) take a token's row, a chunk each at a time,
-// and 256 / group tokens fill a workgroup.
+// and 256 / group tokens fill a workgroup.  A wave has one token: its table
+// entries and weights are scalar loads.
+// whether a call that moves so many bytes stores past the caches (gather_kernel)
+inline bool store_past(int64_t bytes) { return bytes > (int64_t(64) << 20); }
 inline int row_group(int64_t chunks) { return chunks > 128 ? 256 : (chunks > 64 ? 128 : 64); }
+__device__ __forceinline__ int token_of(int group) {
+    return __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (256 / group) + threadIdx.x / group));
+}
 
-template <int DT>
+// PAST: results are stored past the caches, where a call moves more than 64 MiB:
+// lines that one call leaves dirty in them are written back during the next call's
+// reads.  A pass of gather, combine, its gradient and the gather's gradient, 8192 x
+// 2048 bf16 of 2 choices, takes 113 us without the hint and 99 with it; 1999 x 1001
+// fp32 of 8 choices 96 and 87 (where the gather alone, its rows off 16 bytes, takes 18
+// in place of 15).  The hint on loads too: 106.
+template <int DT, bool PAST>
 __global__ __launch_bounds__(256) void gather_kernel(const typename ElemOf<DT>::type *__restrict__ x, int64_t ldx,
                                                      const int32_t *__restrict__ row_of_entry,
                                                      typename ElemOf<DT>::type *__restrict__ rows, int64_t ldr,
                                                      int tokens, int top_k, int64_t cols, int group) {
     using R = Row<DT>;
-    const int t = blockIdx.x * (256 / group) + threadIdx.x / group;
+    const int t = token_of(group);
     if (t >= tokens) return;
     const int n = tokens * top_k;
     const int32_t *row = row_of_entry + (int64_t)t * top_k;
@@ -253,31 +291,30 @@ __global__ __launch_bounds__(256) void gather_kernel(const typename ElemOf<DT>::
         const u32x4 v = R::load(x + (int64_t)t * ldx, c, cols);
         for (int j = 0; j < top_k; ++j) {
             const int r = row[j], at = r < 0 ? ~r : r;
-            if (at < n) R::store(rows + (int64_t)at * ldr, c, cols, r < 0 ? u32x4{0, 0, 0, 0} : v);
+            if (at < n) R::template store<PAST>(rows + (int64_t)at * ldr, c, cols, r < 0 ? u32x4{0, 0, 0, 0} : v);
         }
     }
 }
 
-// JB choices of a token at a time, their loads in flight together.  A choice
-// without an expert loads row 0 in its place (in cache after the first) and is
-// left out of the sum by selection, so that what lies there, a NaN say, goes
-// nowhere.
-template <int DT, int JB>
+// JB choices of a token and U chunks at a time, their loads in flight together.  A
+// choice without an expert loads row 0 in its place (in cache after the first) and is
+// left out of the sum by selection, so that what lies there, a NaN say, goes nowhere.
+template <int DT, int JB, int U, bool PAST>
 __global__ __launch_bounds__(256) void combine_kernel(const typename ElemOf<DT>::type *__restrict__ y, int64_t ldy,
                                                       const int32_t *__restrict__ row_of_entry,
                                                       const float *__restrict__ weights, int64_t ld_w,
                                                       typename ElemOf<DT>::type *__restrict__ out, int64_t ldo,
                                                       int tokens, int top_k, int64_t cols, int group) {
     using R = Row<DT>;
-    const int t = blockIdx.x * (256 / group) + threadIdx.x / group;
+    const int t = token_of(group);
     if (t >= tokens) return;
     const int n = tokens * top_k;
     const int32_t *row = row_of_entry + (int64_t)t * top_k;
     const int64_t chunks = (cols + R::PER - 1) / R::PER;
-    for (int64_t c = threadIdx.x % group; c < chunks; c += group) {
-        float sum[R::PER] = {};
+    for (int64_t c = threadIdx.x % group; c < chunks; c += U * group) {
+        float sum[U][R::PER] = {};
         for (int j0 = 0; j0 < top_k; j0 += JB) {
-            u32x4 v[JB];
+            u32x4 v[JB][U];
             float w[JB];
             bool has[JB];
 #pragma unroll
@@ -285,22 +322,32 @@ __global__ __launch_bounds__(256) void combine_kernel(const typename ElemOf<DT>:
                 const int r = j0 + j < top_k ? row[j0 + j] : -1;
                 has[j] = (uint32_t)r < (uint32_t)n;
                 w[j] = has[j] && weights ? weights[(int64_t)t * ld_w + j0 + j] : 1.0f;
-                v[j] = R::load(y + (has[j] ? (int64_t)r * ldy : 0), c, cols);
+                const typename ElemOf<DT>::type *from = y + (has[j] ? (int64_t)r * ldy : 0);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (u == 0 || c + u * group < chunks) v[j][u] = R::load(from, c + u * group, cols);
             }
 #pragma unroll
             for (int j = 0; j < JB; ++j) {
-                float f[R::PER];
-                R::widen(v[j], f);
+                if (!has[j]) continue;
 #pragma unroll
-                for (int e = 0; e < R::PER; ++e) sum[e] = has[j] ? __builtin_fmaf(w[j], f[e], sum[e]) : sum[e];
+                for (int u = 0; u < U; ++u) {
+                    float f[R::PER];
+                    R::widen(v[j][u], f);
+#pragma unroll
+                    for (int e = 0; e < R::PER; ++e) sum[u][e] = __builtin_fmaf(w[j], f[e], sum[u][e]);
+                }
             }
         }
-        R::store(out + (int64_t)t * ldo, c, cols, R::narrow(sum));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u == 0 || c + u * group < chunks)
+                R::template store<PAST>(out + (int64_t)t * ldo, c + u * group, cols, R::narrow(sum[u]));
     }
 }
 
 // One wave a token: the dot products are summed over its lanes without LDS.
-template <int DT, int JB>
+template <int DT, int JB, bool PAST>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const typename ElemOf<DT>::type *__restrict__ d_out,
                                                            int64_t ldo,
                                                            const typename ElemOf<DT>::type *__restrict__ y,
@@ -310,7 +357,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const typename ElemOf
                                                            float *__restrict__ d_w, int64_t ld_dw, int tokens,
                                                            int top_k, int64_t cols) {
     using R = Row<DT>;
-    const int t = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x & 63;
+    const int t = token_of(64), lane = threadIdx.x & 63;
     if (t >= tokens) return;
     const int n = tokens * top_k;
     const int32_t *row = row_of_entry + (int64_t)t * top_k;
@@ -342,7 +389,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const typename ElemOf
                     dot[j] = has[j] ? __builtin_fmaf(g[e], f[e], dot[j]) : 0.0f;
                     d[e] = has[j] ? w[j] * g[e] : 0.0f;
                 }
-                if (at[j] >= 0) R::store(d_y + (int64_t)at[j] * ldd, c, cols, R::narrow(d));
+                if (at[j] >= 0) R::template store<PAST>(d_y + (int64_t)at[j] * ldd, c, cols, R::narrow(d));
             }
         }
 #pragma unroll

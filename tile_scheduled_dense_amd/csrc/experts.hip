@@ -81,7 +81,10 @@ tg_status sort(int64_t tokens, int64_t top_k, int64_t experts, const int32_t *id
         st = launched();
         if (st != TG_OK) return st;
     }
-    hipLaunchKernelGGL(sort_place_kernel, grid, block, (shape.waves + 2) * keys * 4, s, p);
+    const unsigned lds = (shape.waves + 2) * keys * 4;
+    if (shape.iters == 1) hipLaunchKernelGGL(sort_place_kernel<1>, grid, block, lds, s, p);
+    else if (shape.iters <= kSortOnce) hipLaunchKernelGGL(sort_place_kernel<kSortOnce>, grid, block, lds, s, p);
+    else hipLaunchKernelGGL(sort_place_kernel<0>, grid, block, lds, s, p);
     return launched();
 }
 
@@ -109,11 +112,15 @@ tg_status gather(int64_t tokens, int64_t top_k, int64_t cols, tg_dtype dtype, co
     const int group = row_group(cdiv(cols * esz, 16));
     const dim3 grid((unsigned)cdiv(tokens, 256 / group));
     hipStream_t s = static_cast<hipStream_t>(stream);
-#define TG_GATHER(DT)                                                                                              \
-    hipLaunchKernelGGL((gather_kernel<DT>), grid, dim3(256), 0, s, static_cast<const ElemOf<DT>::type *>(x), ldx,   \
+    const bool past = store_past((n + tokens) * cols * esz);
+#define TG_GATHER(DT, PAST)                                                                                        \
+    hipLaunchKernelGGL((gather_kernel<DT, PAST>), grid, dim3(256), 0, s, static_cast<const ElemOf<DT>::type *>(x), ldx, \
                        row_of_entry, static_cast<ElemOf<DT>::type *>(rows), ldr, (int)tokens, (int)top_k, cols, group)
-    if (dtype == TG_F32) TG_GATHER(DT_F32);
-    else TG_GATHER(DT_F16);      // the bytes are moved as they are
+    // the bytes are moved as they are: one 16-bit kernel
+    if (dtype == TG_F32 && past) TG_GATHER(DT_F32, true);
+    else if (dtype == TG_F32) TG_GATHER(DT_F32, false);
+    else if (past) TG_GATHER(DT_F16, true);
+    else TG_GATHER(DT_F16, false);
 #undef TG_GATHER
     return launched();
 }
@@ -125,17 +132,24 @@ template <int DT>
 void launch_combine(const void *y, int64_t ldy, const int32_t *row_of_entry, const float *weights, int64_t ld_w,
                     void *out, int64_t ldo, int64_t tokens, int64_t top_k, int64_t cols, hipStream_t s) {
     typedef typename ElemOf<DT>::type T;
-    const int group = row_group(cdiv(cols * (int64_t)sizeof(T), 16));
+    // few choices: two chunks a thread, for as many loads in flight
+    const int64_t chunks = cdiv(cols * (int64_t)sizeof(T), 16);
+    const int group = row_group(choices(top_k) <= 2 ? cdiv(chunks, 2) : chunks);
     const dim3 grid((unsigned)cdiv(tokens, 256 / group));
-#define TG_COMBINE(JB)                                                                                            \
-    hipLaunchKernelGGL((combine_kernel<DT, JB>), grid, dim3(256), 0, s, static_cast<const T *>(y), ldy, row_of_entry, \
-                       weights, ld_w, static_cast<T *>(out), ldo, (int)tokens, (int)top_k, cols, group)
+    const bool past = store_past((tokens * top_k + tokens) * cols * (int64_t)sizeof(T));
+#define TG_COMBINE_AS(JB, U, PAST)                                                                                \
+    hipLaunchKernelGGL((combine_kernel<DT, JB, U, PAST>), grid, dim3(256), 0, s, static_cast<const T *>(y), ldy,     \
+                       row_of_entry, weights, ld_w, static_cast<T *>(out), ldo, (int)tokens, (int)top_k, cols, group)
+#define TG_COMBINE(JB, U)                     \
+    if (past) TG_COMBINE_AS(JB, U, true);     \
+    else TG_COMBINE_AS(JB, U, false)
     switch (choices(top_k)) {
-        case 1: TG_COMBINE(1); break;
-        case 2: TG_COMBINE(2); break;
-        case 4: TG_COMBINE(4); break;
-        default: TG_COMBINE(8); break;
+        case 1: TG_COMBINE(1, 2); break;
+        case 2: TG_COMBINE(2, 2); break;
+        case 4: TG_COMBINE(4, 1); break;
+        default: TG_COMBINE(8, 1); break;
     }
+#undef TG_COMBINE_AS
 #undef TG_COMBINE
 }
 
@@ -172,10 +186,14 @@ void launch_combine_grad(const void *d_out, int64_t ldo, const void *y, int64_t 
                          int64_t tokens, int64_t top_k, int64_t cols, hipStream_t s) {
     typedef typename ElemOf<DT>::type T;
     const dim3 grid((unsigned)cdiv(tokens, 4));
-#define TG_GRAD(JB)                                                                                                  \
-    hipLaunchKernelGGL((combine_grad_kernel<DT, JB>), grid, dim3(256), 0, s, static_cast<const T *>(d_out), ldo,       \
-                       static_cast<const T *>(y), ldy, row_of_entry, weights, ld_w, static_cast<T *>(d_y), ldd, d_w, \
+    const bool past = store_past((2 * tokens * top_k + tokens) * cols * (int64_t)sizeof(T));
+#define TG_GRAD_AS(JB, PAST)                                                                                        \
+    hipLaunchKernelGGL((combine_grad_kernel<DT, JB, PAST>), grid, dim3(256), 0, s, static_cast<const T *>(d_out), ldo, \
+                       static_cast<const T *>(y), ldy, row_of_entry, weights, ld_w, static_cast<T *>(d_y), ldd, d_w,  \
                        ld_dw, (int)tokens, (int)top_k, cols)
+#define TG_GRAD(JB)                     \
+    if (past) TG_GRAD_AS(JB, true);     \
+    else TG_GRAD_AS(JB, false)
     switch (choices(top_k)) {
         case 1: TG_GRAD(1); break;
         case 2: TG_GRAD(2); break;
@@ -183,6 +201,7 @@ void launch_combine_grad(const void *d_out, int64_t ldo, const void *y, int64_t 
         default: TG_GRAD(8); break;
     }
 #undef TG_GRAD
+#undef TG_GRAD_AS
 }
 
 tg_status combine_grad(int64_t tokens, int64_t top_k, int64_t cols, tg_dtype dtype, const void *d_out, int64_t ldo,
