@@ -88,17 +88,22 @@ tg_status launch_wgrad_tiles(const GroupedParams &p, hipStream_t s) {
     return launched();
 }
 
+// The tile of a product over rows.
+//  * up to 32 rows an expert on average the weights are streamed; so is an N below a
+//    chunk, which is not for the tiles (grouped_ring.hpp).
+//  * 16 bits: 256 x 256 from 128 such tiles on, 128 x 128 below (f16, 8 uneven experts,
+//    K 1024: 4096 x 2048 32.0 against 33.4 us, 2048 x 2048 26.5 against 22.6).
+//  * fp32: 64 x 64, more workgroups for a matrix rate that 16 of them already fill
+//    (2048 x 1024 x 512 30 us against 42 on 128 x 128; 4096 x 4096 x 512 149, 173 and 163
+//    on 256 x 256); 256 x 256 from 800 tiles on (16384 x 4096 x 2048 1979 against 2147).
 template <int DT, bool TRANS>
 tg_status launch_grouped_as(const GroupedParams &p, hipStream_t s) {
     const int64_t mean = cdiv(p.rows, p.experts);
-    // an N below a chunk is not for the tiles (grouped_ring.hpp)
     if (mean > 32 && p.N >= 8) {
         const int64_t tiles = cdiv(p.rows, 256) * cdiv(p.N, 256);
-        if (tiles >= 200) return launch_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true>(p, s);
-        if constexpr (DT == DT_F32) {
-            if (cdiv(p.rows, 128) * cdiv(p.N, 128) < 512) return launch_tiles<Tile64F32, Tile64F32, !TRANS, false>(p, s);
-        }
-        return launch_tiles<Tile128<DT>, Tile128<DT>, !TRANS, false>(p, s);
+        if (tiles >= (DT == DT_F32 ? 800 : 128)) return launch_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true>(p, s);
+        if constexpr (DT == DT_F32) return launch_tiles<Tile64F32, Tile64F32, !TRANS, false>(p, s);
+        else return launch_tiles<Tile128<DT>, Tile128<DT>, !TRANS, false>(p, s);
     }
     if (mean <= 16) return launch_stream<DT, TRANS, 1>(p, s);
     return launch_stream<DT, TRANS, 2>(p, s);
@@ -111,15 +116,18 @@ tg_status launch_grouped(const GroupedParams &p, bool transposed, hipStream_t s)
     return transposed ? launch_grouped_as<DT, true>(p, s) : launch_grouped_as<DT, false>(p, s);
 }
 
+// The tile of the weights' gradient: 256 x 256 from 200 such tiles on (16 experts of
+// 1024 x 1024, 8192 rows, f16: 29.8 us against 32.2 on 128 x 128; 8 experts: 35.9 against
+// 32.1), unless 128 x 128 pads the extents by a fifth less (257 x 1000: 32 against 19
+// us); fp32: 64 x 64, or 256 x 256 from 800 tiles on, as above.
 template <int DT>
 tg_status launch_wgrad(const GroupedParams &p, hipStream_t s) {
     if (p.M >= 8 && p.N >= 8) {
-        const int64_t tiles = p.experts * cdiv(p.M, 256) * cdiv(p.N, 256);
-        if (tiles >= 200) return launch_wgrad_tiles<Tile256<DT>, true>(p, s);
-        if constexpr (DT == DT_F32) {
-            if (p.experts * cdiv(p.M, 128) * cdiv(p.N, 128) < 512) return launch_wgrad_tiles<Tile64F32, false>(p, s);
-        }
-        return launch_wgrad_tiles<Tile128<DT>, false>(p, s);
+        const int64_t each = cdiv(p.M, 256) * cdiv(p.N, 256), small = cdiv(p.M, 128) * cdiv(p.N, 128);
+        if (p.experts * each >= (DT == DT_F32 ? 800 : 200) && 4 * each * 4 <= 5 * small)
+            return launch_wgrad_tiles<Tile256<DT>, true>(p, s);
+        if constexpr (DT == DT_F32) return launch_wgrad_tiles<Tile64F32, false>(p, s);
+        else return launch_wgrad_tiles<Tile128<DT>, false>(p, s);
     }
     const int64_t blocks = cdiv((int64_t)p.experts * p.M * p.N, 256);
     hipLaunchKernelGGL((wgrad_small_kernel<DT>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, p);
