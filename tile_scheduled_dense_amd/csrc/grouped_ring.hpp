@@ -311,8 +311,8 @@ struct GroupedTile {
     }
 
     // C's tile: rows m < m_left, columns n < n_left, from its element `at`.
-    // A whole tile on 16-byte rows takes straight-line code, without a test between
-    // stores, that writes 128 bytes of each of eight rows at a time, whole cache lines
+    // Rows of whole 16-byte units take straight-line code (a tile at an end of C a mask a
+    // store), that writes 128 bytes of each of eight rows at a time, whole cache lines
     // where C's rows are aligned to them (64 or 32 bytes a row cost up to 40% more).  Of a
     // 16-bit C a lane holds 8 bytes of each fragment, so neighbouring fragments trade
     // halves between lane groups first (v_permlane16_swap: the odd rows of 16 lanes of
@@ -354,8 +354,13 @@ struct GroupedTile {
         if constexpr (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(at));
         else *reinterpret_cast<u32x4 *>(at) = v;
     }
-    template <bool F32, bool PAST>
-    __device__ __forceinline__ void store_whole(char *row, int64_t half) const {
+    // MASKED: rows below `rows` and columns below `cols`, counted from this lane's first
+    // (whole units of 16 bytes: the caller's condition)
+    template <bool F32, bool PAST, bool MASKED>
+    __device__ __forceinline__ void store_whole(char *row, int64_t half, int rows, int cols) const {
+        auto out = [&](char *at, const u32x4 &v, int r, int c) {
+            if (!MASKED || (r < rows && c < cols)) put<PAST>(at, v);
+        };
         // a store takes two fragments (fp32) or four (16 bits) of the wave's columns
         static_assert(C::TN % (C::DT == DT_F32 ? 2 : 4) == 0, "whole 128 bytes of a wave's columns");
         static_for<0, C::TM, 1>([&](auto ic) {
@@ -365,16 +370,16 @@ struct GroupedTile {
                     constexpr int j = decltype(jc)::value;
                     u32x4 low, high;
                     trade_rows(quad32<i, j>(), quad32<i, j + 1>(), low, high);
-                    put<PAST>(row + 64 * j, low);
-                    put<PAST>(row + 64 * j + half, high);
+                    out(row + 64 * j, low, 16 * i, 16 * j);
+                    out(row + 64 * j + half, high, 16 * i + 8, 16 * j);
                 });
             } else if constexpr (C::DT != DT_F32) {
                 static_for<0, C::TN, 4>([&](auto jc) {
                     constexpr int j = decltype(jc)::value;
                     u32x4 low, high;
                     trade_rows(pair16<i, j>(), pair16<i, j + 2>(), low, high);
-                    put<PAST>(row + 32 * j, low);
-                    put<PAST>(row + 32 * j + half, high);
+                    out(row + 32 * j, low, 16 * i, 16 * j);
+                    out(row + 32 * j + half, high, 16 * i + 8, 16 * j);
                 });
             }
             row += 2 * half;
@@ -387,15 +392,21 @@ struct GroupedTile {
         const int size = f32 ? 4 : 2;
         char *first = Cp + at * size;
         const bool wide = ldc * size % 16 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
-        if (wide && m_left >= C::BM && n_left >= C::BN) {
+        const int unit = 16 / size;
+        if (wide && (n_left >= C::BN || n_left % unit == 0)) {
             const int rm = (wave / C::WAVES_N) * C::WTM + lane % 8;
-            char *row = first + ((int64_t)rm * ldc + n) * size + 64 * (lane % 16 / 8);
+            const int rn = n + (f32 ? 4 * g : 8 * (g / 2) + 16 * (g % 2)) + 64 / size * (lane % 16 / 8);
+            char *row = first + ((int64_t)rm * ldc + rn) * size;
             const int64_t half = 8 * ldc * size;
-            row += f32 ? 16 * g : 16 * (g / 2) + 32 * (g % 2);
-            if (f32 && past) store_whole<true, true>(row, half);
-            else if (f32) store_whole<true, false>(row, half);
-            else if (past) store_whole<false, true>(row, half);
-            else store_whole<false, false>(row, half);
+            if (m_left >= C::BM && n_left >= C::BN) {
+                if (f32 && past) store_whole<true, true, false>(row, half, 0, 0);
+                else if (f32) store_whole<true, false, false>(row, half, 0, 0);
+                else if (past) store_whole<false, true, false>(row, half, 0, 0);
+                else store_whole<false, false, false>(row, half, 0, 0);
+            } else {
+                if (f32) store_whole<true, false, true>(row, half, m_left - rm, n_left - rn);
+                else store_whole<false, false, true>(row, half, m_left - rm, n_left - rn);
+            }
             return;
         }
         const bool wide4 = ldc % 4 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
