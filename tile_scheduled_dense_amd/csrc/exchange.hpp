@@ -23,29 +23,34 @@ struct Row {
     static constexpr int PER = 16 / (int)sizeof(T);     // elements per chunk
     typedef T vec __attribute__((ext_vector_type(PER)));
 
-    // chunk c of a row of `cols` elements; past the end +0 (a partial chunk is read element by element)
+    // Chunk c of a row of `cols` elements.  A last chunk that the row's end cuts is moved
+    // back to end with the row: its first elements are the previous chunk's once more,
+    // read, and written with the same values.  Only a row shorter than a chunk goes
+    // element by element.
+    __device__ __forceinline__ static int64_t first(int64_t c, int64_t cols) {
+        return (c + 1) * PER <= cols || cols < PER ? c * PER : cols - PER;
+    }
     __device__ __forceinline__ static u32x4 load(const T *row, int64_t c, int64_t cols) {
-        const int64_t left = cols - c * PER;
-        if (left >= PER) return *reinterpret_cast<const u32x4_any *>(row + c * PER);
+        if (cols >= PER) return *reinterpret_cast<const u32x4_any *>(row + first(c, cols));
         vec v = {};
 #pragma unroll
         for (int e = 0; e < PER - 1; ++e)
-            if (e < left) v[e] = row[c * PER + e];
+            if (e < cols) v[e] = row[e];
         return __builtin_bit_cast(u32x4, v);
     }
     // PAST: with the non-temporal hint
     template <bool PAST = false>
     __device__ __forceinline__ static void store(T *row, int64_t c, int64_t cols, u32x4 x) {
-        const int64_t left = cols - c * PER;
-        if (left >= PER) {
-            if constexpr (PAST) __builtin_nontemporal_store(x, reinterpret_cast<u32x4_any *>(row + c * PER));
-            else *reinterpret_cast<u32x4_any *>(row + c * PER) = x;
+        if (cols >= PER) {
+            u32x4_any *at = reinterpret_cast<u32x4_any *>(row + first(c, cols));
+            if constexpr (PAST) __builtin_nontemporal_store(x, at);
+            else *at = x;
             return;
         }
         const vec v = __builtin_bit_cast(vec, x);
 #pragma unroll
         for (int e = 0; e < PER - 1; ++e)
-            if (e < left) row[c * PER + e] = v[e];
+            if (e < cols) row[e] = v[e];
     }
     __device__ __forceinline__ static void widen(u32x4 x, float (&f)[PER]) {
         const vec v = __builtin_bit_cast(vec, x);
@@ -260,14 +265,20 @@ static __global__ __launch_bounds__(1024) void sort_place_kernel(SortParams p) {
 }
 
 // ---- rows ---------------------------------------------------------------------------
-// `group` threads (64, 128 or 256) take a token's row, a chunk each at a time,
-// and 256 / group tokens fill a workgroup.  A wave has one token: its table
-// entries and weights are scalar loads.
+// `group` threads, 16 to 256, take a token's row, a chunk each at a time, and 256 /
+// group tokens fill a workgroup.  From 64 on a wave has one token, and its table
+// entries and weights are scalar loads; NARROW: fewer, for rows of up to 32 chunks
+// (6508 x 118 bf16 of 8 choices and 91 experts: forward and backward 87 us with a wave
+// for each 15 chunks, 39 us with 16 lanes).
+inline int row_group(int64_t chunks) {
+    return chunks > 128 ? 256 : (chunks > 64 ? 128 : (chunks > 32 ? 64 : (chunks > 16 ? 32 : 16)));
+}
 // whether a call that moves so many bytes stores past the caches (gather_kernel)
 inline bool store_past(int64_t bytes) { return bytes > (int64_t(64) << 20); }
-inline int row_group(int64_t chunks) { return chunks > 128 ? 256 : (chunks > 64 ? 128 : 64); }
+template <bool NARROW>
 __device__ __forceinline__ int token_of(int group) {
-    return __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (256 / group) + threadIdx.x / group));
+    const int t = (int)(blockIdx.x * (256 / group) + threadIdx.x / group);
+    return NARROW ? t : __builtin_amdgcn_readfirstlane(t);
 }
 
 // PAST: results are stored past the caches, where a call moves more than 64 MiB:
@@ -276,13 +287,13 @@ __device__ __forceinline__ int token_of(int group) {
 // 2048 bf16 of 2 choices, takes 113 us without the hint and 99 with it; 1999 x 1001
 // fp32 of 8 choices 96 and 87 (where the gather alone, its rows off 16 bytes, takes 18
 // in place of 15).  The hint on loads too: 106.
-template <int DT, bool PAST>
+template <int DT, bool PAST, bool NARROW>
 __global__ __launch_bounds__(256) void gather_kernel(const typename ElemOf<DT>::type *__restrict__ x, int64_t ldx,
                                                      const int32_t *__restrict__ row_of_entry,
                                                      typename ElemOf<DT>::type *__restrict__ rows, int64_t ldr,
                                                      int tokens, int top_k, int64_t cols, int group) {
     using R = Row<DT>;
-    const int t = token_of(group);
+    const int t = token_of<NARROW>(group);
     if (t >= tokens) return;
     const int n = tokens * top_k;
     const int32_t *row = row_of_entry + (int64_t)t * top_k;
@@ -299,14 +310,14 @@ __global__ __launch_bounds__(256) void gather_kernel(const typename ElemOf<DT>::
 // JB choices of a token and U chunks at a time, their loads in flight together.  A
 // choice without an expert loads row 0 in its place (in cache after the first) and is
 // left out of the sum by selection, so that what lies there, a NaN say, goes nowhere.
-template <int DT, int JB, int U, bool PAST>
+template <int DT, int JB, int U, bool PAST, bool NARROW>
 __global__ __launch_bounds__(256) void combine_kernel(const typename ElemOf<DT>::type *__restrict__ y, int64_t ldy,
                                                       const int32_t *__restrict__ row_of_entry,
                                                       const float *__restrict__ weights, int64_t ld_w,
                                                       typename ElemOf<DT>::type *__restrict__ out, int64_t ldo,
                                                       int tokens, int top_k, int64_t cols, int group) {
     using R = Row<DT>;
-    const int t = token_of(group);
+    const int t = token_of<NARROW>(group);
     if (t >= tokens) return;
     const int n = tokens * top_k;
     const int32_t *row = row_of_entry + (int64_t)t * top_k;
@@ -346,8 +357,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const typename ElemOf<DT>:
     }
 }
 
-// One wave a token: the dot products are summed over its lanes without LDS.
-template <int DT, int JB, bool PAST>
+// `group` of 16, 32 or 64 lanes a token: the dot products are summed over them without LDS.
+template <int DT, int JB, bool PAST, bool NARROW>
 __global__ __launch_bounds__(256) void combine_grad_kernel(const typename ElemOf<DT>::type *__restrict__ d_out,
                                                            int64_t ldo,
                                                            const typename ElemOf<DT>::type *__restrict__ y,
@@ -355,9 +366,9 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const typename ElemOf
                                                            const float *__restrict__ weights, int64_t ld_w,
                                                            typename ElemOf<DT>::type *__restrict__ d_y, int64_t ldd,
                                                            float *__restrict__ d_w, int64_t ld_dw, int tokens,
-                                                           int top_k, int64_t cols) {
+                                                           int top_k, int64_t cols, int group) {
     using R = Row<DT>;
-    const int t = token_of(64), lane = threadIdx.x & 63;
+    const int t = token_of<NARROW>(group), lane = threadIdx.x % group;
     if (t >= tokens) return;
     const int n = tokens * top_k;
     const int32_t *row = row_of_entry + (int64_t)t * top_k;
@@ -374,7 +385,8 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const typename ElemOf
             w[j] = has[j] ? weights[(int64_t)t * ld_w + j0 + j] : 0.0f;
             dot[j] = 0.0f;
         }
-        for (int64_t c = lane; c < chunks; c += 64) {
+        for (int64_t c = lane; c < chunks; c += group) {
+            const int64_t again = cols >= R::PER ? c * R::PER - R::first(c, cols) : 0;   // elements of the previous chunk
             float g[R::PER];
             u32x4 v[JB];
             R::widen(R::load(d_out + (int64_t)t * ldo, c, cols), g);
@@ -386,7 +398,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const typename ElemOf
                 R::widen(v[j], f);
 #pragma unroll
                 for (int e = 0; e < R::PER; ++e) {
-                    dot[j] = has[j] ? __builtin_fmaf(g[e], f[e], dot[j]) : 0.0f;
+                    dot[j] = has[j] && e >= again ? __builtin_fmaf(g[e], f[e], dot[j]) : dot[j];
                     d[e] = has[j] ? w[j] * g[e] : 0.0f;
                 }
                 if (at[j] >= 0) R::template store<PAST>(d_y + (int64_t)at[j] * ldd, c, cols, R::narrow(d));
@@ -394,7 +406,7 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const typename ElemOf
         }
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
-            for (int d = 32; d > 0; d /= 2) dot[j] += __shfl_xor(dot[j], d);
+            for (int d = group / 2; d > 0; d /= 2) dot[j] += __shfl_xor(dot[j], d);
             if (lane == 0 && j0 + j < top_k) d_w[(int64_t)t * ld_dw + j0 + j] = dot[j];
         }
     }

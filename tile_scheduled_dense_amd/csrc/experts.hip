@@ -113,14 +113,22 @@ tg_status gather(int64_t tokens, int64_t top_k, int64_t cols, tg_dtype dtype, co
     const dim3 grid((unsigned)cdiv(tokens, 256 / group));
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool past = store_past((n + tokens) * cols * esz);
-#define TG_GATHER(DT, PAST)                                                                                        \
-    hipLaunchKernelGGL((gather_kernel<DT, PAST>), grid, dim3(256), 0, s, static_cast<const ElemOf<DT>::type *>(x), ldx, \
-                       row_of_entry, static_cast<ElemOf<DT>::type *>(rows), ldr, (int)tokens, (int)top_k, cols, group)
+#define TG_GATHER(DT, PAST, NARROW)                                                                                \
+    hipLaunchKernelGGL((gather_kernel<DT, PAST, NARROW>), grid, dim3(256), 0, s,                                      \
+                       static_cast<const ElemOf<DT>::type *>(x), ldx, row_of_entry,                                   \
+                       static_cast<ElemOf<DT>::type *>(rows), ldr, (int)tokens, (int)top_k, cols, group)
+#define TG_GATHER_AS(DT)                                         \
+    if (past && group < 64) TG_GATHER(DT, true, true);           \
+    else if (past) TG_GATHER(DT, true, false);                   \
+    else if (group < 64) TG_GATHER(DT, false, true);             \
+    else TG_GATHER(DT, false, false)
     // the bytes are moved as they are: one 16-bit kernel
-    if (dtype == TG_F32 && past) TG_GATHER(DT_F32, true);
-    else if (dtype == TG_F32) TG_GATHER(DT_F32, false);
-    else if (past) TG_GATHER(DT_F16, true);
-    else TG_GATHER(DT_F16, false);
+    if (dtype == TG_F32) {
+        TG_GATHER_AS(DT_F32);
+    } else {
+        TG_GATHER_AS(DT_F16);
+    }
+#undef TG_GATHER_AS
 #undef TG_GATHER
     return launched();
 }
@@ -137,12 +145,14 @@ void launch_combine(const void *y, int64_t ldy, const int32_t *row_of_entry, con
     const int group = row_group(choices(top_k) <= 2 ? cdiv(chunks, 2) : chunks);
     const dim3 grid((unsigned)cdiv(tokens, 256 / group));
     const bool past = store_past((tokens * top_k + tokens) * cols * (int64_t)sizeof(T));
-#define TG_COMBINE_AS(JB, U, PAST)                                                                                \
-    hipLaunchKernelGGL((combine_kernel<DT, JB, U, PAST>), grid, dim3(256), 0, s, static_cast<const T *>(y), ldy,     \
+#define TG_COMBINE_AS(JB, U, PAST, NARROW)                                                                        \
+    hipLaunchKernelGGL((combine_kernel<DT, JB, U, PAST, NARROW>), grid, dim3(256), 0, s, static_cast<const T *>(y), ldy, \
                        row_of_entry, weights, ld_w, static_cast<T *>(out), ldo, (int)tokens, (int)top_k, cols, group)
-#define TG_COMBINE(JB, U)                     \
-    if (past) TG_COMBINE_AS(JB, U, true);     \
-    else TG_COMBINE_AS(JB, U, false)
+#define TG_COMBINE(JB, U)                                        \
+    if (past && group < 64) TG_COMBINE_AS(JB, U, true, true);    \
+    else if (past) TG_COMBINE_AS(JB, U, true, false);            \
+    else if (group < 64) TG_COMBINE_AS(JB, U, false, true);      \
+    else TG_COMBINE_AS(JB, U, false, false)
     switch (choices(top_k)) {
         case 1: TG_COMBINE(1, 2); break;
         case 2: TG_COMBINE(2, 2); break;
@@ -185,15 +195,18 @@ void launch_combine_grad(const void *d_out, int64_t ldo, const void *y, int64_t 
                          const float *weights, int64_t ld_w, void *d_y, int64_t ldd, float *d_w, int64_t ld_dw,
                          int64_t tokens, int64_t top_k, int64_t cols, hipStream_t s) {
     typedef typename ElemOf<DT>::type T;
-    const dim3 grid((unsigned)cdiv(tokens, 4));
+    const int rows = row_group(cdiv(cols * (int64_t)sizeof(T), 16)), group = rows < 64 ? rows : 64;
+    const dim3 grid((unsigned)cdiv(tokens, 256 / group));
     const bool past = store_past((2 * tokens * top_k + tokens) * cols * (int64_t)sizeof(T));
-#define TG_GRAD_AS(JB, PAST)                                                                                        \
-    hipLaunchKernelGGL((combine_grad_kernel<DT, JB, PAST>), grid, dim3(256), 0, s, static_cast<const T *>(d_out), ldo, \
-                       static_cast<const T *>(y), ldy, row_of_entry, weights, ld_w, static_cast<T *>(d_y), ldd, d_w,  \
-                       ld_dw, (int)tokens, (int)top_k, cols)
-#define TG_GRAD(JB)                     \
-    if (past) TG_GRAD_AS(JB, true);     \
-    else TG_GRAD_AS(JB, false)
+#define TG_GRAD_AS(JB, PAST, NARROW)                                                                                \
+    hipLaunchKernelGGL((combine_grad_kernel<DT, JB, PAST, NARROW>), grid, dim3(256), 0, s, static_cast<const T *>(d_out), \
+                       ldo, static_cast<const T *>(y), ldy, row_of_entry, weights, ld_w, static_cast<T *>(d_y), ldd, d_w, \
+                       ld_dw, (int)tokens, (int)top_k, cols, group)
+#define TG_GRAD(JB)                                        \
+    if (past && group < 64) TG_GRAD_AS(JB, true, true);    \
+    else if (past) TG_GRAD_AS(JB, true, false);            \
+    else if (group < 64) TG_GRAD_AS(JB, false, true);      \
+    else TG_GRAD_AS(JB, false, false)
     switch (choices(top_k)) {
         case 1: TG_GRAD(1); break;
         case 2: TG_GRAD(2); break;

@@ -70,29 +70,39 @@ inline int64_t most_tiles(int64_t rows, int64_t groups, int64_t bm) {
 // P: the pieces' configuration (C itself: none).  The grid is the most there can
 // be: whole tiles, three more pieces for each tile that is split, and a row of
 // pieces for every group.
-template <class C, class P, bool B_KS, bool PIPE>
+template <class C, class P, bool B_KS, bool PIPE, int STAGES = 4>
 tg_status launch_tiles(const GroupedParams &p, hipStream_t s) {
     int64_t grid = most_tiles(p.rows, p.experts + 1, C::BM) * cdiv(p.N, C::BN);
     if (!std::is_same<C, P>::value)
         grid += 3 * kSplitRound + (p.rows < p.experts + 1 ? p.rows : p.experts + 1) * cdiv(p.N, P::BN);
     if (grid > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((grouped_tile_kernel<C, P, B_KS, PIPE>), dim3((unsigned)grid), dim3(C::THREADS), 0, s, p);
+    hipLaunchKernelGGL((grouped_tile_kernel<C, P, B_KS, PIPE, STAGES>), dim3((unsigned)grid), dim3(C::THREADS), 0, s, p);
     return launched();
 }
 
-template <class C, bool PIPE>
+template <class C, bool PIPE, int STAGES = 4>
 tg_status launch_wgrad_tiles(const GroupedParams &p, hipStream_t s) {
     const int64_t tiles = cdiv(p.M, C::BM) * cdiv(p.N, C::BN), grid = p.experts * cdiv(tiles, 8) * 8;
     if (grid > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((wgrad_tile_kernel<C, PIPE>), dim3((unsigned)grid), dim3(C::THREADS), 0, s, p);
+    hipLaunchKernelGGL((wgrad_tile_kernel<C, PIPE, STAGES>), dim3((unsigned)grid), dim3(C::THREADS), 0, s, p);
     return launched();
 }
+
+// A contraction long enough that the 256 x 256 tile's rate outweighs what its start
+// and its stores cost, which the two or three workgroups of 128 x 128 that a CU holds
+// hide in each other (bf16, 8 uneven experts: 16384 x 4096 over K 256 55 us on 128 x 128
+// against 70, 512 86 against 96, 8192 x 4096 over 1024 81 against 78; the weights'
+// gradient of 2048 x 2048 over 512 rows an expert 86 against 99, over 1024 75 against 74).
+constexpr int64_t kLong = 1024;
 
 // The tile of a product over rows.
 //  * up to 32 rows an expert on average the weights are streamed; so is an N below a
 //    chunk, which is not for the tiles (grouped_ring.hpp).
-//  * 16 bits: 256 x 256 from 128 such tiles on, 128 x 128 below (f16, 8 uneven experts,
-//    K 1024: 4096 x 2048 32.0 against 33.4 us, 2048 x 2048 26.5 against 22.6).
+//  * 16 bits: 256 x 256 over a long K from 128 such tiles on (f16, 8 uneven experts, K
+//    1024: 4096 x 2048 32.0 against 33.4 us on 128 x 128, 2048 x 2048 26.5 against 22.6),
+//    else 128 x 128, three LDS copies for three workgroups a CU (257 x 1000 over 150 rows
+//    18.9 us with four copies, 17.0 with three, 16.8 with two, which cost 5001 x 257 over
+//    1000 28.4 against 21.9).
 //  * fp32: 64 x 64, more workgroups for a matrix rate that 16 of them already fill
 //    (2048 x 1024 x 512 30 us against 42 on 128 x 128; 4096 x 4096 x 512 149, 173 and 163
 //    on 256 x 256); 256 x 256 from 800 tiles on (16384 x 4096 x 2048 1979 against 2147).
@@ -101,9 +111,10 @@ tg_status launch_grouped_as(const GroupedParams &p, hipStream_t s) {
     const int64_t mean = cdiv(p.rows, p.experts);
     if (mean > 32 && p.N >= 8) {
         const int64_t tiles = cdiv(p.rows, 256) * cdiv(p.N, 256);
-        if (tiles >= (DT == DT_F32 ? 800 : 128)) return launch_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true>(p, s);
+        if (p.K >= kLong && tiles >= (DT == DT_F32 ? 800 : 128))
+            return launch_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true>(p, s);
         if constexpr (DT == DT_F32) return launch_tiles<Tile64F32, Tile64F32, !TRANS, false>(p, s);
-        else return launch_tiles<Tile128<DT>, Tile128<DT>, !TRANS, false>(p, s);
+        else return launch_tiles<Tile128<DT>, Tile128<DT>, !TRANS, false, 3>(p, s);
     }
     if (mean <= 16) return launch_stream<DT, TRANS, 1>(p, s);
     return launch_stream<DT, TRANS, 2>(p, s);
@@ -116,18 +127,18 @@ tg_status launch_grouped(const GroupedParams &p, bool transposed, hipStream_t s)
     return transposed ? launch_grouped_as<DT, true>(p, s) : launch_grouped_as<DT, false>(p, s);
 }
 
-// The tile of the weights' gradient: 256 x 256 from 200 such tiles on (16 experts of
-// 1024 x 1024, 8192 rows, f16: 29.8 us against 32.2 on 128 x 128; 8 experts: 35.9 against
-// 32.1), unless 128 x 128 pads the extents by a fifth less (257 x 1000: 32 against 19
-// us); fp32: 64 x 64, or 256 x 256 from 800 tiles on, as above.
+// The tile of the weights' gradient, by the same rules; its contraction is an expert's
+// rows, on average.  256 x 256 from 200 tiles on (16 experts of 1024 x 1024: 29.8 us
+// against 32.2 on 128 x 128; 8 experts 35.9 against 32.1), unless 128 x 128 pads the
+// extents by a fifth less.
 template <int DT>
 tg_status launch_wgrad(const GroupedParams &p, hipStream_t s) {
     if (p.M >= 8 && p.N >= 8) {
         const int64_t each = cdiv(p.M, 256) * cdiv(p.N, 256), small = cdiv(p.M, 128) * cdiv(p.N, 128);
-        if (p.experts * each >= (DT == DT_F32 ? 800 : 200) && 4 * each * 4 <= 5 * small)
+        if (p.experts * each >= (DT == DT_F32 ? 800 : 200) && 4 * each * 4 <= 5 * small && cdiv(p.rows, p.experts) >= kLong)
             return launch_wgrad_tiles<Tile256<DT>, true>(p, s);
         if constexpr (DT == DT_F32) return launch_wgrad_tiles<Tile64F32, false>(p, s);
-        else return launch_wgrad_tiles<Tile128<DT>, false>(p, s);
+        else return launch_wgrad_tiles<Tile128<DT>, false, 3>(p, s);
     }
     const int64_t blocks = cdiv((int64_t)p.experts * p.M * p.N, 256);
     hipLaunchKernelGGL((wgrad_small_kernel<DT>), dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, p);

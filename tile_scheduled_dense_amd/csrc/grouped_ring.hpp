@@ -543,10 +543,10 @@ __device__ __forceinline__ bool row_tile(const GroupedParams &p, RowTile &t) {
     return false;
 }
 
-template <class C, bool A_KS, bool B_KS, bool PIPE>
+template <class C, bool A_KS, bool B_KS, bool PIPE, int STAGES>
 __device__ __forceinline__ void run_tile_of(const GroupedParams &p, char *smem, const char *A, int64_t lda, int m_left,
                                             const char *B, int n_left, int K, int64_t c_at) {
-    GroupedTile<C, A_KS, B_KS, 4> tile;
+    GroupedTile<C, A_KS, B_KS, STAGES> tile;
     tile.init(A, lda, m_left, B, p.ldb, n_left, K, smem);
     if constexpr (PIPE) tile.run_pipe();
     else tile.run_ring();
@@ -554,11 +554,11 @@ __device__ __forceinline__ void run_tile_of(const GroupedParams &p, char *smem, 
 }
 
 // P: the configuration of the pieces (C itself: none).
-template <class C, class P, bool B_KS, bool PIPE>
+template <class C, class P, bool B_KS, bool PIPE, int STAGES>
 __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void grouped_tile_kernel(GroupedParams p) {
     constexpr bool PIECES = !std::is_same<C, P>::value;
     static_assert(!PIECES || (P::BM * 2 == C::BM && P::BN * 2 == C::BN && P::THREADS == C::THREADS), "quarters");
-    __shared__ __attribute__((aligned(1024))) char smem[GroupedTile<C, false, B_KS, 4>::LDS];
+    __shared__ __attribute__((aligned(1024))) char smem[GroupedTile<C, false, B_KS, STAGES>::LDS];
     RowTile t;
     if (!row_tile<C::BM, C::BN, PIECES>(p, t)) return;
     const bool dead = t.g == p.experts;
@@ -567,9 +567,9 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void grouped_tile_kernel(
     const char *B = p.B + ((dead ? 0 : (int64_t)t.g * p.sB) + (B_KS ? (int64_t)t.n0 : t.n0 * p.ldb)) * C::ELEM;
     const int K = dead ? 0 : p.K;
     if (PIECES && t.piece)
-        run_tile_of<P, false, B_KS, PIPE>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0);
+        run_tile_of<P, false, B_KS, PIPE, STAGES>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0);
     else
-        run_tile_of<C, false, B_KS, PIPE>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0);
+        run_tile_of<C, false, B_KS, PIPE, STAGES>(p, smem, A, p.lda, t.rows, B, p.N - t.n0, K, row * p.ldc + t.n0);
 }
 
 // The gradient with respect to B: experts x tiles_m x tiles_n tiles, whose work
@@ -579,9 +579,9 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void grouped_tile_kernel(
 // tiles to end are short ones (8 uneven experts of 2048 x 4096: 220 -> 214 us; the order
 // costs a small tile more than it gives: 33 of 257 x 1000 19.0 -> 20.5, so only the
 // large ones).
-template <class C, bool PIPE>
+template <class C, bool PIPE, int STAGES>
 __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void wgrad_tile_kernel(GroupedParams p) {
-    __shared__ __attribute__((aligned(1024))) char smem[GroupedTile<C, true, true, 4>::LDS];
+    __shared__ __attribute__((aligned(1024))) char smem[GroupedTile<C, true, true, STAGES>::LDS];
     const uint32_t tiles_m = (p.M + C::BM - 1) / C::BM, tiles_n = (p.N + C::BN - 1) / C::BN, tiles = tiles_m * tiles_n;
     const uint32_t run = (tiles + 7) / 8;
     int g = (int)(blockIdx.x / (8 * run));
@@ -603,7 +603,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void wgrad_tile_kernel(Gr
     }
     const RowSpan s = rows_of(p.offsets, g, p.experts, p.rows);
     const int lo = __builtin_amdgcn_readfirstlane(s.lo), K = __builtin_amdgcn_readfirstlane(s.hi) - lo;
-    run_tile_of<C, true, true, PIPE>(p, smem, p.A + ((int64_t)lo * p.lda + m0) * C::ELEM, p.lda, p.M - m0,
+    run_tile_of<C, true, true, PIPE, STAGES>(p, smem, p.A + ((int64_t)lo * p.lda + m0) * C::ELEM, p.lda, p.M - m0,
                                      p.B + ((int64_t)lo * p.ldb + n0) * C::ELEM, p.N - n0, K,
                                      (int64_t)g * p.sC + (int64_t)m0 * p.ldc + n0);
 }
