@@ -105,7 +105,8 @@ constexpr int64_t kLong = 1024;
 //    1000 28.4 against 21.9).
 //  * fp32: 64 x 64, more workgroups for a matrix rate that 16 of them already fill
 //    (2048 x 1024 x 512 30 us against 42 on 128 x 128; 4096 x 4096 x 512 149, 173 and 163
-//    on 256 x 256); 256 x 256 from 800 tiles on (16384 x 4096 x 2048 1979 against 2147).
+//    on 256 x 256), with the software pipeline (2048 x 1024 x 512 28 us, 30 without);
+//    256 x 256 from 800 tiles on (16384 x 4096 x 2048 1979 against 2147).
 template <int DT, bool TRANS>
 tg_status launch_grouped_as(const GroupedParams &p, hipStream_t s) {
     const int64_t mean = cdiv(p.rows, p.experts);
@@ -113,7 +114,7 @@ tg_status launch_grouped_as(const GroupedParams &p, hipStream_t s) {
         const int64_t tiles = cdiv(p.rows, 256) * cdiv(p.N, 256);
         if (p.K >= kLong && tiles >= (DT == DT_F32 ? 800 : 128))
             return launch_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true>(p, s);
-        if constexpr (DT == DT_F32) return launch_tiles<Tile64F32, Tile64F32, !TRANS, false>(p, s);
+        if constexpr (DT == DT_F32) return launch_tiles<Tile64F32, Tile64F32, !TRANS, true>(p, s);
         else return launch_tiles<Tile128<DT>, Tile128<DT>, !TRANS, false, 3>(p, s);
     }
     if (mean <= 16) return launch_stream<DT, TRANS, 1>(p, s);
@@ -130,14 +131,17 @@ tg_status launch_grouped(const GroupedParams &p, bool transposed, hipStream_t s)
 // The tile of the weights' gradient, by the same rules; its contraction is an expert's
 // rows, on average.  256 x 256 from 200 tiles on (16 experts of 1024 x 1024: 29.8 us
 // against 32.2 on 128 x 128; 8 experts 35.9 against 32.1), unless 128 x 128 pads the
-// extents by a fifth less.
+// extents by a fifth less.  128 x 128 with the software pipeline where no CU has a
+// second tile to hide the first one's waits (464 x 96 over 1464 rows, 2 experts: 20.4 ->
+// 13.1 us; 33 of 257 x 1000 over 150 16.9 -> 20.9).
 template <int DT>
 tg_status launch_wgrad(const GroupedParams &p, hipStream_t s) {
     if (p.M >= 8 && p.N >= 8) {
         const int64_t each = cdiv(p.M, 256) * cdiv(p.N, 256), small = cdiv(p.M, 128) * cdiv(p.N, 128);
         if (p.experts * each >= (DT == DT_F32 ? 800 : 200) && 4 * each * 4 <= 5 * small && cdiv(p.rows, p.experts) >= kLong)
             return launch_wgrad_tiles<Tile256<DT>, true>(p, s);
-        if constexpr (DT == DT_F32) return launch_wgrad_tiles<Tile64F32, false>(p, s);
+        if constexpr (DT == DT_F32) return launch_wgrad_tiles<Tile64F32, true>(p, s);
+        else if (p.experts * small <= 256) return launch_wgrad_tiles<Tile128<DT>, true>(p, s);
         else return launch_wgrad_tiles<Tile128<DT>, false, 3>(p, s);
     }
     const int64_t blocks = cdiv((int64_t)p.experts * p.M * p.N, 256);
