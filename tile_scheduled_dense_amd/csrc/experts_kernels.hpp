@@ -13,13 +13,15 @@ namespace {
 inline tg_status launched() { return hipGetLastError() == hipSuccess ? TG_OK : TG_ERR_LAUNCH; }
 
 // Waves that split K: enough for two stages each, eight at most.
-template <int DT, bool TRANS, int MT>
+template <int DT, bool TRANS>
 tg_status launch_stream(const GroupedParams &p, hipStream_t s) {
     using S = StreamShape<DT, TRANS>;
     const int64_t stages = cdiv(p.K, S::K);
     const int waves = stages >= 16 ? 8 : (stages >= 8 ? 4 : 2);
-    const dim3 grid((unsigned)cdiv(p.N, S::COLS), (unsigned)p.experts + 1);
-    hipLaunchKernelGGL((grouped_stream_kernel<DT, TRANS, MT>), grid, dim3(64 * waves), waves * S::FRAGS * 1024, s, p);
+    // row tiles at the same time: twice an expert's on average, for uneven experts
+    const int64_t tiles = cdiv(2 * cdiv(p.rows, p.experts), 16);
+    const dim3 grid((unsigned)cdiv(p.N, S::COLS), (unsigned)p.experts + 1, (unsigned)(tiles < 8 ? tiles : 8));
+    hipLaunchKernelGGL((grouped_stream_kernel<DT, TRANS>), grid, dim3(64 * waves), waves * S::FRAGS * 1024, s, p);
     return launched();
 }
 
@@ -96,8 +98,13 @@ tg_status launch_wgrad_tiles(const GroupedParams &p, hipStream_t s) {
 constexpr int64_t kLong = 1024;
 
 // The tile of a product over rows.
-//  * up to 32 rows an expert on average the weights are streamed; so is an N below a
-//    chunk, which is not for the tiles (grouped_ring.hpp).
+//  * The weights are streamed, by workgroups that split K among their waves, while they
+//    are at most 96 MiB and an expert has on average at most 8 rows, or at most 128 and
+//    a workgroup a CU takes all 16-row tiles at the same time (bf16: 8 experts of 1024 x
+//    4096, 4 rows 13.6 us against 17.6 on tiles; one of 4096 x 256, 16 rows 14.5 against
+//    45.6, 96 rows 14.6 against 45.9; 4 of 2048 x 2048, 24 rows 11.1 against 24.3; but 32
+//    of 2048 x 1024, 4 rows, 31.5 against 24.6, where the tiles' copies read at 5.5 TB/s,
+//    and two workgroups a CU, 8 experts of 1024 x 4096, 32 rows, 28.7 against 18.1).  So is an N below a chunk, which is not for the tiles (grouped_ring.hpp).
 //  * 16 bits: 256 x 256 over a long K from 128 such tiles on (f16, 8 uneven experts, K
 //    1024: 4096 x 2048 32.0 against 33.4 us on 128 x 128, 2048 x 2048 26.5 against 22.6),
 //    else 128 x 128, three LDS copies for three workgroups a CU (257 x 1000 over 150 rows
@@ -110,15 +117,17 @@ constexpr int64_t kLong = 1024;
 template <int DT, bool TRANS>
 tg_status launch_grouped_as(const GroupedParams &p, hipStream_t s) {
     const int64_t mean = cdiv(p.rows, p.experts);
-    if (mean > 32 && p.N >= 8) {
+    const int64_t weights = (int64_t)p.experts * p.N * p.K * (DT == DT_F32 ? 4 : 2);
+    const int64_t strips = cdiv(p.N, StreamShape<DT, TRANS>::COLS) * p.experts * cdiv(mean, 16);
+    const bool stream = weights <= (int64_t(96) << 20) && (mean <= 8 || (mean <= 128 && strips < 256));
+    if (!stream && p.N >= 8) {
         const int64_t tiles = cdiv(p.rows, 256) * cdiv(p.N, 256);
         if (p.K >= kLong && tiles >= (DT == DT_F32 ? 800 : 128))
             return launch_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true>(p, s);
         if constexpr (DT == DT_F32) return launch_tiles<Tile64F32, Tile64F32, !TRANS, true>(p, s);
         else return launch_tiles<Tile128<DT>, Tile128<DT>, !TRANS, false, 3>(p, s);
     }
-    if (mean <= 16) return launch_stream<DT, TRANS, 1>(p, s);
-    return launch_stream<DT, TRANS, 2>(p, s);
+    return launch_stream<DT, TRANS>(p, s);
 }
 
 }  // namespace

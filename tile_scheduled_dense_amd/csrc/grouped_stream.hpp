@@ -1,8 +1,7 @@
 // grouped_stream.hpp -- expert products with few rows an expert: C[r] = A[r] .
 // B[g], bound by the bytes of the experts' weights.
 //
-// The weights go from HBM straight to registers, every byte once (per 16 * MT
-// rows), and no LDS lies between: at a few rows a weight is used by a single
+// The weights go from HBM straight to registers, every byte once (per 16 rows), and no LDS lies between: at a few rows a weight is used by a single
 // matrix instruction.  A workgroup takes a strip of columns of one expert, its
 // waves split K stage by stage, and their sums are added in LDS in wave order.
 // The weights are the matrix instruction's first operand and the tokens its
@@ -91,38 +90,36 @@ struct StreamB {
     }
 };
 
-// rows of A: A_LOADS chunks of row tile i's row of this lane
-template <int DT, bool TRANS, int MT>
+// rows of A: A_LOADS chunks of this lane's row of 16
+template <int DT, bool TRANS>
 struct StreamA {
     using S = StreamShape<DT, TRANS>;
-    u32x4 a[MT][S::A_LOADS];
+    u32x4 a[S::A_LOADS];
     template <bool FULL>
     __device__ __forceinline__ void load(const char *A, int64_t lda, int rows, int k_left, int lane) {
         const rsrc_t r = make_rsrc(A);
         const int g = lane / 16;
+        const int row = lane % 16;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int row = 16 * i + lane % 16;
-#pragma unroll
-            for (int s = 0; s < S::A_LOADS; ++s) {
-                const int k = 4 * S::PER * s + S::PER * g;
-                const int at = row < rows ? (row * (int)lda + k) * S::E : kOutOfRange;
-                const int left = row < rows ? k_left - k : 0;
-                if constexpr (FULL) a[i][s] = bload16(r, at, 0);
-                else {
-                    int here = at;
-                    asm volatile("" : "+v"(here));
-                    a[i][s] = bload16_n<S::E>(r, here, 0, left < 0 ? 0 : left);
-                    asm volatile("" : "+v"(a[i][s]) : : "memory");
-                }
+        for (int s = 0; s < S::A_LOADS; ++s) {
+            const int k = 4 * S::PER * s + S::PER * g;
+            const int at = row < rows ? (row * (int)lda + k) * S::E : kOutOfRange;
+            const int left = row < rows ? k_left - k : 0;
+            if constexpr (FULL) {
+                a[s] = bload16(r, at, 0);
+            } else {
+                int here = at;
+                asm volatile("" : "+v"(here));
+                a[s] = bload16_n<S::E>(r, here, 0, left < 0 ? 0 : left);
+                asm volatile("" : "+v"(a[s]) : : "memory");
             }
         }
     }
 };
 
-template <int DT, bool TRANS, int MT>
-__device__ __forceinline__ void stream_mma(const StreamB<DT, TRANS> &b, const StreamA<DT, TRANS, MT> &a,
-                                           f32x4 (&acc)[MT][StreamShape<DT, TRANS>::FRAGS]) {
+template <int DT, bool TRANS>
+__device__ __forceinline__ void stream_mma(const StreamB<DT, TRANS> &b, const StreamA<DT, TRANS> &a,
+                                           f32x4 (&acc)[StreamShape<DT, TRANS>::FRAGS]) {
     using S = StreamShape<DT, TRANS>;
     if constexpr (DT == DT_F32) {
 #pragma unroll
@@ -131,33 +128,26 @@ __device__ __forceinline__ void stream_mma(const StreamB<DT, TRANS> &b, const St
             for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int j = 0; j < S::FRAGS; ++j) {
-                    const uint32_t w = TRANS ? b.q[4 * j + s][e] : b.q[4 * s + e][j];
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        const uint32_t x = a.a[i][s][e];
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, w),
-                                                                        __builtin_bit_cast(float, x), acc[i][j], 0, 0, 0);
-                    }
+                    const uint32_t w = TRANS ? b.q[4 * j + s][e] : b.q[4 * s + e][j], x = a.a[s][e];
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, w),
+                                                                 __builtin_bit_cast(float, x), acc[j], 0, 0, 0);
                 }
     } else if constexpr (TRANS) {
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < MT; ++i) mfma_chunk<DT>(b.q[4 * j + s], a.a[i][s], acc[i][j]);
+            for (int j = 0; j < 2; ++j) mfma_chunk<DT>(b.q[4 * j + s], a.a[s], acc[j]);
     } else {
         u32x4 f[8];
         transpose_square<2>(b.q, f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) mfma_chunk<DT>(f[j], a.a[i][0], acc[i][j]);
+        for (int j = 0; j < 8; ++j) mfma_chunk<DT>(f[j], a.a[0], acc[j]);
     }
 }
 
-// grid: column strips x (experts + 1); the last takes the rows without an expert.
-template <int DT, bool TRANS, int MT>
+// grid: column strips x (experts + 1; the last takes the rows without an expert) x the
+// row tiles taken at the same time, which read the weights again from cache.
+template <int DT, bool TRANS>
 __global__ __launch_bounds__(512) void grouped_stream_kernel(GroupedParams p) {
     using S = StreamShape<DT, TRANS>;
     extern __shared__ f32x4 stream_lds[];           // [waves][FRAGS][64]
@@ -170,15 +160,13 @@ __global__ __launch_bounds__(512) void grouped_stream_kernel(GroupedParams p) {
     const int stages = e == p.experts ? 0 : (p.K + S::K - 1) / S::K;
     const char *B = p.B + (e == p.experts ? 0 : (int64_t)e * p.sB) * S::E + (TRANS ? n0 * p.ldb : (int64_t)n0) * S::E;
     const int64_t b_step = (TRANS ? (int64_t)S::K : S::K * p.ldb) * S::E;
-    for (int r0 = span.lo; r0 < span.hi; r0 += 16 * MT) {
-        const int rows = span.hi - r0 < 16 * MT ? span.hi - r0 : 16 * MT;
+    for (int r0 = span.lo + 16 * (int)blockIdx.z; r0 < span.hi; r0 += 16 * (int)gridDim.z) {
+        const int rows = span.hi - r0 < 16 ? span.hi - r0 : 16;
         const char *A = p.A + (int64_t)r0 * p.lda * S::E;
-        f32x4 acc[MT][S::FRAGS];
+        f32x4 acc[S::FRAGS];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < S::FRAGS; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-        auto fetch = [&](int s, StreamB<DT, TRANS> &b, StreamA<DT, TRANS, MT> &a, auto full) {
+        for (int j = 0; j < S::FRAGS; ++j) acc[j] = f32x4{0, 0, 0, 0};
+        auto fetch = [&](int s, StreamB<DT, TRANS> &b, StreamA<DT, TRANS> &a, auto full) {
             constexpr bool FULL = decltype(full)::value;
             const int k_left = p.K - s * S::K;
             b.template load<FULL>(B + s * b_step, p.ldb, n_left, k_left, lane);
@@ -191,14 +179,14 @@ __global__ __launch_bounds__(512) void grouped_stream_kernel(GroupedParams p) {
         if (s < whole) {
             const std::true_type full;
             StreamB<DT, TRANS> b0, b1;
-            StreamA<DT, TRANS, MT> a0, a1;
+            StreamA<DT, TRANS> a0, a1;
             fetch(s, b0, a0, full);
             for (;;) {
                 s += waves;
                 const bool more = s < whole;
                 if (more) fetch(s, b1, a1, full);
                 __builtin_amdgcn_sched_barrier(0);
-                stream_mma<DT, TRANS, MT>(b0, a0, acc);
+                stream_mma<DT, TRANS>(b0, a0, acc);
                 if (!more) break;
                 b0 = b1;
                 a0 = a1;
@@ -206,51 +194,42 @@ __global__ __launch_bounds__(512) void grouped_stream_kernel(GroupedParams p) {
         }
         for (; s < stages; s += waves) {
             StreamB<DT, TRANS> b;
-            StreamA<DT, TRANS, MT> a;
+            StreamA<DT, TRANS> a;
             fetch(s, b, a, std::false_type{});
-            stream_mma<DT, TRANS, MT>(b, a, acc);
+            stream_mma<DT, TRANS>(b, a, acc);
         }
-        for (int i = 0; i < MT; ++i) {
-            if (16 * i >= rows) break;
 #pragma unroll
-            for (int j = 0; j < S::FRAGS; ++j) {
-                f32x4 v = acc[0][j];
-#pragma unroll
-                for (int m = 1; m < MT; ++m)
-                    if (m == i) v = acc[m][j];
-                stream_lds[(wave * S::FRAGS + j) * 64 + lane] = v;
+        for (int j = 0; j < S::FRAGS; ++j) stream_lds[(wave * S::FRAGS + j) * 64 + lane] = acc[j];
+        __syncthreads();
+        // wave w sums and stores value w, w + waves, ... of the tile's four: the FRAGS
+        // columns of a value are neighbours (B as stored), the four values of a
+        // fragment are (B transposed)
+        const int r = r0 + lane % 16, g = lane / 16;
+        if constexpr (TRANS) {
+            for (int j = wave; j < S::FRAGS; j += waves) {
+                f32x4 v = stream_lds[j * 64 + lane];
+                for (int w = 1; w < waves; ++w) v += stream_lds[(w * S::FRAGS + j) * 64 + lane];
+                const int n = 16 * j + 4 * g;
+                if (r < span.hi && n < n_left)
+                    store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, v);
             }
-            __syncthreads();
-            // wave w sums and stores value w, w + waves, ... of the tile's four: the FRAGS
-            // columns of a value are neighbours (B as stored), the four values of a
-            // fragment are (B transposed)
-            const int r = r0 + 16 * i + lane % 16, g = lane / 16;
-            if constexpr (TRANS) {
-                for (int j = wave; j < S::FRAGS; j += waves) {
-                    f32x4 v = stream_lds[j * 64 + lane];
-                    for (int w = 1; w < waves; ++w) v += stream_lds[(w * S::FRAGS + j) * 64 + lane];
-                    const int n = 16 * j + 4 * g;
-                    if (r < span.hi && n < n_left)
-                        store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, v);
-                }
-            } else {
-                for (int q = wave; q < S::FRAGS; q += waves) {      // (value, four fragments)
-                    const int v = q / (S::FRAGS / 4), j0 = 4 * (q % (S::FRAGS / 4));
-                    f32x4 x;
+        } else {
+            for (int q = wave; q < S::FRAGS; q += waves) {      // (value, four fragments)
+                const int v = q / (S::FRAGS / 4), j0 = 4 * (q % (S::FRAGS / 4));
+                f32x4 x;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float *at = reinterpret_cast<const float *>(stream_lds + (j0 + j) * 64 + lane) + v;
-                        float y = at[0];
-                        for (int w = 1; w < waves; ++w) y += at[w * S::FRAGS * 256];
-                        x[j] = y;
-                    }
-                    const int n = S::PER * (4 * g + v) + j0;
-                    if (r < span.hi && n < n_left)
-                        store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, x);
+                for (int j = 0; j < 4; ++j) {
+                    const float *at = reinterpret_cast<const float *>(stream_lds + (j0 + j) * 64 + lane) + v;
+                    float y = at[0];
+                    for (int w = 1; w < waves; ++w) y += at[w * S::FRAGS * 256];
+                    x[j] = y;
                 }
+                const int n = S::PER * (4 * g + v) + j0;
+                if (r < span.hi && n < n_left)
+                    store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, x);
             }
-            __syncthreads();
         }
+        __syncthreads();
     }
 }
 
