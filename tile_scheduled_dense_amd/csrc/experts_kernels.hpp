@@ -18,9 +18,12 @@ tg_status launch_stream(const GroupedParams &p, hipStream_t s) {
     using S = StreamShape<DT, TRANS>;
     const int64_t stages = cdiv(p.K, S::K);
     const int waves = stages >= 16 ? 8 : (stages >= 8 ? 4 : 2);
-    // row tiles at the same time: twice an expert's on average, for uneven experts
-    const int64_t tiles = cdiv(2 * cdiv(p.rows, p.experts), 16);
-    const dim3 grid((unsigned)cdiv(p.N, S::COLS), (unsigned)p.experts + 1, (unsigned)(tiles < 8 ? tiles : 8));
+    // Row tiles at the same time: all there can be, if one expert had every row, while
+    // that is two workgroups a CU at most; else twice an expert's on average.
+    const int64_t strips = cdiv(p.N, S::COLS), mean = cdiv(2 * cdiv(p.rows, p.experts), 16);
+    int64_t tiles = cdiv(p.rows, 16) < 8 ? cdiv(p.rows, 16) : 8;
+    while (tiles > 1 && tiles > mean && strips * (p.experts + 1) * tiles > 512) --tiles;
+    const dim3 grid((unsigned)strips, (unsigned)p.experts + 1, (unsigned)tiles);
     hipLaunchKernelGGL((grouped_stream_kernel<DT, TRANS>), grid, dim3(64 * waves), waves * S::FRAGS * 1024, s, p);
     return launched();
 }
