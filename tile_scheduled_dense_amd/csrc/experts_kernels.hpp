@@ -107,7 +107,8 @@ constexpr int64_t kLong = 1024;
 //    4096, 4 rows 13.6 us against 17.6 on tiles; one of 4096 x 256, 16 rows 14.5 against
 //    45.6, 96 rows 14.6 against 45.9; 4 of 2048 x 2048, 24 rows 11.1 against 24.3; but 32
 //    of 2048 x 1024, 4 rows, 31.5 against 24.6, where the tiles' copies read at 5.5 TB/s,
-//    and two workgroups a CU, 8 experts of 1024 x 4096, 32 rows, 28.7 against 18.1).  So is an N below a chunk, which is not for the tiles (grouped_ring.hpp).
+//    and two workgroups a CU, 8 experts of 1024 x 4096, 32 rows, 28.7 against 18.1).  So
+//    is an N below a chunk, which is not for the tiles (grouped_ring.hpp).
 //  * 16 bits: 256 x 256 over a long K from 128 such tiles on (f16, 8 uneven experts, K
 //    1024: 4096 x 2048 32.0 against 33.4 us on 128 x 128, 2048 x 2048 26.5 against 22.6),
 //    else 128 x 128, three LDS copies for three workgroups a CU (257 x 1000 over 150 rows

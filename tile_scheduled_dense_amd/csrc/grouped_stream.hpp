@@ -1,9 +1,10 @@
 // grouped_stream.hpp -- expert products with few rows an expert: C[r] = A[r] .
 // B[g], bound by the bytes of the experts' weights.
 //
-// The weights go from HBM straight to registers, every byte once (per 16 rows), and no LDS lies between: at a few rows a weight is used by a single
-// matrix instruction.  A workgroup takes a strip of columns of one expert, its
-// waves split K stage by stage, and their sums are added in LDS in wave order.
+// The weights go from HBM straight to registers, every byte once per 16 rows, and
+// no LDS lies between: at a few rows a weight is used by a single matrix
+// instruction.  A workgroup takes a strip of columns of one expert, its waves
+// split K stage by stage, and their sums are added in LDS in wave order.
 // The weights are the matrix instruction's first operand and the tokens its
 // second, so that a lane holds neighbouring columns of one row of C.
 //
