@@ -65,7 +65,7 @@
 extern "C" {
 #endif
 
-#define TILE_GEMM_EXPERTS_VERSION 1
+#define TILE_GEMM_EXPERTS_VERSION 2    /* 2: the plan queries */
 #define TILE_GEMM_MAX_EXPERTS 2048
 
 int tile_gemm_experts_version(void);
@@ -146,6 +146,38 @@ tg_status tile_gemm_pack_q4(int64_t experts, int64_t N, int64_t K, int64_t group
 tg_status tile_gemm_q4(int64_t experts, int64_t rows, int64_t N, int64_t K, int64_t group, tg_dtype dtype,
                        const void *A, int64_t lda, const void *packed, void *C, int64_t ldc, tg_dtype c_dtype,
                        const int32_t *offsets, void *stream);
+
+/*
+ * The kernel and grid a product would be launched with (pure host arithmetic on
+ * sizes and types; no device is needed).  The arguments are the calls' own and
+ * are refused as they are there; rows, N or M of 0: kernel TG_EXPERTS_NOTHING.
+ */
+typedef enum {
+    TG_EXPERTS_NOTHING = 0,
+    TG_EXPERTS_STREAM = 1,     /* weights streamed to registers, the waves of a workgroup split K */
+    TG_EXPERTS_TILES = 2,      /* block tiles through LDS */
+    TG_EXPERTS_NARROW = 3,     /* the weights' gradient of an extent below one chunk */
+    TG_EXPERTS_Q4 = 4          /* 4-bit weights */
+} tg_experts_kernel;
+
+typedef struct {
+    int kernel;                /* tg_experts_kernel */
+    int tile_m, tile_n;        /* rows and columns of the result a workgroup holds at a time */
+    int pieces;                /* 1: short last tile rows and part-filled rounds in quarters of the tile */
+    int pipeline;              /* tiles: 1: fragments a K tile ahead in registers */
+    int waves;                 /* of a workgroup */
+    int past_caches;           /* tiles: 1: whole tiles are stored past the caches */
+    int pad_;
+    int64_t workgroups;
+    int64_t row_tiles;         /* tiles of rows one workgroup takes in turn at most, however the rows are split */
+} tg_experts_plan_info;
+
+tg_status tile_gemm_grouped_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed,
+                                 tg_dtype c_dtype, tg_experts_plan_info *out);
+tg_status tile_gemm_grouped_wgrad_plan(int64_t experts, int64_t rows, int64_t M, int64_t N, tg_dtype dtype,
+                                       tg_dtype c_dtype, tg_experts_plan_info *out);
+tg_status tile_gemm_q4_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, int64_t group, tg_dtype dtype,
+                            tg_dtype c_dtype, tg_experts_plan_info *out);
 
 #ifdef __cplusplus
 }

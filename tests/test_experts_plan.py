@@ -1,0 +1,97 @@
+"""The plan queries of the expert products (include/tile_gemm_experts.h) on the CPU: refusals, and the
+kernel that each case of tests/expert_cases.py is there for."""
+import ctypes
+
+import pytest
+
+import tile_scheduled_dense_amd as tg
+from tests import expert_cases as cases
+
+OK, INVALID, UNSUPPORTED = tg.TG_OK, tg.TG_ERR_INVALID_ARG, tg.TG_ERR_UNSUPPORTED
+
+
+def has(plan, **want):
+    assert {k: plan[k] for k in want} == want
+
+
+@pytest.mark.parametrize("transposed", [0, 1])
+@pytest.mark.parametrize("dt,out,sizes,spare,N,K,pad,skew", cases.TILE256, ids=lambda v: str(v)[:30])
+def test_products_on_the_largest_tile(dt, out, sizes, spare, N, K, pad, skew, transposed):
+    plan = tg.tile_gemm_grouped_plan(len(sizes), sum(sizes) + spare, N, K, dt, c_dtype=out, transposed=transposed)
+    has(plan, kernel="tiles", tile_m=256, tile_n=256, pieces=1, pipeline=1)
+
+
+def test_the_largest_tile_is_stored_both_ways():
+    past = {tg.tile_gemm_grouped_plan(len(s), sum(s) + x, N, K, dt, c_dtype=o)["past_caches"]
+            for dt, o, s, x, N, K, _, _ in cases.TILE256}
+    grad = {tg.tile_gemm_grouped_wgrad_plan(len(s), sum(s) + x, M, N, dt, c_dtype=o)["past_caches"]
+            for dt, o, s, x, M, N, _, _ in cases.WGRAD256}
+    assert past == grad == {0, 1}
+
+
+@pytest.mark.parametrize("dt,out,sizes,spare,M,N,pad,skew", cases.WGRAD256, ids=lambda v: str(v)[:30])
+def test_weight_gradients_on_the_largest_tile(dt, out, sizes, spare, M, N, pad, skew):
+    plan = tg.tile_gemm_grouped_wgrad_plan(len(sizes), sum(sizes) + spare, M, N, dt, c_dtype=out)
+    has(plan, kernel="tiles", tile_m=256, tile_n=256, pieces=0, pipeline=1)
+
+
+@pytest.mark.parametrize("dt,experts,rows,spare,active,N,K,pad,skew,transposed", cases.STREAM8, ids=lambda v: str(v))
+def test_streamed_weights_in_eight_waves(dt, experts, rows, spare, active, N, K, pad, skew, transposed):
+    has(tg.tile_gemm_grouped_plan(experts, rows + spare, N, K, dt, transposed=transposed), kernel="stream", waves=8)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("tile,experts,rows,spare,active,N,K,pad", cases.Q4_TILES, ids=lambda v: str(v))
+def test_tiles_of_4_bit_products(tile, experts, rows, spare, active, N, K, pad, dt, group):
+    plan = tg.tile_gemm_q4_plan(experts, rows + spare, N, K, group, dt)
+    has(plan, kernel="q4", tile_m=tile[0], tile_n=tile[1])
+
+
+def test_small_tiles():
+    """The tiles below the largest, by type and form."""
+    has(tg.tile_gemm_grouped_plan(33, 5001, 1000, 257, "f16"), kernel="tiles", tile_m=128, pieces=0, pipeline=0)
+    has(tg.tile_gemm_grouped_plan(4, 2048, 1024, 512, "f32"), kernel="tiles", tile_m=64, pieces=0, pipeline=1)
+    has(tg.tile_gemm_grouped_wgrad_plan(33, 5001, 257, 1000, "f16"), kernel="tiles", tile_m=128, pipeline=0)
+    has(tg.tile_gemm_grouped_wgrad_plan(2, 1464, 464, 96, "bf16"), kernel="tiles", tile_m=128, pipeline=1)
+    has(tg.tile_gemm_grouped_wgrad_plan(4, 2048, 512, 1024, "f32"), kernel="tiles", tile_m=64, pipeline=1)
+    has(tg.tile_gemm_grouped_wgrad_plan(2, 500, 3, 1024, "bf16"), kernel="narrow")
+    has(tg.tile_gemm_q4_plan(1, 37, 1001, 4100, 32, "f32"), kernel="q4", tile_m=16, tile_n=16)
+
+
+def test_a_product_of_nothing():
+    nothing = dict(kernel="nothing", workgroups=0)
+    has(tg.tile_gemm_grouped_plan(4, 0, 32, 48, "bf16"), **nothing)
+    has(tg.tile_gemm_grouped_plan(4, 9, 0, 48, "bf16"), **nothing)
+    has(tg.tile_gemm_grouped_wgrad_plan(4, 9, 0, 48, "bf16"), **nothing)
+    has(tg.tile_gemm_q4_plan(4, 0, 32, 48, 32, "bf16"), **nothing)
+    # a sum of nothing is written
+    assert tg.tile_gemm_grouped_plan(4, 9, 32, 0, "bf16")["workgroups"] > 0
+    assert tg.tile_gemm_grouped_wgrad_plan(4, 0, 32, 48, "bf16")["workgroups"] > 0
+
+
+OUT = tg.ExpertsPlanInfo()
+ARGS = {
+    "tile_gemm_grouped_plan": dict(experts=4, rows=64, N=32, K=48, dtype=1, transposed=0, c_dtype=1),
+    "tile_gemm_grouped_wgrad_plan": dict(experts=4, rows=64, M=48, N=32, dtype=1, c_dtype=0),
+    "tile_gemm_q4_plan": dict(experts=4, rows=64, N=32, K=48, group=32, dtype=2, c_dtype=2),
+}
+
+
+def ask(fn, out=None, **kw):
+    out = ctypes.byref(OUT) if out is None else out
+    return int(getattr(tg._lib(), fn)(*{**ARGS[fn], **kw}.values(), out))
+
+
+@pytest.mark.parametrize("fn", list(ARGS))
+def test_plan_refusals(fn):
+    assert ask(fn) == OK
+    assert ask(fn, out=ctypes.POINTER(tg.ExpertsPlanInfo)()) == INVALID
+    for kw in (dict(experts=0), dict(rows=-1), dict(N=-1), dict(dtype=3), dict(c_dtype=3), dict(dtype=0, c_dtype=1)):
+        assert ask(fn, **kw) == INVALID, kw
+    assert ask(fn, experts=2049) == UNSUPPORTED
+    assert ask(fn, rows=(1 << 30) + 1) == UNSUPPORTED
+    if fn == "tile_gemm_grouped_plan":
+        assert ask(fn, transposed=2) == INVALID
+    if fn == "tile_gemm_q4_plan":
+        assert ask(fn, group=0) == INVALID and ask(fn, group=48) == UNSUPPORTED

@@ -54,8 +54,8 @@ EXPORTED = ["tile_gemm", "tile_gemm_strided_batched", "tile_gemm_ex", "tile_gemm
 EXPORTED_EXPERTS = ["tile_gemm_experts_version", "tile_gemm_expert_sort_workspace_size", "tile_gemm_expert_sort",
                     "tile_gemm_expert_gather", "tile_gemm_expert_combine", "tile_gemm_expert_combine_grad",
                     "tile_gemm_grouped", "tile_gemm_grouped_wgrad", "tile_gemm_q4_packed_size", "tile_gemm_pack_q4",
-                    "tile_gemm_q4"]
-EXPERTS_VERSION = 1     # TILE_GEMM_EXPERTS_VERSION
+                    "tile_gemm_q4", "tile_gemm_grouped_plan", "tile_gemm_grouped_wgrad_plan", "tile_gemm_q4_plan"]
+EXPERTS_VERSION = 2     # TILE_GEMM_EXPERTS_VERSION
 MAX_EXPERTS = 2048      # TILE_GEMM_MAX_EXPERTS
 
 
@@ -95,6 +95,19 @@ class PlanInfo(ctypes.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+EXPERTS_KERNELS = ["nothing", "stream", "tiles", "narrow", "q4"]     # tg_experts_kernel
+
+
+class ExpertsPlanInfo(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("kernel", "tile_m", "tile_n", "pieces", "pipeline", "waves", "past_caches",
+                                            "pad_")] + [("workgroups", ctypes.c_int64), ("row_tiles", ctypes.c_int64)]
+
+    def as_dict(self):
+        d = {f: getattr(self, f) for f, _ in self._fields_ if f != "pad_"}
+        d["kernel"] = EXPERTS_KERNELS[self.kernel]
+        return d
 
 
 class Iter(ctypes.Structure):
@@ -170,6 +183,7 @@ def _lib():
 def _declare_experts(lib, i64, vp, ci):
     """Argument types of the mixture-of-experts operators (include/tile_gemm_experts.h)."""
     size = ctypes.POINTER(i64)
+    info = ctypes.POINTER(ExpertsPlanInfo)
     for name, args in {
         "tile_gemm_experts_version": [],
         "tile_gemm_expert_sort_workspace_size": [i64, i64, i64, size],
@@ -182,6 +196,9 @@ def _declare_experts(lib, i64, vp, ci):
         "tile_gemm_q4_packed_size": [i64, i64, i64, i64, ci, size],
         "tile_gemm_pack_q4": [i64, i64, i64, i64, ci, vp, i64, i64, vp, i64, i64, vp, i64, vp],
         "tile_gemm_q4": [i64, i64, i64, i64, i64, ci, vp, i64, vp, vp, i64, ci, vp, vp],
+        "tile_gemm_grouped_plan": [i64, i64, i64, i64, ci, ci, ci, info],
+        "tile_gemm_grouped_wgrad_plan": [i64, i64, i64, i64, ci, ci, info],
+        "tile_gemm_q4_plan": [i64, i64, i64, i64, i64, ci, ci, info],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ci
@@ -418,6 +435,27 @@ def tile_gemm_q4(experts, rows, N, K, group, dtype, A, lda, packed, C, ldc, offs
     expert with every row."""
     _check(_lib().tile_gemm_q4(experts, rows, N, K, group, _dtype(dtype), _addr(A), lda, _addr(packed), _addr(C),
                                ldc, _dtype(c_dtype), _addr(offsets), _stream(stream)), "tile_gemm_q4")
+
+
+def _experts_plan(fn, *args) -> dict:
+    info = ExpertsPlanInfo()
+    _check(getattr(_lib(), fn)(*args, ctypes.byref(info)), fn)
+    return info.as_dict()
+
+
+def tile_gemm_grouped_plan(experts, rows, N, K, dtype, c_dtype="f32", transposed=0) -> dict:
+    """The kernel ("stream", "tiles", ...) and grid of a tile_gemm_grouped call."""
+    return _experts_plan("tile_gemm_grouped_plan", experts, rows, N, K, _dtype(dtype), int(transposed), _dtype(c_dtype))
+
+
+def tile_gemm_grouped_wgrad_plan(experts, rows, M, N, dtype, c_dtype="f32") -> dict:
+    """The kernel ("tiles", "narrow") and grid of a tile_gemm_grouped_wgrad call."""
+    return _experts_plan("tile_gemm_grouped_wgrad_plan", experts, rows, M, N, _dtype(dtype), _dtype(c_dtype))
+
+
+def tile_gemm_q4_plan(experts, rows, N, K, group, dtype, c_dtype="f32") -> dict:
+    """The tile and grid of a tile_gemm_q4 call."""
+    return _experts_plan("tile_gemm_q4_plan", experts, rows, N, K, group, _dtype(dtype), _dtype(c_dtype))
 
 
 def make_layout(shape, shard, replica=(), offset=None, swizzle=None) -> Layout:

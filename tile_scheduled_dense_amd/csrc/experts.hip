@@ -1,13 +1,12 @@
 // experts.hip -- the C ABI of the operators of a mixture-of-experts layer:
-// argument checks and launches on the caller's stream.  Declarations and
+// argument checks, launches on the caller's stream, plan queries.  Declarations and
 // contracts are in include/tile_gemm_experts.h.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 
 #include "exchange.hpp"
-#include "experts.hpp"
-#include "ranges.hpp"
+#include "experts_plan.hpp"
 #include "tile_gemm_experts.h"
 
 using namespace tg;
@@ -252,19 +251,29 @@ tg_status combine_grad(int64_t tokens, int64_t top_k, int64_t cols, tg_dtype dty
 }
 
 // What the products of both kinds have in common.
-tg_status product_arguments(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, tg_dtype c_dtype,
-                            const int32_t *offsets) {
+tg_status product_sizes(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, tg_dtype c_dtype) {
     if (experts < 1 || rows < 0 || N < 0 || K < 0 || !known(dtype)) return TG_ERR_INVALID_ARG;
     if (c_dtype != TG_F32 && c_dtype != dtype) return TG_ERR_INVALID_ARG;
-    if ((!offsets && experts != 1) || !aligned(offsets, 4)) return TG_ERR_INVALID_ARG;
     if (experts > TILE_GEMM_MAX_EXPERTS || rows > kMaxExtent || N > kMaxExtent || K > kMaxExtent)
         return TG_ERR_UNSUPPORTED;
     return TG_OK;
+}
+tg_status product_arguments(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, tg_dtype c_dtype,
+                            const int32_t *offsets) {
+    const tg_status st = product_sizes(experts, rows, N, K, dtype, c_dtype);
+    if (st == TG_ERR_INVALID_ARG || (!offsets && experts != 1) || !aligned(offsets, 4)) return TG_ERR_INVALID_ARG;
+    return st;
 }
 
 // whether operands and result together exceed the last-level cache (GroupedParams::past)
 bool past_caches(int64_t operand_bytes, int64_t result_bytes) {
     return operand_bytes + result_bytes > (int64_t(256) << 20);
+}
+bool grouped_past(int64_t experts, int64_t rows, int64_t N, int64_t K, int esz, int csz) {
+    return past_caches((rows * K + experts * N * K) * esz, rows * N * csz);
+}
+bool wgrad_past(int64_t experts, int64_t rows, int64_t M, int64_t N, int esz, int csz) {
+    return past_caches(rows * (M + N) * esz, experts * M * N * csz);
 }
 
 // A block's tile of an operand (256 rows of ld elements at most) is addressed
@@ -305,7 +314,7 @@ tg_status grouped(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype 
     p.N = (int)N;
     p.K = (int)K;
     p.c_f32 = c_dtype == TG_F32;
-    p.past = past_caches((rows * K + experts * N * K) * esz, rows * N * csz);
+    p.past = grouped_past(experts, rows, N, K, esz, csz);
     hipStream_t s = static_cast<hipStream_t>(stream);
     switch (dtype) {
         case TG_F32: return launch_grouped<DT_F32>(p, transposed != 0, s);
@@ -347,7 +356,7 @@ tg_status wgrad(int64_t experts, int64_t rows, int64_t M, int64_t N, tg_dtype dt
     p.M = (int)M;
     p.N = (int)N;
     p.c_f32 = c_dtype == TG_F32;
-    p.past = past_caches(rows * (M + N) * esz, experts * M * N * csz);
+    p.past = wgrad_past(experts, rows, M, N, esz, csz);
     hipStream_t s = static_cast<hipStream_t>(stream);
     switch (dtype) {
         case TG_F32: return launch_wgrad<DT_F32>(p, s);
@@ -445,6 +454,62 @@ tg_status q4(int64_t experts, int64_t rows, int64_t N, int64_t K, int64_t group,
     return TG_ERR_INTERNAL;
 }
 
+tg_status answer(const ProductPlan &plan, bool past, tg_experts_plan_info *out) {
+    *out = plan.info;
+    out->past_caches = plan.info.kernel == TG_EXPERTS_TILES && past;
+    return TG_OK;
+}
+
+tg_status grouped_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed,
+                       tg_dtype c_dtype, tg_experts_plan_info *out) {
+    const tg_status st = product_sizes(experts, rows, N, K, dtype, c_dtype);
+    if (st == TG_ERR_INVALID_ARG || (transposed != 0 && transposed != 1) || !out) return TG_ERR_INVALID_ARG;
+    if (st != TG_OK) return st;
+    *out = {};
+    if (rows == 0 || N == 0) return TG_OK;
+    const bool past = grouped_past(experts, rows, N, K, size_of(dtype), size_of(c_dtype));
+    switch (dtype) {
+        case TG_F32: return answer(plan_grouped<DT_F32>(transposed != 0, experts, rows, N, K), past, out);
+        case TG_BF16: return answer(plan_grouped<DT_BF16>(transposed != 0, experts, rows, N, K), past, out);
+        case TG_F16: return answer(plan_grouped<DT_F16>(transposed != 0, experts, rows, N, K), past, out);
+    }
+    return TG_ERR_INTERNAL;
+}
+
+tg_status wgrad_plan(int64_t experts, int64_t rows, int64_t M, int64_t N, tg_dtype dtype, tg_dtype c_dtype,
+                     tg_experts_plan_info *out) {
+    const tg_status st = product_sizes(experts, rows, N, M, dtype, c_dtype);
+    if (st == TG_ERR_INVALID_ARG || !out) return TG_ERR_INVALID_ARG;
+    if (st != TG_OK) return st;
+    *out = {};
+    if (M == 0 || N == 0) return TG_OK;
+    const bool past = wgrad_past(experts, rows, M, N, size_of(dtype), size_of(c_dtype));
+    switch (dtype) {
+        case TG_F32: return answer(plan_wgrad<DT_F32>(experts, rows, M, N), past, out);
+        case TG_BF16: return answer(plan_wgrad<DT_BF16>(experts, rows, M, N), past, out);
+        case TG_F16: return answer(plan_wgrad<DT_F16>(experts, rows, M, N), past, out);
+    }
+    return TG_ERR_INTERNAL;
+}
+
+tg_status q4_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, int64_t group, tg_dtype dtype, tg_dtype c_dtype,
+                  tg_experts_plan_info *out) {
+    tg_status st = product_sizes(experts, rows, N, K, dtype, c_dtype);
+    if (st == TG_ERR_INVALID_ARG || !out) return TG_ERR_INVALID_ARG;
+    if (st != TG_OK) return st;
+    Q4Shape shape;
+    st = q4_arguments(experts, N, K, group, dtype, shape);
+    if (st != TG_OK) return st;
+    *out = {};
+    if (rows == 0 || N == 0) return TG_OK;
+    switch (dtype) {
+        case TG_F32: return answer(plan_q4<DT_F32>(experts, rows, N, K), false, out);
+        case TG_BF16: return answer(plan_q4<DT_BF16>(experts, rows, N, K), false, out);
+        case TG_F16: return answer(plan_q4<DT_F16>(experts, rows, N, K), false, out);
+    }
+    return TG_ERR_INTERNAL;
+}
+
 }  // namespace
 
 // no exception leaves the library
@@ -527,6 +592,21 @@ tg_status tile_gemm_q4(int64_t experts, int64_t rows, int64_t N, int64_t K, int6
                        const void *A, int64_t lda, const void *packed, void *C, int64_t ldc, tg_dtype c_dtype,
                        const int32_t *offsets, void *stream) {
     TG_GUARD(q4(experts, rows, N, K, group, dtype, A, lda, packed, C, ldc, c_dtype, offsets, stream))
+}
+
+tg_status tile_gemm_grouped_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed,
+                                 tg_dtype c_dtype, tg_experts_plan_info *out) {
+    TG_GUARD(grouped_plan(experts, rows, N, K, dtype, transposed, c_dtype, out))
+}
+
+tg_status tile_gemm_grouped_wgrad_plan(int64_t experts, int64_t rows, int64_t M, int64_t N, tg_dtype dtype,
+                                       tg_dtype c_dtype, tg_experts_plan_info *out) {
+    TG_GUARD(wgrad_plan(experts, rows, M, N, dtype, c_dtype, out))
+}
+
+tg_status tile_gemm_q4_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, int64_t group, tg_dtype dtype,
+                            tg_dtype c_dtype, tg_experts_plan_info *out) {
+    TG_GUARD(q4_plan(experts, rows, N, K, group, dtype, c_dtype, out))
 }
 
 }  // extern "C"

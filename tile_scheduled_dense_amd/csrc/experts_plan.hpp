@@ -1,0 +1,164 @@
+// experts_plan.hpp -- which kernel an expert product takes and the grid it is
+// started with: host arithmetic on sizes and types alone, shared by the launches
+// (experts_kernels.hpp) and the plan queries of the C ABI (experts.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "experts.hpp"
+#include "ranges.hpp"
+#include "tile_gemm_experts.h"
+
+namespace tg {
+
+struct ProductPlan {
+    tg_experts_plan_info info;
+    int lds_copies;              // of a K tile (tiles)
+    int64_t gx;                  // workgroups: gx * gy * gz
+    unsigned gy, gz;
+};
+
+inline ProductPlan plan_of(int kernel, int tile_m, int tile_n, int waves, int64_t gx, int64_t gy = 1, int64_t gz = 1) {
+    ProductPlan p = {};
+    p.info.kernel = kernel;
+    p.info.tile_m = tile_m;
+    p.info.tile_n = tile_n;
+    p.info.waves = waves;
+    p.info.workgroups = gx * gy * gz;
+    p.info.row_tiles = 1;
+    p.gx = gx;
+    p.gy = (unsigned)gy;
+    p.gz = (unsigned)gz;
+    return p;
+}
+
+// Waves that split K: enough for two stages each, eight at most.
+template <int DT, bool TRANS>
+ProductPlan plan_stream(int64_t experts, int64_t rows, int64_t N, int64_t K) {
+    using S = StreamShape<DT, TRANS>;
+    const int64_t stages = cdiv(K, S::K);
+    const int waves = stages >= 16 ? 8 : (stages >= 8 ? 4 : 2);
+    // Row tiles at the same time: all there can be, if one expert had every row, while
+    // that is two workgroups a CU at most; else twice an expert's on average.
+    const int64_t strips = cdiv(N, S::COLS), mean = cdiv(2 * cdiv(rows, experts), 16);
+    int64_t tiles = cdiv(rows, 16) < 8 ? cdiv(rows, 16) : 8;
+    while (tiles > 1 && tiles > mean && strips * (experts + 1) * tiles > 512) --tiles;
+    ProductPlan p = plan_of(TG_EXPERTS_STREAM, 16, S::COLS, waves, strips, experts + 1, tiles);
+    p.info.row_tiles = cdiv(cdiv(rows, 16), tiles);
+    return p;
+}
+
+// the most tile rows that `groups` groups of `rows` rows together can have
+inline int64_t most_tiles(int64_t rows, int64_t groups, int64_t bm) {
+    const int64_t parts = rows < groups ? rows : groups;
+    return (rows + parts * (bm - 1)) / bm;
+}
+
+// The grid is the most there can be: whole tiles and, with pieces, three more for each
+// tile that is split, and a row of pieces for every group.
+inline ProductPlan plan_tiles(int64_t experts, int64_t rows, int64_t N, int tile, bool pieces, bool pipeline, int copies) {
+    int64_t grid = most_tiles(rows, experts + 1, tile) * cdiv(N, tile);
+    if (pieces) grid += 3 * kSplitRound + (rows < experts + 1 ? rows : experts + 1) * cdiv(N, tile / 2);
+    ProductPlan p = plan_of(TG_EXPERTS_TILES, tile, tile, 4, grid);
+    p.info.pieces = pieces;
+    p.info.pipeline = pipeline;
+    p.lds_copies = copies;
+    return p;
+}
+
+// A contraction long enough that the 256 x 256 tile's rate outweighs what its start
+// and its stores cost, which the two or three workgroups of 128 x 128 that a CU holds
+// hide in each other (bf16, 8 uneven experts: 16384 x 4096 over K 256 55 us on 128 x 128
+// against 70, 512 86 against 96, 8192 x 4096 over 1024 81 against 78; the weights'
+// gradient of 2048 x 2048 over 512 rows an expert 86 against 99, over 1024 75 against 74).
+constexpr int64_t kLong = 1024;
+
+// The tile of a product over rows.
+//  * The weights are streamed, by workgroups that split K among their waves, while they
+//    are at most 96 MiB and an expert has on average at most 8 rows, or at most 128 and
+//    a workgroup a CU takes all 16-row tiles at the same time (bf16: 8 experts of 1024 x
+//    4096, 4 rows 13.6 us against 17.6 on tiles; one of 4096 x 256, 16 rows 14.5 against
+//    45.6, 96 rows 14.6 against 45.9; 4 of 2048 x 2048, 24 rows 11.1 against 24.3; but 32
+//    of 2048 x 1024, 4 rows, 31.5 against 24.6, where the tiles' copies read at 5.5 TB/s,
+//    and two workgroups a CU, 8 experts of 1024 x 4096, 32 rows, 28.7 against 18.1).  So
+//    is an N below a chunk, which is not for the tiles (grouped_ring.hpp).
+//  * 16 bits: 256 x 256 over a long K from 128 such tiles on (f16, 8 uneven experts, K
+//    1024: 4096 x 2048 32.0 against 33.4 us on 128 x 128, 2048 x 2048 26.5 against 22.6),
+//    else 128 x 128, three LDS copies for three workgroups a CU (257 x 1000 over 150 rows
+//    18.9 us with four copies, 17.0 with three, 16.8 with two, which cost 5001 x 257 over
+//    1000 28.4 against 21.9).
+//  * fp32: 64 x 64, more workgroups for a matrix rate that 16 of them already fill
+//    (2048 x 1024 x 512 30 us against 42 on 128 x 128; 4096 x 4096 x 512 149, 173 and 163
+//    on 256 x 256), with the software pipeline (2048 x 1024 x 512 28 us, 30 without);
+//    256 x 256 from 800 tiles on (16384 x 4096 x 2048 1979 against 2147).
+template <int DT, bool TRANS>
+ProductPlan plan_grouped_as(int64_t experts, int64_t rows, int64_t N, int64_t K) {
+    const int64_t mean = cdiv(rows, experts);
+    const int64_t weights = experts * N * K * (DT == DT_F32 ? 4 : 2);
+    const int64_t strips = cdiv(N, StreamShape<DT, TRANS>::COLS) * experts * cdiv(mean, 16);
+    const bool stream = weights <= (int64_t(96) << 20) && (mean <= 8 || (mean <= 128 && strips < 256));
+    if (stream || N < 8) return plan_stream<DT, TRANS>(experts, rows, N, K);
+    const int64_t tiles = cdiv(rows, 256) * cdiv(N, 256);
+    if (K >= kLong && tiles >= (DT == DT_F32 ? 800 : 128)) return plan_tiles(experts, rows, N, 256, true, true, 4);
+    return DT == DT_F32 ? plan_tiles(experts, rows, N, 64, false, true, 4)
+                        : plan_tiles(experts, rows, N, 128, false, false, 3);
+}
+template <int DT>
+ProductPlan plan_grouped(bool transposed, int64_t experts, int64_t rows, int64_t N, int64_t K) {
+    return transposed ? plan_grouped_as<DT, true>(experts, rows, N, K) : plan_grouped_as<DT, false>(experts, rows, N, K);
+}
+
+// The tile of the weights' gradient, by the same rules; its contraction is an expert's
+// rows, on average.  256 x 256 from 200 tiles on (16 experts of 1024 x 1024: 29.8 us
+// against 32.2 on 128 x 128; 8 experts 35.9 against 32.1), unless 128 x 128 pads the
+// extents by a fifth less.  128 x 128 with the software pipeline where no CU has a
+// second tile to hide the first one's waits (464 x 96 over 1464 rows, 2 experts: 20.4 ->
+// 13.1 us; 33 of 257 x 1000 over 150 16.9 -> 20.9).
+template <int DT>
+ProductPlan plan_wgrad(int64_t experts, int64_t rows, int64_t M, int64_t N) {
+    if (M < 8 || N < 8) {
+        const int64_t blocks = cdiv(experts * M * N, 256);
+        return plan_of(TG_EXPERTS_NARROW, 1, 1, 4, blocks < 65536 ? blocks : 65536);
+    }
+    const int64_t each = cdiv(M, 256) * cdiv(N, 256), small = cdiv(M, 128) * cdiv(N, 128);
+    int tile = DT == DT_F32 ? 64 : 128;
+    bool pipeline = DT == DT_F32 || experts * small <= 256;
+    if (experts * each >= (DT == DT_F32 ? 800 : 200) && 4 * each * 4 <= 5 * small && cdiv(rows, experts) >= kLong) {
+        tile = 256;
+        pipeline = true;
+    }
+    ProductPlan p = plan_of(TG_EXPERTS_TILES, tile, tile, 4, experts * cdiv(cdiv(M, tile) * cdiv(N, tile), 8) * 8);
+    p.info.pipeline = pipeline;
+    p.lds_copies = pipeline ? 4 : 3;
+    return p;
+}
+
+// Row tiles (MT) and n tiles (NT) of a workgroup: more of either reads the codes or
+// the activations less often, as long as there are workgroups for the 256 CUs.
+// fp32 takes one of each, in as many workgroups: two row tiles leave room for half the
+// waves, whose latency then shows (37 rows, 1001 x 4100: 12 us against 28).
+// chunks: row tiles that an expert has on average.
+template <int DT>
+ProductPlan plan_q4(int64_t experts, int64_t rows, int64_t N, int64_t K) {
+    const int64_t n_tiles = cdiv(N, kQ4N), k_blocks = cdiv(K, kQ4K);
+    const int64_t chunks = cdiv(cdiv(rows, experts), 16) < 64 ? cdiv(cdiv(rows, experts), 16) : 64;
+    const int64_t all = n_tiles * experts;
+    int mt = 1, nt = 1, most = q4_waves<DT, 1>();
+    if (DT != DT_F32) {
+        if (chunks > 2 && all * cdiv(chunks, 4) >= 256) mt = 4, most = q4_waves<DT, 4>();
+        else if (chunks > 1 && all * cdiv(chunks, 2) >= 256) mt = 2, most = q4_waves<DT, 2>();
+        else if (all * chunks >= 512) nt = 2;
+    }
+    // waves that split K: more while they have four blocks each and there are not yet
+    // 4096 (a wave costs 0.6 ns to start: 64 experts of 2048 x 2048, 24 of them with
+    // rows, take 15 us in workgroups of 2 waves, 17 of 4, 27 of 8)
+    const int64_t strips = cdiv(n_tiles, nt);
+    int waves = 1;
+    while (waves < most && waves * 4 <= k_blocks && (waves < 2 || strips * experts * waves < 4096)) waves *= 2;
+    const int64_t gz = cdiv(chunks, mt);
+    ProductPlan p = plan_of(TG_EXPERTS_Q4, 16 * mt, 16 * nt, waves, strips, experts + 1, gz);
+    p.info.row_tiles = cdiv(cdiv(rows, 16 * mt), gz);
+    return p;
+}
+
+}  // namespace tg
