@@ -279,9 +279,17 @@ inline int row_group(int64_t chunks) {
 }
 // whether a call that moves so many bytes stores past the caches (gather_kernel)
 inline bool store_past(int64_t bytes) { return bytes > (int64_t(64) << 20); }
+// A dimension of a grid holds fewer than 2^32 threads: workgroups past kGridX lie in
+// further rows of it, the last of which may reach past the tokens.
+constexpr int64_t kGridX = int64_t(1) << 22;
+inline dim3 token_grid(int64_t tokens, int group) {
+    const int64_t per = 256 / group, blocks = (tokens + per - 1) / per;
+    return blocks <= kGridX ? dim3((unsigned)blocks) : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
+}
 template <bool NARROW>
-__device__ __forceinline__ int token_of(int group) {
-    const int t = (int)(blockIdx.x * (256 / group) + threadIdx.x / group);
+__device__ __forceinline__ uint32_t token_of(int group) {
+    const uint32_t block = blockIdx.y * (uint32_t)kGridX + blockIdx.x;
+    const uint32_t t = block * (256 / group) + threadIdx.x / group;
     return NARROW ? t : __builtin_amdgcn_readfirstlane(t);
 }
 
@@ -297,8 +305,8 @@ __global__ __launch_bounds__(256) void gather_kernel(const typename ElemOf<DT>::
                                                      typename ElemOf<DT>::type *__restrict__ rows, int64_t ldr,
                                                      int tokens, int top_k, int64_t cols, int group) {
     using R = Row<DT>;
-    const int t = token_of<NARROW>(group);
-    if (t >= tokens) return;
+    const uint32_t t = token_of<NARROW>(group);
+    if (t >= (uint32_t)tokens) return;
     const int n = tokens * top_k;
     const int32_t *row = row_of_entry + (int64_t)t * top_k;
     const int64_t chunks = (cols + R::PER - 1) / R::PER;
@@ -321,8 +329,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const typename ElemOf<DT>:
                                                       typename ElemOf<DT>::type *__restrict__ out, int64_t ldo,
                                                       int tokens, int top_k, int64_t cols, int group) {
     using R = Row<DT>;
-    const int t = token_of<NARROW>(group);
-    if (t >= tokens) return;
+    const uint32_t t = token_of<NARROW>(group);
+    if (t >= (uint32_t)tokens) return;
     const int n = tokens * top_k;
     const int32_t *row = row_of_entry + (int64_t)t * top_k;
     const int64_t chunks = (cols + R::PER - 1) / R::PER;
@@ -372,8 +380,9 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(const typename ElemOf
                                                            float *__restrict__ d_w, int64_t ld_dw, int tokens,
                                                            int top_k, int64_t cols, int group) {
     using R = Row<DT>;
-    const int t = token_of<NARROW>(group), lane = threadIdx.x % group;
-    if (t >= tokens) return;
+    const uint32_t t = token_of<NARROW>(group);
+    const int lane = threadIdx.x % group;
+    if (t >= (uint32_t)tokens) return;
     const int n = tokens * top_k;
     const int32_t *row = row_of_entry + (int64_t)t * top_k;
     const int64_t chunks = (cols + R::PER - 1) / R::PER;

@@ -109,7 +109,7 @@ tg_status gather(int64_t tokens, int64_t top_k, int64_t cols, tg_dtype dtype, co
     st = device_ok();
     if (st != TG_OK) return st;
     const int group = row_group(cdiv(cols * esz, 16));
-    const dim3 grid((unsigned)cdiv(tokens, 256 / group));
+    const dim3 grid = token_grid(tokens, group);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const bool past = store_past((n + tokens) * cols * esz);
 #define TG_GATHER(DT, PAST, NARROW)                                                                                \
@@ -142,7 +142,7 @@ void launch_combine(const void *y, int64_t ldy, const int32_t *row_of_entry, con
     // few choices: two chunks a thread, for as many loads in flight
     const int64_t chunks = cdiv(cols * (int64_t)sizeof(T), 16);
     const int group = row_group(choices(top_k) <= 2 ? cdiv(chunks, 2) : chunks);
-    const dim3 grid((unsigned)cdiv(tokens, 256 / group));
+    const dim3 grid = token_grid(tokens, group);
     const bool past = store_past((tokens * top_k + tokens) * cols * (int64_t)sizeof(T));
 #define TG_COMBINE_AS(JB, U, PAST, NARROW)                                                                        \
     hipLaunchKernelGGL((combine_kernel<DT, JB, U, PAST, NARROW>), grid, dim3(256), 0, s, static_cast<const T *>(y), ldy, \
@@ -195,7 +195,7 @@ void launch_combine_grad(const void *d_out, int64_t ldo, const void *y, int64_t 
                          int64_t tokens, int64_t top_k, int64_t cols, hipStream_t s) {
     typedef typename ElemOf<DT>::type T;
     const int rows = row_group(cdiv(cols * (int64_t)sizeof(T), 16)), group = rows < 64 ? rows : 64;
-    const dim3 grid((unsigned)cdiv(tokens, 256 / group));
+    const dim3 grid = token_grid(tokens, group);
     const bool past = store_past((2 * tokens * top_k + tokens) * cols * (int64_t)sizeof(T));
 #define TG_GRAD_AS(JB, PAST, NARROW)                                                                                \
     hipLaunchKernelGGL((combine_grad_kernel<DT, JB, PAST, NARROW>), grid, dim3(256), 0, s, static_cast<const T *>(d_out), \
