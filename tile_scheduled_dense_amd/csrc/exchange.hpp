@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include "expert_rows.hpp"
+#include "grid.hpp"
 
 namespace tg {
 
@@ -279,17 +280,10 @@ inline int row_group(int64_t chunks) {
 }
 // whether a call that moves so many bytes stores past the caches (gather_kernel)
 inline bool store_past(int64_t bytes) { return bytes > (int64_t(64) << 20); }
-// A dimension of a grid holds fewer than 2^32 threads: workgroups past kGridX lie in
-// further rows of it, the last of which may reach past the tokens.
-constexpr int64_t kGridX = int64_t(1) << 22;
-inline dim3 token_grid(int64_t tokens, int group) {
-    const int64_t per = 256 / group, blocks = (tokens + per - 1) / per;
-    return blocks <= kGridX ? dim3((unsigned)blocks) : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
-}
+inline dim3 token_grid(int64_t tokens, int group) { return wide_grid((tokens + 256 / group - 1) / (256 / group)); }
 template <bool NARROW>
 __device__ __forceinline__ uint32_t token_of(int group) {
-    const uint32_t block = blockIdx.y * (uint32_t)kGridX + blockIdx.x;
-    const uint32_t t = block * (256 / group) + threadIdx.x / group;
+    const uint32_t t = wide_block() * (256 / group) + threadIdx.x / group;
     return NARROW ? t : __builtin_amdgcn_readfirstlane(t);
 }
 

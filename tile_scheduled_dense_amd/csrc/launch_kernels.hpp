@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "gemm_ring.hpp"
+#include "grid.hpp"
 #include "launch.hpp"
 
 namespace tg {
@@ -13,7 +14,7 @@ namespace {
 
 template <class C, int DEPTH, int SWZ, bool TAIL = false>
 tg_status launch_one(const GemmParams &gp, int64_t grid, hipStream_t stream) {
-    if (grid > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
+    if (!grid_fits(grid, C::THREADS)) return TG_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((gemm_kernel<C, DEPTH, SWZ, TAIL>), dim3((unsigned)grid), dim3(C::THREADS), 0, stream, gp);
     return hipGetLastError() == hipSuccess ? TG_OK : TG_ERR_LAUNCH;
 }
@@ -34,7 +35,7 @@ tg_status launch_variants(const GemmParams &gp, const tg_plan_info &p, hipStream
 
 template <class C, int STAGES, int SWZ, int SCHED, bool TAIL = false>
 tg_status launch_ring_one(const GemmParams &gp, int64_t grid, hipStream_t stream) {
-    if (grid > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
+    if (!grid_fits(grid, C::THREADS)) return TG_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((gemm_ring_kernel<C, STAGES, SWZ, SCHED, TAIL>), dim3((unsigned)grid), dim3(C::THREADS), 0,
                        stream, gp);
     return hipGetLastError() == hipSuccess ? TG_OK : TG_ERR_LAUNCH;
@@ -74,6 +75,7 @@ tg_status launch_dtype(const GemmParams &gp, const tg_plan_info &p, hipStream_t 
     if (p.persistent && p.config == TG_CFG_288x160) {     // two batch entries per workgroup
         if (p.pipeline_depth != 4 || p.swizzle != SWZ_XOR) return TG_ERR_INTERNAL;
         using C = Ring288x160<DT>;
+        if (!grid_fits(p.grid, C::THREADS)) return TG_ERR_UNSUPPORTED;
         if (tail)
             hipLaunchKernelGGL((gemm_ring_chain_kernel<C, 4, SWZ_XOR, true>), dim3((unsigned)p.grid), dim3(C::THREADS),
                                0, s, gp);
