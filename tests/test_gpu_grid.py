@@ -26,3 +26,15 @@ def test_batch_of_many_problems(past, want):
     torch.cuda.synchronize()
     assert got == want
     assert torch.equal(C, A * B if want == tg.TG_OK else torch.full_like(C, -1.0))
+
+
+def test_pack_of_many_rows():
+    """64 threads a row of B: more rows than one dimension of a grid holds."""
+    K = (1 << 26) + 9
+    B = (torch.arange(K, device="cuda") % 251).to(torch.bfloat16)
+    ld = tg.tile_gemm_packed_b_ld(1, "bf16")
+    packed = torch.full((K, ld), -1.0, dtype=torch.bfloat16, device="cuda")
+    assert tg.tile_gemm_packed_b_size(1, K, 1, "bf16") == K * ld * 2
+    tg.tile_gemm_pack_b(1, K, 1, "bf16", B, 1, K, packed)
+    assert torch.equal(packed[:, 0], B)
+    assert not packed[:, 1:].any()

@@ -11,6 +11,7 @@
 #pragma once
 
 #include "gemm_kernel.hpp"
+#include "grid.hpp"
 
 namespace tg {
 
@@ -28,7 +29,7 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const char *__restrict__
                                                         int64_t cols, int64_t total_rows, int group) {
     constexpr int PER = 16 / ESZ;     // elements per chunk
     const int per_block = 256 / group;
-    const int64_t q = (int64_t)blockIdx.x * per_block + threadIdx.x / group;
+    const int64_t q = (int64_t)wide_block() * per_block + threadIdx.x / group;
     if (q >= total_rows) return;
     const int64_t b = q / rows, r = q - b * rows;
     const char *s = src + (b * stride + r * ld) * ESZ;

@@ -854,11 +854,11 @@ tg_status launch_pack_rows(int esz, const void *src, int64_t ld, int64_t stride,
     const int64_t blocks = cdiv(total_rows, 256 / group);
     if (blocks > 0x7fffffffLL || ld_out * esz > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
     if (esz == 4)
-        hipLaunchKernelGGL(pack_rows_kernel<4>, dim3((unsigned)blocks), dim3(256), 0, s,
+        hipLaunchKernelGGL(pack_rows_kernel<4>, wide_grid(blocks), dim3(256), 0, s,
                            static_cast<const char *>(src), ld, stride, static_cast<char *>(dst), ld_out, rows, cols,
                            total_rows, group);
     else
-        hipLaunchKernelGGL(pack_rows_kernel<2>, dim3((unsigned)blocks), dim3(256), 0, s,
+        hipLaunchKernelGGL(pack_rows_kernel<2>, wide_grid(blocks), dim3(256), 0, s,
                            static_cast<const char *>(src), ld, stride, static_cast<char *>(dst), ld_out, rows, cols,
                            total_rows, group);
     return hipGetLastError() == hipSuccess ? TG_OK : TG_ERR_LAUNCH;
@@ -901,7 +901,7 @@ tg_status pack_b(int64_t batch, int64_t K, int64_t N, tg_dtype dtype, const void
     if (!transposed) return launch_pack_rows(esz, B, ldb, sB, packed, ldp, K, N, batch * K, s);
     {
         const int64_t gk = cdiv(K, 64), gn = cdiv(ldp, 64);
-        if (gk > 0x7fffffffLL || gn > 65535 || batch > 65535) return TG_ERR_UNSUPPORTED;
+        if (!grid_fits(gk, 256) || gn > 65535 || batch > 65535) return TG_ERR_UNSUPPORTED;
         const dim3 grid((unsigned)gk, (unsigned)gn, (unsigned)batch);
         if (esz == 4)
             hipLaunchKernelGGL(pack_transposed_kernel<uint32_t>, grid, dim3(256), 0, s,
