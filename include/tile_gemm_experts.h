@@ -48,8 +48,10 @@
  *    `stream`: no allocation, no memset, no synchronisation, so they can be
  *    captured into a HIP graph.  Results are bitwise reproducible: no atomics.
  *  - TG_ERR_UNSUPPORTED: no visible gfx950 device; tokens * top_k of 2^31 or
- *    more; more than TILE_GEMM_MAX_EXPERTS experts; a leading dimension at
- *    which a block's tile would span 2^31 bytes; a group size that is not built.
+ *    more (the sort: 2^31 - 2^24); more than TILE_GEMM_MAX_EXPERTS experts; in the products, rows or an
+ *    extent above 2^30, a leading dimension at which a block's tile would span
+ *    2^31 bytes, a result of 2^24 tiles or more, K of 2^30 bytes (4-bit products);
+ *    a group size that is not built.
  *
  * These entry points were added beside version 11 of tile_gemm.h, whose structs
  * and calls they leave as they are; they have a version of their own.

@@ -95,3 +95,12 @@ def test_plan_refusals(fn):
         assert ask(fn, transposed=2) == INVALID
     if fn == "tile_gemm_q4_plan":
         assert ask(fn, group=0) == INVALID and ask(fn, group=48) == UNSUPPORTED
+
+
+def test_grids_past_one_dimension_are_refused():
+    """A workgroup has 256 threads, a grid fewer than 2^32: tiles of 64 x 64 over 2^30 rows, or over 2048 wide
+    gradients of 8 rows."""
+    assert ask("tile_gemm_grouped_plan", experts=1, rows=1 << 30, N=8, K=8, dtype=0, c_dtype=0) == UNSUPPORTED
+    assert ask("tile_gemm_grouped_plan", experts=1, rows=1 << 29, N=8, K=8, dtype=0, c_dtype=0) == OK
+    assert ask("tile_gemm_grouped_wgrad_plan", experts=2048, M=8, N=1 << 20) == UNSUPPORTED
+    assert ask("tile_gemm_grouped_wgrad_plan", experts=2048, M=8, N=1 << 19) == OK

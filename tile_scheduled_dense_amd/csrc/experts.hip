@@ -455,6 +455,7 @@ tg_status q4(int64_t experts, int64_t rows, int64_t N, int64_t K, int64_t group,
 }
 
 tg_status answer(const ProductPlan &plan, bool past, tg_experts_plan_info *out) {
+    if (!plan.fits()) return TG_ERR_UNSUPPORTED;
     *out = plan.info;
     out->past_caches = plan.info.kernel == TG_EXPERTS_TILES && past;
     return TG_OK;

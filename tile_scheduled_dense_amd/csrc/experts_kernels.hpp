@@ -48,14 +48,14 @@ using Tile64F32 = RingCfg<DT_F32, 64, 64, 2, 2, 16>;
 // P: the pieces' configuration (C itself: none).
 template <class C, class P, bool B_KS, bool PIPE, int STAGES>
 tg_status launch_tiles(const GroupedParams &p, const ProductPlan &plan, hipStream_t s) {
-    if (plan.gx > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
+    if (!plan.fits()) return TG_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((grouped_tile_kernel<C, P, B_KS, PIPE, STAGES>), dim3((unsigned)plan.gx), dim3(C::THREADS), 0, s, p);
     return launched();
 }
 
 template <class C, bool PIPE, int STAGES>
 tg_status launch_wgrad_tiles(const GroupedParams &p, const ProductPlan &plan, hipStream_t s) {
-    if (plan.gx > 0x7fffffffLL) return TG_ERR_UNSUPPORTED;
+    if (!plan.fits()) return TG_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((wgrad_tile_kernel<C, PIPE, STAGES>), dim3((unsigned)plan.gx), dim3(C::THREADS), 0, s, p);
     return launched();
 }

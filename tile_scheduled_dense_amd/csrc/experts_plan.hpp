@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "experts.hpp"
+#include "grid.hpp"
 #include "ranges.hpp"
 #include "tile_gemm_experts.h"
 
@@ -16,6 +17,7 @@ struct ProductPlan {
     int lds_copies;              // of a K tile (tiles)
     int64_t gx;                  // workgroups: gx * gy * gz
     unsigned gy, gz;
+    bool fits() const { return grid_fits(gx, 64 * info.waves); }
 };
 
 inline ProductPlan plan_of(int kernel, int tile_m, int tile_n, int waves, int64_t gx, int64_t gy = 1, int64_t gz = 1) {
