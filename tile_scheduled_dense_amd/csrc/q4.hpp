@@ -228,6 +228,14 @@ struct Q4Rows {
             if (16 * i + RPI * d < rows) lds[(16 * i + r) * ROW + (lane % ROW ^ r)] = a[d];
         }
     }
+    // Activations pass from lane to lane between stage and read.  A wave's LDS operations
+    // take effect in program order, which this keeps: nothing else tells the compiler that a
+    // lane reads what another has stored (the fences are of a wave alone: no instruction).
+    __device__ __forceinline__ static void order() {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
     // unit h of this lane's eight k of step s, row lane % 16 of tile i
     __device__ __forceinline__ u32x4 read(int i, int s, int h) const {
         const int r = lane % 16, unit = 4 * PIECES * s + PIECES * (lane / 16) + h;
@@ -264,11 +272,13 @@ struct Q4Block {
     }
     template <bool TAIL>
     __device__ __forceinline__ void multiply(const Rows &rows, int kb, f32x4 (&acc)[NT][MT]) {
+        Rows::order();          // the block before has been read
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             if constexpr (!A_AHEAD) rows.template load<TAIL>(kb, i, a[0]);
             rows.stage(i, a[A_AHEAD ? i : 0]);
         }
+        Rows::order();
         f32x4 sum[NT][MT];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
