@@ -104,3 +104,11 @@ def test_grids_past_one_dimension_are_refused():
     assert ask("tile_gemm_grouped_plan", experts=1, rows=1 << 29, N=8, K=8, dtype=0, c_dtype=0) == OK
     assert ask("tile_gemm_grouped_wgrad_plan", experts=2048, M=8, N=1 << 20) == UNSUPPORTED
     assert ask("tile_gemm_grouped_wgrad_plan", experts=2048, M=8, N=1 << 19) == OK
+
+
+@pytest.mark.parametrize("experts,rows,N,K,dt", [(64, 512, 768, 1024, "f16"), (64, 512, 512, 512, "f32"), (256, 2048, 256, 256, "bf16"),
+                                                 (2048, 8192, 128, 128, "bf16"), (8, 32, 4096, 1024, "bf16")])
+def test_streamed_rows_of_one_expert_are_not_one_workgroups(experts, rows, N, K, dt):
+    """Which expert has the rows is known on the device alone: wherever they are, a workgroup takes one row tile."""
+    for transposed in (0, 1):
+        has(tg.tile_gemm_grouped_plan(experts, rows, N, K, dt, transposed=transposed), kernel="stream", row_tiles=1)

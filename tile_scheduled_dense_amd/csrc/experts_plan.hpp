@@ -29,6 +29,10 @@ inline ProductPlan plan_of(int kernel, int tile_m, int tile_n, int waves, int64_
     p.info.workgroups = gx * gy * gz;
     p.info.row_tiles = 1;
     p.gx = gx;
+    if (gy > kGridY) {                    // in whole layers (slot_of)
+        gz = cdiv(gy, kGridY);
+        gy = kGridY;
+    }
     p.gy = (unsigned)gy;
     p.gz = (unsigned)gz;
     return p;
@@ -40,14 +44,7 @@ ProductPlan plan_stream(int64_t experts, int64_t rows, int64_t N, int64_t K) {
     using S = StreamShape<DT, TRANS>;
     const int64_t stages = cdiv(K, S::K);
     const int waves = stages >= 16 ? 8 : (stages >= 8 ? 4 : 2);
-    // Row tiles at the same time: all there can be, if one expert had every row, while
-    // that is two workgroups a CU at most; else twice an expert's on average.
-    const int64_t strips = cdiv(N, S::COLS), mean = cdiv(2 * cdiv(rows, experts), 16);
-    int64_t tiles = cdiv(rows, 16) < 8 ? cdiv(rows, 16) : 8;
-    while (tiles > 1 && tiles > mean && strips * (experts + 1) * tiles > 512) --tiles;
-    ProductPlan p = plan_of(TG_EXPERTS_STREAM, 16, S::COLS, waves, strips, experts + 1, tiles);
-    p.info.row_tiles = cdiv(cdiv(rows, 16), tiles);
-    return p;
+    return plan_of(TG_EXPERTS_STREAM, 16, S::COLS, waves, cdiv(N, S::COLS), tiles_and_slots(rows, experts, 16));
 }
 
 // the most tile rows that `groups` groups of `rows` rows together can have

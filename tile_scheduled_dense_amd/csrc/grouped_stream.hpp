@@ -150,95 +150,94 @@ __device__ __forceinline__ void stream_mma(const StreamB<DT, TRANS> &b, const St
     }
 }
 
-// grid: column strips x (experts + 1; the last takes the rows without an expert) x the
-// row tiles taken at the same time, which read the weights again from cache.
+// grid: column strips x row tiles (row_slot), at the same time; an expert's further row
+// tiles read its weights again, from cache.
 template <int DT, bool TRANS>
 __global__ __launch_bounds__(512) void grouped_stream_kernel(GroupedParams p) {
     using S = StreamShape<DT, TRANS>;
     extern __shared__ f32x4 stream_lds[];           // [waves][FRAGS][64]
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-    const int e = blockIdx.y, n0 = blockIdx.x * S::COLS;
-    const RowSpan span = rows_of(p.offsets, e, p.experts, p.rows);
+    const int n0 = blockIdx.x * S::COLS;
     const int n_left = p.N - n0;
     const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
+    const int64_t b_step = (TRANS ? (int64_t)S::K : S::K * p.ldb) * S::E;
+    int e;
+    RowSpan span;
+    if (!row_slot<16>(p.offsets, p.experts, p.rows, slot_of(p.experts), e, span)) return;
+    const int r0 = span.lo, rows = span.hi - r0;
     const int stages = e == p.experts ? 0 : (p.K + S::K - 1) / S::K;
     const char *B = p.B + (e == p.experts ? 0 : (int64_t)e * p.sB) * S::E + (TRANS ? n0 * p.ldb : (int64_t)n0) * S::E;
-    const int64_t b_step = (TRANS ? (int64_t)S::K : S::K * p.ldb) * S::E;
-    for (int r0 = span.lo + 16 * (int)blockIdx.z; r0 < span.hi; r0 += 16 * (int)gridDim.z) {
-        const int rows = span.hi - r0 < 16 ? span.hi - r0 : 16;
-        const char *A = p.A + (int64_t)r0 * p.lda * S::E;
-        f32x4 acc[S::FRAGS];
+    const char *A = p.A + (int64_t)r0 * p.lda * S::E;
+    f32x4 acc[S::FRAGS];
 #pragma unroll
-        for (int j = 0; j < S::FRAGS; ++j) acc[j] = f32x4{0, 0, 0, 0};
-        using Loads = StreamB<DT, TRANS>;
-        auto fetch = [&](int s, Loads &b, StreamA<DT, TRANS> &a, auto part) {
-            constexpr int PART = decltype(part)::value;
-            const int k_left = p.K - s * S::K;
-            b.template load<PART>(B + s * b_step, p.ldb, n_left, k_left, lane);
-            a.template load<PART>(A + (int64_t)s * S::K * S::E, p.lda, rows, k_left, lane);
-        };
-        // whole stages, the next one's loads in flight during the current one's
-        // products; then those that N or K cuts, one at a time
-        const int whole = n_left < S::COLS || stages == 0 ? 0 : p.K / S::K;
-        int s = wave;
-        if (s < whole) {
-            const std::integral_constant<int, Loads::ALL> full;
-            StreamB<DT, TRANS> b0, b1;
-            StreamA<DT, TRANS> a0, a1;
-            fetch(s, b0, a0, full);
-            for (;;) {
-                s += waves;
-                const bool more = s < whole;
-                if (more) fetch(s, b1, a1, full);
-                __builtin_amdgcn_sched_barrier(0);
-                stream_mma<DT, TRANS>(b0, a0, acc);
-                if (!more) break;
-                b0 = b1;
-                a0 = a1;
-            }
+    for (int j = 0; j < S::FRAGS; ++j) acc[j] = f32x4{0, 0, 0, 0};
+    using Loads = StreamB<DT, TRANS>;
+    auto fetch = [&](int s, Loads &b, StreamA<DT, TRANS> &a, auto part) {
+        constexpr int PART = decltype(part)::value;
+        const int k_left = p.K - s * S::K;
+        b.template load<PART>(B + s * b_step, p.ldb, n_left, k_left, lane);
+        a.template load<PART>(A + (int64_t)s * S::K * S::E, p.lda, rows, k_left, lane);
+    };
+    // whole stages, the next one's loads in flight during the current one's
+    // products; then those that N or K cuts, one at a time
+    const int whole = n_left < S::COLS || stages == 0 ? 0 : p.K / S::K;
+    int s = wave;
+    if (s < whole) {
+        const std::integral_constant<int, Loads::ALL> full;
+        StreamB<DT, TRANS> b0, b1;
+        StreamA<DT, TRANS> a0, a1;
+        fetch(s, b0, a0, full);
+        for (;;) {
+            s += waves;
+            const bool more = s < whole;
+            if (more) fetch(s, b1, a1, full);
+            __builtin_amdgcn_sched_barrier(0);
+            stream_mma<DT, TRANS>(b0, a0, acc);
+            if (!more) break;
+            b0 = b1;
+            a0 = a1;
         }
-        const bool chunks = p.K % S::PER == 0 && (TRANS || p.N % S::PER == 0);
-        for (; s < stages; s += waves) {
-            StreamB<DT, TRANS> b;
-            StreamA<DT, TRANS> a;
-            // (25 rows, N 728, K 1912 transposed: 12.6 us element by element, 5.8 in chunks)
-            if (chunks) fetch(s, b, a, std::integral_constant<int, Loads::CHUNKS>{});
-            else fetch(s, b, a, std::integral_constant<int, Loads::ELEMENTS>{});
-            stream_mma<DT, TRANS>(b, a, acc);
-        }
+    }
+    const bool chunks = p.K % S::PER == 0 && (TRANS || p.N % S::PER == 0);
+    for (; s < stages; s += waves) {
+        StreamB<DT, TRANS> b;
+        StreamA<DT, TRANS> a;
+        // (25 rows, N 728, K 1912 transposed: 12.6 us element by element, 5.8 in chunks)
+        if (chunks) fetch(s, b, a, std::integral_constant<int, Loads::CHUNKS>{});
+        else fetch(s, b, a, std::integral_constant<int, Loads::ELEMENTS>{});
+        stream_mma<DT, TRANS>(b, a, acc);
+    }
 #pragma unroll
-        for (int j = 0; j < S::FRAGS; ++j) stream_lds[(wave * S::FRAGS + j) * 64 + lane] = acc[j];
-        __syncthreads();
-        // wave w sums and stores value w, w + waves, ... of the tile's four: the FRAGS
-        // columns of a value are neighbours (B as stored), the four values of a
-        // fragment are (B transposed)
-        const int r = r0 + lane % 16, g = lane / 16;
-        if constexpr (TRANS) {
-            for (int j = wave; j < S::FRAGS; j += waves) {
-                f32x4 v = stream_lds[j * 64 + lane];
-                for (int w = 1; w < waves; ++w) v += stream_lds[(w * S::FRAGS + j) * 64 + lane];
-                const int n = 16 * j + 4 * g;
-                if (r < span.hi && n < n_left)
-                    store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, v);
-            }
-        } else {
-            for (int q = wave; q < S::FRAGS; q += waves) {      // (value, four fragments)
-                const int v = q / (S::FRAGS / 4), j0 = 4 * (q % (S::FRAGS / 4));
-                f32x4 x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float *at = reinterpret_cast<const float *>(stream_lds + (j0 + j) * 64 + lane) + v;
-                    float y = at[0];
-                    for (int w = 1; w < waves; ++w) y += at[w * S::FRAGS * 256];
-                    x[j] = y;
-                }
-                const int n = S::PER * (4 * g + v) + j0;
-                if (r < span.hi && n < n_left)
-                    store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, x);
-            }
+    for (int j = 0; j < S::FRAGS; ++j) stream_lds[(wave * S::FRAGS + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    // wave w sums and stores value w, w + waves, ... of the tile's four: the FRAGS
+    // columns of a value are neighbours (B as stored), the four values of a
+    // fragment are (B transposed)
+    const int r = r0 + lane % 16, g = lane / 16;
+    if constexpr (TRANS) {
+        for (int j = wave; j < S::FRAGS; j += waves) {
+            f32x4 v = stream_lds[j * 64 + lane];
+            for (int w = 1; w < waves; ++w) v += stream_lds[(w * S::FRAGS + j) * 64 + lane];
+            const int n = 16 * j + 4 * g;
+            if (r < span.hi && n < n_left)
+                store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, v);
         }
-        __syncthreads();
+    } else {
+        for (int q = wave; q < S::FRAGS; q += waves) {      // (value, four fragments)
+            const int v = q / (S::FRAGS / 4), j0 = 4 * (q % (S::FRAGS / 4));
+            f32x4 x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float *at = reinterpret_cast<const float *>(stream_lds + (j0 + j) * 64 + lane) + v;
+                float y = at[0];
+                for (int w = 1; w < waves; ++w) y += at[w * S::FRAGS * 256];
+                x[j] = y;
+            }
+            const int n = S::PER * (4 * g + v) + j0;
+            if (r < span.hi && n < n_left)
+                store4<DT>(p.C, (int64_t)r * p.ldc + n0 + n, n_left - n, p.c_f32, wide, x);
+        }
     }
 }
 
