@@ -112,3 +112,9 @@ def test_streamed_rows_of_one_expert_are_not_one_workgroups(experts, rows, N, K,
     """Which expert has the rows is known on the device alone: wherever they are, a workgroup takes one row tile."""
     for transposed in (0, 1):
         has(tg.tile_gemm_grouped_plan(experts, rows, N, K, dt, transposed=transposed), kernel="stream", row_tiles=1)
+
+
+@pytest.mark.parametrize("experts,rows,N,K,dt", [(64, 256, 2048, 2048, "bf16"), (64, 1024, 2048, 2048, "f16"), (1, 2048, 4096, 4096, "bf16"),
+                                                 (16, 128, 1024, 1024, "f32"), (4, 9000, 300, 512, "bf16")])
+def test_rows_of_one_4_bit_expert_are_not_one_workgroups(experts, rows, N, K, dt):
+    has(tg.tile_gemm_q4_plan(experts, rows, N, K, 128, dt), kernel="q4", row_tiles=1)

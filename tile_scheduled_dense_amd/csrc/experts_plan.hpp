@@ -154,10 +154,7 @@ ProductPlan plan_q4(int64_t experts, int64_t rows, int64_t N, int64_t K) {
     const int64_t strips = cdiv(n_tiles, nt);
     int waves = 1;
     while (waves < most && waves * 4 <= k_blocks && (waves < 2 || strips * experts * waves < 4096)) waves *= 2;
-    const int64_t gz = cdiv(chunks, mt);
-    ProductPlan p = plan_of(TG_EXPERTS_Q4, 16 * mt, 16 * nt, waves, strips, experts + 1, gz);
-    p.info.row_tiles = cdiv(cdiv(rows, 16 * mt), gz);
-    return p;
+    return plan_of(TG_EXPERTS_Q4, 16 * mt, 16 * nt, waves, strips, tiles_and_slots(rows, experts, 16 * mt));
 }
 
 }  // namespace tg

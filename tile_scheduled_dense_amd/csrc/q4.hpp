@@ -161,9 +161,9 @@ struct Q4Params {
 // A workgroup takes NT neighbouring n tiles of one expert; its waves split K
 // (blocks w, w + W, ...) and add their sums in LDS, in wave order.  Weights are the
 // matrix instruction's first operand, so lane l holds C[row l % 16][n 4 (l / 16)
-// .. + 3]: four neighbours in a row of C, one store.  MT row tiles of 16 at a
-// time; further ones go to gridDim.z workgroups in turn, each reading the codes
-// again (from cache).
+// .. + 3]: four neighbours in a row of C, one store.  It takes MT row tiles of 16;
+// an expert's further rows have workgroups of their own (row_slot), which read the codes
+// again, from cache.
 //
 // The codes, scales and activations of the next block are in flight while a block
 // is multiplied.  Activations are loaded as they lie, 256 bytes of a row by 16
@@ -339,8 +339,10 @@ __global__ __launch_bounds__(512) void q4_kernel(Q4Params p) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // the same in every lane of a wave
     const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
     const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
-    const int g = blockIdx.y, tile = blockIdx.x * NT;
-    const RowSpan span = rows_of(p.offsets, g, p.experts, p.rows);
+    const int tile = blockIdx.x * NT;
+    int g;
+    RowSpan span;
+    if (!row_slot<16 * MT>(p.offsets, p.experts, p.rows, slot_of(p.experts), g, span)) return;
     const bool dead = g == p.experts || p.K == 0;    // zeros
     const int n0 = tile * kQ4N + 4 * (lane / 16);
     const u32x4 *codes[NT];
@@ -352,53 +354,51 @@ __global__ __launch_bounds__(512) void q4_kernel(Q4Params p) {
         codes[t] = reinterpret_cast<const u32x4 *>(p.codes) + at * p.k_blocks * 64 + lane;
         scales[t] = reinterpret_cast<const T *>(p.scales) + at * p.groups * kQ4N + 4 * (kQ4K / GROUP) * (lane / 16);
     }
-    for (int r0 = span.lo + 16 * MT * (int)blockIdx.z; r0 < span.hi; r0 += 16 * MT * (int)gridDim.z) {
-        f32x4 acc[NT][MT];
+    const int r0 = span.lo;
+    f32x4 acc[NT][MT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) acc[t][i] = f32x4{0, 0, 0, 0};
-        if (!dead) {
-            Rows rows;
-            const int count = __builtin_amdgcn_readfirstlane(span.hi - r0 < 16 * MT ? span.hi - r0 : 16 * MT);
-            rows.init(p.A + (int64_t)r0 * p.lda * Rows::E, p.lda, count, p.K, lane, q4_lds + wave * Rows::LDS);
-            const int full = p.K / kQ4K;
-            int kb = wave;
-            if (kb < full) {
-                Block b, n;
-                b.template load<false>(codes, scales, rows, kb);
-                for (;;) {
-                    if (kb + waves < full) n.template load<false>(codes, scales, rows, kb + waves);
-                    b.template multiply<false>(rows, kb, acc);
-                    kb += waves;
-                    if (kb >= full) break;
-                    if (kb + waves < full) b.template load<false>(codes, scales, rows, kb + waves);
-                    n.template multiply<false>(rows, kb, acc);
-                    kb += waves;
-                    if (kb >= full) break;
-                }
-            }
-            if (kb < p.k_blocks) {
-                Block b;
-                b.template load<true>(codes, scales, rows, kb);
-                b.template multiply<true>(rows, kb, acc);
+        for (int i = 0; i < MT; ++i) acc[t][i] = f32x4{0, 0, 0, 0};
+    if (!dead) {
+        Rows rows;
+        const int count = __builtin_amdgcn_readfirstlane(span.hi - r0);
+        rows.init(p.A + (int64_t)r0 * p.lda * Rows::E, p.lda, count, p.K, lane, q4_lds + wave * Rows::LDS);
+        const int full = p.K / kQ4K;
+        int kb = wave;
+        if (kb < full) {
+            Block b, n;
+            b.template load<false>(codes, scales, rows, kb);
+            for (;;) {
+                if (kb + waves < full) n.template load<false>(codes, scales, rows, kb + waves);
+                b.template multiply<false>(rows, kb, acc);
+                kb += waves;
+                if (kb >= full) break;
+                if (kb + waves < full) b.template load<false>(codes, scales, rows, kb + waves);
+                n.template multiply<false>(rows, kb, acc);
+                kb += waves;
+                if (kb >= full) break;
             }
         }
-        __syncthreads();
-        f32x4 *sums = reinterpret_cast<f32x4 *>(q4_lds);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) sums[((wave * NT + t) * MT + i) * 64 + lane] = acc[t][i];
-        __syncthreads();
-        for (int q = wave; q < NT * MT; q += waves) {
-            f32x4 v = sums[q * 64 + lane];
-            for (int w = 1; w < waves; ++w) v += sums[(w * NT * MT + q) * 64 + lane];
-            const int r = r0 + 16 * (q % MT) + lane % 16, n = n0 + 16 * (q / MT);
-            v *= Q4Unit<DT>::value;
-            if (r < span.hi && n < p.N) store4<DT>(p.C, (int64_t)r * p.ldc + n, p.N - n, p.c_f32, wide, v);
+        if (kb < p.k_blocks) {
+            Block b;
+            b.template load<true>(codes, scales, rows, kb);
+            b.template multiply<true>(rows, kb, acc);
         }
-        __syncthreads();
+    }
+    __syncthreads();
+    f32x4 *sums = reinterpret_cast<f32x4 *>(q4_lds);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sums[((wave * NT + t) * MT + i) * 64 + lane] = acc[t][i];
+    __syncthreads();
+    for (int q = wave; q < NT * MT; q += waves) {
+        f32x4 v = sums[q * 64 + lane];
+        for (int w = 1; w < waves; ++w) v += sums[(w * NT * MT + q) * 64 + lane];
+        const int r = r0 + 16 * (q % MT) + lane % 16, n = n0 + 16 * (q / MT);
+        v *= Q4Unit<DT>::value;
+        if (r < span.hi && n < p.N) store4<DT>(p.C, (int64_t)r * p.ldc + n, p.N - n, p.c_f32, wide, v);
     }
 }
 
