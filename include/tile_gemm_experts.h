@@ -158,7 +158,7 @@ typedef enum {
     TG_EXPERTS_NOTHING = 0,
     TG_EXPERTS_STREAM = 1,     /* weights streamed to registers, the waves of a workgroup split K */
     TG_EXPERTS_TILES = 2,      /* block tiles through LDS */
-    TG_EXPERTS_NARROW = 3,     /* the weights' gradient of an extent below one chunk */
+    TG_EXPERTS_NARROW = 3,     /* the weights' gradient of an extent below 8 */
     TG_EXPERTS_Q4 = 4          /* 4-bit weights */
 } tg_experts_kernel;
 

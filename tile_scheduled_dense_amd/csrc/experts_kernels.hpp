@@ -80,7 +80,8 @@ template <int DT>
 tg_status launch_wgrad(const GroupedParams &p, hipStream_t s) {
     const ProductPlan plan = plan_wgrad<DT>(p.experts, p.rows, p.M, p.N);
     if (plan.info.kernel == TG_EXPERTS_NARROW) {
-        hipLaunchKernelGGL((wgrad_small_kernel<DT>), dim3((unsigned)plan.gx), dim3(256), 0, s, p);
+        const int width = p.M < p.N ? plan.info.tile_n : plan.info.tile_m;
+        hipLaunchKernelGGL((wgrad_narrow_kernel<DT>), dim3((unsigned)plan.gx, plan.gy), dim3(1024), 0, s, p, width);
         return launched();
     }
     if (plan.info.tile_m == 256) return launch_wgrad_tiles<Tile256<DT>, true, 4>(p, plan, s);

@@ -80,7 +80,8 @@ constexpr int64_t kLong = 1024;
 //    45.6, 96 rows 14.6 against 45.9; 4 of 2048 x 2048, 24 rows 11.1 against 24.3; but 32
 //    of 2048 x 1024, 4 rows, 31.5 against 24.6, where the tiles' copies read at 5.5 TB/s,
 //    and two workgroups a CU, 8 experts of 1024 x 4096, 32 rows, 28.7 against 18.1).  So
-//    is an N below a chunk, which is not for the tiles (grouped_ring.hpp).
+//    is an N below kNarrow, of which a tile would be mostly empty (and the tiles need a
+//    16-byte chunk of it: grouped_ring.hpp).
 //  * 16 bits: 256 x 256 over a long K from 128 such tiles on (f16, 8 uneven experts, K
 //    1024: 4096 x 2048 32.0 against 33.4 us on 128 x 128, 2048 x 2048 26.5 against 22.6),
 //    else 128 x 128, three LDS copies for three workgroups a CU (257 x 1000 over 150 rows
@@ -96,7 +97,7 @@ ProductPlan plan_grouped_as(int64_t experts, int64_t rows, int64_t N, int64_t K)
     const int64_t weights = experts * N * K * (DT == DT_F32 ? 4 : 2);
     const int64_t strips = cdiv(N, StreamShape<DT, TRANS>::COLS) * experts * cdiv(mean, 16);
     const bool stream = weights <= (int64_t(96) << 20) && (mean <= 8 || (mean <= 128 && strips < 256));
-    if (stream || N < 8) return plan_stream<DT, TRANS>(experts, rows, N, K);
+    if (stream || N < kNarrow) return plan_stream<DT, TRANS>(experts, rows, N, K);
     const int64_t tiles = cdiv(rows, 256) * cdiv(N, 256);
     if (K >= kLong && tiles >= (DT == DT_F32 ? 800 : 128)) return plan_tiles(experts, rows, N, 256, true, true, 4);
     return DT == DT_F32 ? plan_tiles(experts, rows, N, 64, false, true, 4)
@@ -115,9 +116,10 @@ ProductPlan plan_grouped(bool transposed, int64_t experts, int64_t rows, int64_t
 // 13.1 us; 33 of 257 x 1000 over 150 16.9 -> 20.9).
 template <int DT>
 ProductPlan plan_wgrad(int64_t experts, int64_t rows, int64_t M, int64_t N) {
-    if (M < 8 || N < 8) {
-        const int64_t blocks = cdiv(experts * M * N, 256);
-        return plan_of(TG_EXPERTS_NARROW, 1, 1, 4, blocks < 65536 ? blocks : 65536);
+    if (M < kNarrow || N < kNarrow) {
+        const int width = narrow_width(M < N ? N : M, DT == DT_F32);
+        return plan_of(TG_EXPERTS_NARROW, M < N ? (int)M : width, M < N ? width : (int)N, 16, cdiv(M < N ? N : M, width),
+                       experts);
     }
     const int64_t each = cdiv(M, 256) * cdiv(N, 256), small = cdiv(M, 128) * cdiv(N, 128);
     int tile = DT == DT_F32 ? 64 : 128;

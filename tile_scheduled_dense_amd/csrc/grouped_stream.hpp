@@ -241,22 +241,52 @@ __global__ __launch_bounds__(512) void grouped_stream_kernel(GroupedParams p) {
     }
 }
 
-// C[g] = A[rows of g]^T . D[rows of g], one output a thread: for extents below
-// one 16-byte chunk, where there is no tile to fill.
+// C[g] = A[rows of g]^T . D[rows of g] where an extent is below kNarrow, of which a tile
+// would be mostly empty: a thread a column of the longer extent and `width` of them a row,
+// all of the shorter extent in its registers, an expert's rows dealt to the 1024 / width
+// threads of a column, whose sums are added in LDS in their order.  Bound by the latency of
+// the loads: 16384 rows, M 4096, N 4 bf16 341 us, M 7, N 7 38 us (with a thread an output
+// and one running sum of an expert's rows 6240 and 1175).
+constexpr int kNarrow = 8;
+inline int narrow_width(int64_t longer, bool f32) {
+    int w = 8;
+    while (w < longer && w < (f32 ? 32 : 64)) w *= 2;      // a cache line of a row at most
+    return w;
+}
 template <int DT>
-__global__ __launch_bounds__(256) void wgrad_small_kernel(GroupedParams p) {
+__global__ __launch_bounds__(1024) void wgrad_narrow_kernel(GroupedParams p, int width) {
     typedef typename ElemOf<DT>::type T;
-    const int64_t per = (int64_t)p.M * p.N, total = per * p.experts;
-    const T *A = reinterpret_cast<const T *>(p.A), *D = reinterpret_cast<const T *>(p.B);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int g = (int)(i / per), m = (int)(i % per / p.N), n = (int)(i % p.N);
-        const RowSpan span = rows_of(p.offsets, g, p.experts, p.rows);
-        float sum = 0.0f;
-        for (int r = span.lo; r < span.hi; ++r)
-            sum = __builtin_fmaf((float)A[(int64_t)r * p.lda + m], (float)D[(int64_t)r * p.ldb + n], sum);
-        const int64_t at = (int64_t)g * p.sC + (int64_t)m * p.ldc + n;
-        if (DT == DT_F32 || p.c_f32) reinterpret_cast<float *>(p.C)[at] = sum;
-        else reinterpret_cast<T *>(p.C)[at] = (T)sum;
+    __shared__ float part[(kNarrow - 1) * 1024];
+    const bool m_short = p.M < p.N;
+    const int few = m_short ? p.M : p.N, many = m_short ? p.N : p.M;
+    const T *S = reinterpret_cast<const T *>(m_short ? p.A : p.B), *L = reinterpret_cast<const T *>(m_short ? p.B : p.A);
+    const int64_t ld_s = m_short ? p.lda : p.ldb, ld_l = m_short ? p.ldb : p.lda;
+    const int tid = threadIdx.x, slots = 1024 / width, x = blockIdx.x * width + tid % width, g = blockIdx.y;
+    const RowSpan span = rows_of(p.offsets, g, p.experts, p.rows);
+    float sum[kNarrow - 1] = {};
+    int from[kNarrow - 1];          // past the extent its last again: loads without a branch, in flight together
+#pragma unroll
+    for (int j = 0; j < kNarrow - 1; ++j) from[j] = j < few ? j : few - 1;
+    if (x < many) {
+#pragma unroll 4
+        for (int r = span.lo + tid / width; r < span.hi; r += slots) {
+            const float v = (float)L[r * ld_l + x];
+#pragma unroll
+            for (int j = 0; j < kNarrow - 1; ++j) sum[j] = __builtin_fmaf(v, (float)S[r * ld_s + from[j]], sum[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kNarrow - 1; ++j)
+        if (j < few) part[j * 1024 + tid] = sum[j];
+    __syncthreads();
+    for (int i = tid; i < few * width; i += 1024) {
+        const int j = i / width, c = i % width, at = blockIdx.x * width + c;
+        if (at >= many) continue;
+        float v = part[j * 1024 + c];
+        for (int k = 1; k < slots; ++k) v += part[j * 1024 + k * width + c];
+        const int64_t to = (int64_t)g * p.sC + (m_short ? j * p.ldc + at : at * p.ldc + j);
+        if (DT == DT_F32 || p.c_f32) reinterpret_cast<float *>(p.C)[to] = v;
+        else reinterpret_cast<T *>(p.C)[to] = (T)v;
     }
 }
 
