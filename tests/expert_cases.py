@@ -51,8 +51,8 @@ STREAM8 = [
 Q4_TILES = [
     ((16, 32), 8, 50, 3, 5, 1035, 300, 1),      # 65 tiles of 16 columns: the last workgroup's second is past them
     ((16, 32), 1, 16, 0, 1, 8193, 640, 0),
-    ((32, 16), 8, 200, 0, 3, 520, 300, 0),
-    ((32, 16), 1, 31, 0, 1, 4100, 390, 2),
-    ((64, 16), 4, 160, 5, 3, 1100, 300, 0),
-    ((64, 16), 1, 200, 0, 1, 1037, 1290, 3),
+    ((16, 32), 4, 160, 5, 3, 1100, 300, 0),     # by the number of rows
+    ((16, 32), 1, 200, 0, 1, 1037, 1290, 3),
+    ((16, 16), 8, 200, 0, 3, 520, 300, 0),
+    ((16, 16), 1, 31, 0, 1, 4100, 390, 2),
 ]

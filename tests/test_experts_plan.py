@@ -48,6 +48,13 @@ def test_tiles_of_4_bit_products(tile, experts, rows, spare, active, N, K, pad, 
     has(plan, kernel="q4", tile_m=tile[0], tile_n=tile[1])
 
 
+@pytest.mark.parametrize("rows,N,K", [(48, 4096, 4096), (64, 4096, 4096), (200, 1037, 1290), (64, 8192, 8192), (2048, 4096, 4096)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_many_rows_of_4_bit_weights_go_16_at_a_time(rows, N, K, dt):
+    """32 or 64 rows a workgroup were slower than 16 and two column tiles at every size measured."""
+    has(tg.tile_gemm_q4_plan(1, rows, N, K, 128, dt), tile_m=16, tile_n=32)
+
+
 def test_small_tiles():
     """The tiles below the largest, by type and form."""
     has(tg.tile_gemm_grouped_plan(33, 5001, 1000, 257, "f16"), kernel="tiles", tile_m=128, pieces=0, pipeline=0)

@@ -48,7 +48,7 @@ def test_streamed_products(dt, experts, rows, spare, N, K, transposed):
 
 @pytest.mark.parametrize("tile,dt,experts,rows,spare,N,K,group", [
     ((16, 16), "bf16", 64, 300, 0, 40, 300, 64), ((16, 16), "f32", 65, 200, 21, 33, 130, 32), ((16, 32), "f16", 130, 400, 0, 70, 140, 128),
-    ((32, 16), "bf16", 64, 1400, 19, 70, 260, 32), ((64, 16), "f16", 63, 2500, 0, 70, 130, 64), ((16, 32), "bf16", 2048, 3000, 5, 20, 33, 32),
+    ((16, 16), "bf16", 64, 1400, 19, 70, 260, 32), ((16, 32), "f16", 63, 2500, 0, 70, 130, 64), ((16, 32), "bf16", 2048, 3000, 5, 20, 33, 32),
 ])
 def test_4_bit_products(tile, dt, experts, rows, spare, N, K, group):
     total = rows + spare

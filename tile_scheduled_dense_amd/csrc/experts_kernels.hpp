@@ -21,12 +21,11 @@ tg_status launch_stream(const GroupedParams &p, const ProductPlan &plan, hipStre
     return launched();
 }
 
-template <int DT, int GROUP, int MT, int NT>
+template <int DT, int GROUP, int NT>
 tg_status launch_q4_as(const Q4Params &p, const ProductPlan &plan, hipStream_t s) {
     const int waves = plan.info.waves;
-    const unsigned lds = waves * Q4Rows<DT, MT>::LDS * 16;
-    hipLaunchKernelGGL((q4_kernel<DT, GROUP, MT, NT>), dim3((unsigned)plan.gx, plan.gy, plan.gz), dim3(64 * waves), lds,
-                       s, p);
+    const unsigned lds = waves * Q4Rows<DT>::LDS * 16;
+    hipLaunchKernelGGL((q4_kernel<DT, GROUP, NT>), dim3((unsigned)plan.gx, plan.gy, plan.gz), dim3(64 * waves), lds, s, p);
     return launched();
 }
 
@@ -34,11 +33,9 @@ template <int DT, int GROUP>
 tg_status launch_q4_group(const Q4Params &p, hipStream_t s) {
     const ProductPlan plan = plan_q4<DT>(p.experts, p.rows, p.N, p.K);
     if constexpr (DT != DT_F32) {
-        if (plan.info.tile_m == 64) return launch_q4_as<DT, GROUP, 4, 1>(p, plan, s);
-        if (plan.info.tile_m == 32) return launch_q4_as<DT, GROUP, 2, 1>(p, plan, s);
-        if (plan.info.tile_n == 32) return launch_q4_as<DT, GROUP, 1, 2>(p, plan, s);
+        if (plan.info.tile_n == 32) return launch_q4_as<DT, GROUP, 2>(p, plan, s);
     }
-    return launch_q4_as<DT, GROUP, 1, 1>(p, plan, s);
+    return launch_q4_as<DT, GROUP, 1>(p, plan, s);
 }
 
 template <int DT> using Tile256 = RingCfg<DT, 256, 256, 2, 2, 16>;

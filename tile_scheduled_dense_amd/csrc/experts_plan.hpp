@@ -134,29 +134,26 @@ ProductPlan plan_wgrad(int64_t experts, int64_t rows, int64_t M, int64_t N) {
     return p;
 }
 
-// Row tiles (MT) and n tiles (NT) of a workgroup: more of either reads the codes or
-// the activations less often, as long as there are workgroups for the 256 CUs.
-// fp32 takes one of each, in as many workgroups: two row tiles leave room for half the
-// waves, whose latency then shows (37 rows, 1001 x 4100: 12 us against 28).
-// chunks: row tiles that an expert has on average.
+// Column tiles of 16 that a workgroup takes: two, which read the activations once, from 512
+// column tiles on, or from 768 tiles with the rows there are on average; below, one, in
+// twice the workgroups (one and two, K 4096, bf16: 4096 columns, 16 rows 5.5 and 6.8 us, 32
+// rows 7.4 and 9.2, 48 rows 10.3 and 9.3, 64 rows 12.2 and 9.4; 8192, 32 rows 12.9 and 10.1;
+// f16: 6144, 16 rows 7.3 and 6.6, 8192 x 8192, 8 rows 9.1 and 9.6, 16 rows 11.7 and 10.6; 64
+// experts of 2048 x 2048 with 16 rows each 51.7 and 40.7, 8 with 2 each 6.8 and 7.4).  fp32
+// one: 37 rows of 1001 x 4100 11.7 and 17.4, 64 experts of 1024 x 1024 29.6 and 34.6; two pay
+// for a large matrix alone (16 rows of 8192 x 8192 33.4 and 28.9).
 template <int DT>
 ProductPlan plan_q4(int64_t experts, int64_t rows, int64_t N, int64_t K) {
-    const int64_t n_tiles = cdiv(N, kQ4N), k_blocks = cdiv(K, kQ4K);
-    const int64_t chunks = cdiv(cdiv(rows, experts), 16) < 64 ? cdiv(cdiv(rows, experts), 16) : 64;
-    const int64_t all = n_tiles * experts;
-    int mt = 1, nt = 1, most = q4_waves<DT, 1>();
-    if (DT != DT_F32) {
-        if (chunks > 2 && all * cdiv(chunks, 4) >= 256) mt = 4, most = q4_waves<DT, 4>();
-        else if (chunks > 1 && all * cdiv(chunks, 2) >= 256) mt = 2, most = q4_waves<DT, 2>();
-        else if (all * chunks >= 512) nt = 2;
-    }
+    const int64_t n_tiles = cdiv(N, kQ4N), k_blocks = cdiv(K, kQ4K), all = n_tiles * experts;
+    const int nt = DT != DT_F32 && (all >= 512 || all * cdiv(cdiv(rows, experts), 16) >= 768) ? 2 : 1;
     // waves that split K: more while they have four blocks each and there are not yet
-    // 4096 (a wave costs 0.6 ns to start: 64 experts of 2048 x 2048, 24 of them with
-    // rows, take 15 us in workgroups of 2 waves, 17 of 4, 27 of 8)
+    // 4096 (a wave costs 0.6 ns to start: 64 experts of 2048 x 2048, 64 rows, take 24 us in
+    // workgroups of 1 wave, 15.5 of 2, 16.4 of 4, 20 of 8; one of 4096 x 4096, 16 rows, 16,
+    // 9.5, 6.7 and 5.5)
     const int64_t strips = cdiv(n_tiles, nt);
     int waves = 1;
-    while (waves < most && waves * 4 <= k_blocks && (waves < 2 || strips * experts * waves < 4096)) waves *= 2;
-    return plan_of(TG_EXPERTS_Q4, 16 * mt, 16 * nt, waves, strips, tiles_and_slots(rows, experts, 16 * mt));
+    while (waves < q4_waves<DT>() && waves * 4 <= k_blocks && (waves < 2 || strips * experts * waves < 4096)) waves *= 2;
+    return plan_of(TG_EXPERTS_Q4, 16, 16 * nt, waves, strips, tiles_and_slots(rows, experts, 16));
 }
 
 }  // namespace tg

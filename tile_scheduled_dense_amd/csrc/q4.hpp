@@ -161,24 +161,26 @@ struct Q4Params {
 // A workgroup takes NT neighbouring n tiles of one expert; its waves split K
 // (blocks w, w + W, ...) and add their sums in LDS, in wave order.  Weights are the
 // matrix instruction's first operand, so lane l holds C[row l % 16][n 4 (l / 16)
-// .. + 3]: four neighbours in a row of C, one store.  It takes MT row tiles of 16;
-// an expert's further rows have workgroups of their own (row_slot), which read the codes
-// again, from cache.
+// .. + 3]: four neighbours in a row of C, one store.  It takes 16 rows; an expert's further
+// rows have workgroups of their own (row_slot), which read the codes again, from cache.
+// (Two or four row tiles a workgroup, to turn the codes into operands once for them, were
+// slower for every number of rows: 64 rows of 4096 x 4096 bf16 13.9 and 23.8 us against 9.4;
+// 2048 rows, K 8192, N 4096, 570 and 632 against 380.)
 //
 // The codes, scales and activations of the next block are in flight while a block
 // is multiplied.  Activations are loaded as they lie, 256 bytes of a row by 16
 // lanes (fp32: 512 by 32), and cross to the lanes that need them through LDS of
 // the wave's own, in 16-byte units whose place in a row is XORed with the row so
-// that 16 rows meet distinct banks (64 rows of 8192 x 8192 bf16: 43 us, 65 when each lane
-// loads its own operands, 64 bytes of 16 rows an instruction; at 16 rows the two are
-// equal).
+// that 16 rows meet distinct banks (64 rows of 8192 x 8192 bf16, 64 a workgroup: 43 us, 65
+// when each lane loads its own operands, 64 bytes of 16 rows an instruction; at 16 rows the
+// two are equal).
 //
-// Measured: one token through 4096 x 4096 bf16 5.6 us, a launch and its latency; 16 rows
-// through 8192 x 8192 f16 10.7 us (3.4 TB/s; the codes alone, neither multiplied nor
-// scaled, took 9.2); 64 rows over 24 of 64 experts of 2048 x 2048 bf16 15.8 us (3.3 TB/s,
-// 2.8 us of it for turning codes into bf16); 37 rows through 1001 x 4100 fp32 12 us, the
-// latency of its few workgroups.
-template <int DT, int MT>
+// Measured: one token through 4096 x 4096 bf16 5.5 us, a launch and its latency; 16 rows
+// through 8192 x 8192 f16 10.6 us (3.4 TB/s; the codes alone, neither multiplied nor
+// scaled, took 9.2), 64 rows bf16 27.7; 64 rows over 24 of 64 experts of 2048 x 2048 bf16
+// 15.1 us (3.5 TB/s, 2.8 us of it for turning codes into bf16); 37 rows through 1001 x 4100
+// fp32 11.7 us, the latency of its few workgroups.
+template <int DT>
 struct Q4Rows {
     typedef typename ElemOf<DT>::type T;
     static constexpr int E = (int)sizeof(T), PER = 16 / E;
@@ -186,7 +188,7 @@ struct Q4Rows {
     static constexpr int RPI = 64 / ROW;               // rows of a load: 4 or 2
     static constexpr int LOADS = 16 / RPI;             // loads of a row tile
     static constexpr int PIECES = DT == DT_F32 ? 2 : 1;    // units of a lane's eight k
-    static constexpr int LDS = MT * 16 * ROW;          // units of a wave's region
+    static constexpr int LDS = 16 * ROW;               // units of a wave's region
 
     rsrc_t ra;
     int voff, lda, rows, K, lane;
@@ -201,15 +203,15 @@ struct Q4Rows {
         voff = (lane / ROW * lda + lane % ROW * PER) * E;
         // rows that are never loaded
 #pragma unroll
-        for (int i = 0; i < MT * LOADS; ++i)
+        for (int i = 0; i < LOADS; ++i)
             if (i * RPI >= rows) lds[i * 64 + lane] = u32x4{0, 0, 0, 0};
     }
     // TAIL: K ends in the block (past it +0, so that a NaN behind a row's end meets no weight)
     template <bool TAIL>
-    __device__ __forceinline__ void load(int kb, int i, u32x4 (&a)[LOADS]) const {
+    __device__ __forceinline__ void load(int kb, u32x4 (&a)[LOADS]) const {
 #pragma unroll
         for (int d = 0; d < LOADS; ++d) {
-            const int r0 = 16 * i + RPI * d;
+            const int r0 = RPI * d;
             if (r0 >= rows) continue;
             const int soff = (r0 * lda + kb * kQ4K) * E;
             const bool in = r0 + lane / ROW < rows;
@@ -221,11 +223,11 @@ struct Q4Rows {
             }
         }
     }
-    __device__ __forceinline__ void stage(int i, const u32x4 (&a)[LOADS]) const {
+    __device__ __forceinline__ void stage(const u32x4 (&a)[LOADS]) const {
 #pragma unroll
         for (int d = 0; d < LOADS; ++d) {
             const int r = RPI * d + lane / ROW;
-            if (16 * i + RPI * d < rows) lds[(16 * i + r) * ROW + (lane % ROW ^ r)] = a[d];
+            if (RPI * d < rows) lds[r * ROW + (lane % ROW ^ r)] = a[d];
         }
     }
     // Activations pass from lane to lane between stage and read.  A wave's LDS operations
@@ -236,24 +238,22 @@ struct Q4Rows {
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
-    // unit h of this lane's eight k of step s, row lane % 16 of tile i
-    __device__ __forceinline__ u32x4 read(int i, int s, int h) const {
+    // unit h of this lane's eight k of step s, row lane % 16
+    __device__ __forceinline__ u32x4 read(int s, int h) const {
         const int r = lane % 16, unit = 4 * PIECES * s + PIECES * (lane / 16) + h;
-        return lds[(16 * i + r) * ROW + (unit ^ r)];
+        return lds[r * ROW + (unit ^ r)];
     }
 };
 
-template <int DT, int GROUP, int MT, int NT>
+template <int DT, int GROUP, int NT>
 struct Q4Block {
-    using Rows = Q4Rows<DT, MT>;
+    using Rows = Q4Rows<DT>;
     typedef typename ElemOf<DT>::type T;
     typedef T t4 __attribute__((ext_vector_type(4)));
     static constexpr int SCALES = kQ4K / GROUP;
-    // held ahead where that is at most 64 registers a block
-    static constexpr bool A_AHEAD = MT * Rows::LOADS <= 8;
     u32x4 w[NT];
     t4 q[NT][SCALES];           // loaded together
-    u32x4 a[A_AHEAD ? MT : 1][Rows::LOADS];
+    u32x4 a[Rows::LOADS];
 
     template <bool TAIL>
     __device__ __forceinline__ void load(const u32x4 *const (&codes)[NT], const T *const (&scales)[NT], const Rows &rows,
@@ -265,57 +265,36 @@ struct Q4Block {
 #pragma unroll
             for (int g = 0; g < SCALES; ++g) q[t][g] = from[g];
         }
-        if constexpr (A_AHEAD) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) rows.template load<TAIL>(kb, i, a[i]);
-        }
+        rows.template load<TAIL>(kb, a);
     }
-    template <bool TAIL>
-    __device__ __forceinline__ void multiply(const Rows &rows, int kb, f32x4 (&acc)[NT][MT]) {
+    __device__ __forceinline__ void multiply(const Rows &rows, f32x4 (&acc)[NT]) {
         Rows::order();          // the block before has been read
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            if constexpr (!A_AHEAD) rows.template load<TAIL>(kb, i, a[0]);
-            rows.stage(i, a[A_AHEAD ? i : 0]);
-        }
+        rows.stage(a);
         Rows::order();
-        f32x4 sum[NT][MT];
+        f32x4 sum[NT];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            u32x4 x[MT][Rows::PIECES];
+            u32x4 x[Rows::PIECES];
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < Rows::PIECES; ++h) x[i][h] = rows.read(i, s, h);
+            for (int h = 0; h < Rows::PIECES; ++h) x[h] = rows.read(s, h);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                if (32 * s % GROUP == 0) {
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) sum[t][i] = f32x4{0, 0, 0, 0};
-                }
+                if (32 * s % GROUP == 0) sum[t] = f32x4{0, 0, 0, 0};
                 if constexpr (DT == DT_F32) {
                     float f[8];
                     q4_floats(w[t][s], f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            const uint32_t y = x[i][e / 4][e % 4];
-                            sum[t][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[e], __builtin_bit_cast(float, y), sum[t][i],
-                                                                             0, 0, 0);
-                        }
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t y = x[e / 4][e % 4];
+                        sum[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[e], __builtin_bit_cast(float, y), sum[t], 0, 0, 0);
+                    }
                 } else {
-                    const u32x4 b = q4_operand<DT>(w[t][s]);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) mfma_chunk<DT>(b, x[i][0], sum[t][i]);
+                    mfma_chunk<DT>(q4_operand<DT>(w[t][s]), x[0], sum[t]);
                 }
                 if ((32 * s + 32) % GROUP == 0) {
                     const t4 c = q[t][32 * s / GROUP];
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            acc[t][i][v] = __builtin_fmaf((float)c[v], sum[t][i][v], acc[t][i][v]);
+                    for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf((float)c[v], sum[t][v], acc[t][v]);
                 }
             }
         }
@@ -323,26 +302,26 @@ struct Q4Block {
 };
 
 // Waves of a workgroup at most: their LDS regions are 64 KiB together.
-template <int DT, int MT>
+template <int DT>
 constexpr int q4_waves() {
-    const int fit = 65536 / (Q4Rows<DT, MT>::LDS * 16);
+    const int fit = 65536 / (Q4Rows<DT>::LDS * 16);
     return fit < 8 ? fit : 8;
 }
 
-template <int DT, int GROUP, int MT, int NT>
+template <int DT, int GROUP, int NT>
 __global__ __launch_bounds__(512) void q4_kernel(Q4Params p) {
-    using Block = Q4Block<DT, GROUP, MT, NT>;
-    using Rows = Q4Rows<DT, MT>;
+    using Block = Q4Block<DT, GROUP, NT>;
+    using Rows = Q4Rows<DT>;
     typedef typename Block::T T;
-    extern __shared__ u32x4 q4_lds[];                // [waves][Rows::LDS], then the sums [waves][NT * MT][64]
-    static_assert(Rows::LDS >= NT * MT * 64, "the sums fit the waves' regions");
+    extern __shared__ u32x4 q4_lds[];                // [waves][Rows::LDS], then the sums [waves][NT][64]
+    static_assert(Rows::LDS >= NT * 64, "the sums fit the waves' regions");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // the same in every lane of a wave
     const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
     const bool wide = p.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(p.C) % 16 == 0;
     const int tile = blockIdx.x * NT;
     int g;
     RowSpan span;
-    if (!row_slot<16 * MT>(p.offsets, p.experts, p.rows, slot_of(p.experts), g, span)) return;
+    if (!row_slot<16>(p.offsets, p.experts, p.rows, slot_of(p.experts), g, span)) return;
     const bool dead = g == p.experts || p.K == 0;    // zeros
     const int n0 = tile * kQ4N + 4 * (lane / 16);
     const u32x4 *codes[NT];
@@ -355,11 +334,9 @@ __global__ __launch_bounds__(512) void q4_kernel(Q4Params p) {
         scales[t] = reinterpret_cast<const T *>(p.scales) + at * p.groups * kQ4N + 4 * (kQ4K / GROUP) * (lane / 16);
     }
     const int r0 = span.lo;
-    f32x4 acc[NT][MT];
+    f32x4 acc[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[t][i] = f32x4{0, 0, 0, 0};
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
     if (!dead) {
         Rows rows;
         const int count = __builtin_amdgcn_readfirstlane(span.hi - r0);
@@ -371,11 +348,11 @@ __global__ __launch_bounds__(512) void q4_kernel(Q4Params p) {
             b.template load<false>(codes, scales, rows, kb);
             for (;;) {
                 if (kb + waves < full) n.template load<false>(codes, scales, rows, kb + waves);
-                b.template multiply<false>(rows, kb, acc);
+                b.multiply(rows, acc);
                 kb += waves;
                 if (kb >= full) break;
                 if (kb + waves < full) b.template load<false>(codes, scales, rows, kb + waves);
-                n.template multiply<false>(rows, kb, acc);
+                n.multiply(rows, acc);
                 kb += waves;
                 if (kb >= full) break;
             }
@@ -383,20 +360,18 @@ __global__ __launch_bounds__(512) void q4_kernel(Q4Params p) {
         if (kb < p.k_blocks) {
             Block b;
             b.template load<true>(codes, scales, rows, kb);
-            b.template multiply<true>(rows, kb, acc);
+            b.multiply(rows, acc);
         }
     }
     __syncthreads();
     f32x4 *sums = reinterpret_cast<f32x4 *>(q4_lds);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) sums[((wave * NT + t) * MT + i) * 64 + lane] = acc[t][i];
+    for (int t = 0; t < NT; ++t) sums[(wave * NT + t) * 64 + lane] = acc[t];
     __syncthreads();
-    for (int q = wave; q < NT * MT; q += waves) {
-        f32x4 v = sums[q * 64 + lane];
-        for (int w = 1; w < waves; ++w) v += sums[(w * NT * MT + q) * 64 + lane];
-        const int r = r0 + 16 * (q % MT) + lane % 16, n = n0 + 16 * (q / MT);
+    for (int t = wave; t < NT; t += waves) {
+        f32x4 v = sums[t * 64 + lane];
+        for (int w = 1; w < waves; ++w) v += sums[(w * NT + t) * 64 + lane];
+        const int r = r0 + lane % 16, n = n0 + 16 * t;
         v *= Q4Unit<DT>::value;
         if (r < span.hi && n < p.N) store4<DT>(p.C, (int64_t)r * p.ldc + n, p.N - n, p.c_f32, wide, v);
     }
