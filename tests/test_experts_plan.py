@@ -125,3 +125,12 @@ def test_streamed_rows_of_one_expert_are_not_one_workgroups(experts, rows, N, K,
                                                  (16, 128, 1024, 1024, "f32"), (4, 9000, 300, 512, "bf16")])
 def test_rows_of_one_4_bit_expert_are_not_one_workgroups(experts, rows, N, K, dt):
     has(tg.tile_gemm_q4_plan(experts, rows, N, K, 128, dt), kernel="q4", row_tiles=1)
+
+
+@pytest.mark.parametrize("dt,experts,M,N", [("bf16", 64, 100, 100), ("bf16", 64, 384, 384), ("f16", 33, 257, 1000),
+                                                 ("f32", 9, 64, 64), ("bf16", 64, 512, 512)])
+def test_weight_gradients_have_a_workgroup_a_tile(dt, experts, M, N):
+    """Workgroups go to the eight XCDs in turn, so that tiles without gaps are even between them."""
+    plan = tg.tile_gemm_grouped_wgrad_plan(experts, 1100 * experts, M, N, dt)
+    tiles = -(-M // plan["tile_m"]) * -(-N // plan["tile_n"])
+    has(plan, kernel="tiles", workgroups=experts * tiles)

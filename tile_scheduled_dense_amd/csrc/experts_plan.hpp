@@ -128,7 +128,7 @@ ProductPlan plan_wgrad(int64_t experts, int64_t rows, int64_t M, int64_t N) {
         tile = 256;
         pipeline = true;
     }
-    ProductPlan p = plan_of(TG_EXPERTS_TILES, tile, tile, 4, experts * cdiv(cdiv(M, tile) * cdiv(N, tile), 8) * 8);
+    ProductPlan p = plan_of(TG_EXPERTS_TILES, tile, tile, 4, experts * cdiv(M, tile) * cdiv(N, tile));
     p.info.pipeline = pipeline;
     p.lds_copies = pipeline ? 4 : 3;
     return p;
