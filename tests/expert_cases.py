@@ -29,14 +29,14 @@ TILE256 = [
 
 # 256 x 256 tiles of the weights' gradient: dtype, out, rows of each expert, rows of no expert, M, N, pad, skew
 WGRAD256 = [
-    ("bf16", "bf16", [3100, 0, 1005, 1], 0, 2304, 2048, 0, 0),
-    ("bf16", "f32", [1, 2111, 1005], 9, 2307, 2050, 1, 1),
+    ("bf16", "bf16", [3100, 0, 1005, 1], 0, 2040, 2048, 0, 0),
+    ("bf16", "f32", [1, 2111, 1005], 9, 2303, 2090, 1, 1),
     ("f16", "f16", [4093], 0, 3650, 3588, 0, 0),
-    ("f16", "f32", [600, 1500, 1024], 0, 2055, 2500, 0, 1),
-    ("bf16", "bf16", [2100 * (g % 2) + g % 3 for g in range(71)], 0, 490, 500, 0, 0),      # more than 64 experts
+    ("f16", "f32", [600, 1500, 1024], 0, 2055, 2301, 0, 1),
+    ("bf16", "bf16", [2100 * (g % 2) + g % 3 for g in range(121)], 0, 490, 500, 0, 0),     # more than 64 experts
     ("bf16", "bf16", [2000, 900, 0, 1300], 0, 5888, 5800, 0, 0),                           # past the caches
-    ("f32", "f32", [2090, 2047, 0, 20], 0, 3600, 3838, 0, 0),
-    ("f32", "f32", [1025, 1100, 1030, 999], 2, 3585, 3841, 1, 1),
+    ("f32", "f32", [1030], 0, 7960, 8190, 0, 0),
+    ("f32", "f32", [1025, 1100, 1030, 999], 2, 4093, 4091, 1, 1),                          # past the caches
 ]
 
 # streamed weights, eight waves: dtype, experts, rows, spare, active, N, K, pad, skew, transposed

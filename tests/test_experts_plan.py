@@ -134,3 +134,13 @@ def test_weight_gradients_have_a_workgroup_a_tile(dt, experts, M, N):
     plan = tg.tile_gemm_grouped_wgrad_plan(experts, 1100 * experts, M, N, dt)
     tiles = -(-M // plan["tile_m"]) * -(-N // plan["tile_n"])
     has(plan, kernel="tiles", workgroups=experts * tiles)
+
+
+@pytest.mark.parametrize("dt,experts,M,N,tile", [
+    ("bf16", 16, 1024, 1024, 256), ("f16", 12, 1024, 1024, 128), ("bf16", 17, 1024, 1024, 128), ("bf16", 64, 512, 512, 256),
+    ("bf16", 8, 1300, 1304, 128), ("bf16", 5, 2048, 2048, 128), ("bf16", 8, 2048, 4096, 256), ("f32", 16, 2048, 2048, 256),
+    ("f32", 8, 2560, 2560, 64), ("f32", 4, 3600, 3840, 64),
+])
+def test_tile_of_a_weight_gradient_by_its_rounds(dt, experts, M, N, tile):
+    """The largest tile is for rounds that it fills (times of both sides: experts_plan.hpp)."""
+    has(tg.tile_gemm_grouped_wgrad_plan(experts, 1100 * experts, M, N, dt, c_dtype=dt), kernel="tiles", tile_m=tile)

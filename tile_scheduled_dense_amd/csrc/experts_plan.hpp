@@ -108,12 +108,20 @@ ProductPlan plan_grouped(bool transposed, int64_t experts, int64_t rows, int64_t
     return transposed ? plan_grouped_as<DT, true>(experts, rows, N, K) : plan_grouped_as<DT, false>(experts, rows, N, K);
 }
 
-// The tile of the weights' gradient, by the same rules; its contraction is an expert's
-// rows, on average.  256 x 256 from 200 tiles on (16 experts of 1024 x 1024: 29.8 us
-// against 32.2 on 128 x 128; 8 experts 35.9 against 32.1), unless 128 x 128 pads the
-// extents by a fifth less.  128 x 128 with the software pipeline where no CU has a
-// second tile to hide the first one's waits (464 x 96 over 1464 rows, 2 experts: 20.4 ->
-// 13.1 us; 33 of 257 x 1000 over 150 16.9 -> 20.9).
+// The tile of the weights' gradient; its contraction is an expert's rows, on average.
+//  * 256 x 256 over a long one from 200 such tiles on, fp32 800 (fewer leave a popular
+//    expert's tiles to end alone: 12 uneven experts of 1024 x 1024, 192 tiles, 79 us and 60.5
+//    on 128 x 128, even ones 35.5 and 43), where whole rounds of 256 of them (one a CU)
+//    cover at most half more than the small tiles do, padding and part-filled rounds
+//    together; fp32, whose small tile reaches the same rate, a twentieth more (bf16, 1100
+//    rows an expert, 256 x 256 and 128 x 128: 16 experts of 1024 x 1024, a whole round, 44.6
+//    and 56.5 us, 20, 1.6, 76.4 and 67.8, 17, 1.88, 74.6 and 62.2; 8 of 1300 x 1304, 2.1, 61
+//    and 49; 64 of 512 x 512, 1.0, 54.6 and 71.3; over 2500 rows 1.6 is 133 and 144, 2.1 114
+//    and 112; fp32 against 64 x 64: 8 of 2048 x 2048, 1.0, 536 and 545, 4 of 3600 x 3840,
+//    1.2, 1385 and 1206).
+//  * else 128 x 128, fp32 64 x 64; with the software pipeline where no CU has a second tile
+//    to hide the first one's waits (464 x 96 over 1464 rows, 2 experts: 20.4 -> 13.1 us; 33
+//    of 257 x 1000 over 150 16.9 -> 20.9).
 template <int DT>
 ProductPlan plan_wgrad(int64_t experts, int64_t rows, int64_t M, int64_t N) {
     if (M < kNarrow || N < kNarrow) {
@@ -121,10 +129,12 @@ ProductPlan plan_wgrad(int64_t experts, int64_t rows, int64_t M, int64_t N) {
         return plan_of(TG_EXPERTS_NARROW, M < N ? (int)M : width, M < N ? width : (int)N, 16, cdiv(M < N ? N : M, width),
                        experts);
     }
-    const int64_t each = cdiv(M, 256) * cdiv(N, 256), small = cdiv(M, 128) * cdiv(N, 128);
     int tile = DT == DT_F32 ? 64 : 128;
-    bool pipeline = DT == DT_F32 || experts * small <= 256;
-    if (experts * each >= (DT == DT_F32 ? 800 : 200) && 4 * each * 4 <= 5 * small && cdiv(rows, experts) >= kLong) {
+    const int64_t small = experts * cdiv(M, tile) * cdiv(N, tile);
+    const int64_t large = experts * cdiv(M, 256) * cdiv(N, 256), area = cdiv(large, kRound) * kRound;
+    bool pipeline = DT == DT_F32 || small <= 256;
+    if (cdiv(rows, experts) >= kLong && (DT == DT_F32 ? large >= 800 && 20 * 16 * area <= 21 * small
+                                                      : large >= 200 && 2 * 4 * area <= 3 * small)) {
         tile = 256;
         pipeline = true;
     }

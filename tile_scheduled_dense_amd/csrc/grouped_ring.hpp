@@ -583,10 +583,10 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void grouped_tile_kernel(
 // a contiguous run each (an XCD of its own for a popular expert would work on
 // alone); workgroups go to them in turn, so that no gap may lie between experts (a
 // multiple of eight for each left XCDs idle: 256 experts of 128 x 128 bf16, 65536 rows, 41
-// us and 10 without, 10 of 1280 x 1280 67.5 and 41.5).  Up to 64 experts go in order of their rows, the most first, so that the last
-// tiles to end are short ones (8 uneven experts of 2048 x 4096: 220 -> 214 us; the order
-// costs a small tile more than it gives: 33 of 257 x 1000 19.0 -> 20.5, so only the
-// large ones).
+// us and 10 without, 10 of 1280 x 1280 67.5 and 41.5).  Up to 64 experts go in order of
+// their rows, the most first, so that the last tiles to end are short ones (8 uneven
+// experts of 2048 x 4096: 220 -> 214 us; the order costs a small tile more than it gives:
+// 33 of 257 x 1000 19.0 -> 20.5, so only the large ones).
 template <class C, bool PIPE, int STAGES>
 __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void wgrad_tile_kernel(GroupedParams p) {
     __shared__ __attribute__((aligned(1024))) char smem[GroupedTile<C, true, true, STAGES>::LDS];
