@@ -74,13 +74,18 @@ constexpr int64_t kLong = 1024;
 
 // The tile of a product over rows.
 //  * The weights are streamed, by workgroups that split K among their waves, while they
-//    are at most 96 MiB and an expert has on average at most 8 rows, or at most 128 and
-//    a workgroup a CU takes all 16-row tiles at the same time (bf16: 8 experts of 1024 x
-//    4096, 4 rows 13.6 us against 17.6 on tiles; one of 4096 x 256, 16 rows 14.5 against
-//    45.6, 96 rows 14.6 against 45.9; 4 of 2048 x 2048, 24 rows 11.1 against 24.3; but 32
-//    of 2048 x 1024, 4 rows, 31.5 against 24.6, where the tiles' copies read at 5.5 TB/s,
-//    and two workgroups a CU, 8 experts of 1024 x 4096, 32 rows, 28.7 against 18.1).  So
-//    is an N below kNarrow, of which a tile would be mostly empty (and the tiles need a
+//    are at most 96 MiB and an expert has on average at most 8 rows, or at most 128 in
+//    fewer than 256 workgroups.  bf16, streamed and on tiles, weights from HBM:
+//      up to 8 rows    8 experts of 1024 x 4096 (K x N), 32 rows 16.3 and 19.5 us; one of
+//                      1024 x 4096, 8 rows 7.6 and 14.5
+//      16 each         8 of 2048 x 4096, even 29.7 and 32.5, skewed 38.3 and 32.4
+//      workgroups      16 of 512 x 256, 63 rows each, 128 of them, 6.9 and 9.4, 125 rows, 256,
+//                      11.3 and 9.7; 2 of 2048 x 4096 transposed, 128 rows each, 2048, 49.5
+//                      and 29.3
+//      96 MiB          12 of 1024 x 4096, 48 rows 26.3 and 22.9, 64 of 1024 x 768, 512 rows
+//                      skewed 25.6 and 31.7; more: 64 of 2048 x 2048, 500 rows 101 and 114
+//                      (transposed 92 and 115), but in one expert 28.7 and 25.5 (50 and 24)
+//    So is an N below kNarrow, of which a tile would be mostly empty (and the tiles need a
 //    16-byte chunk of it: grouped_ring.hpp).
 //  * 16 bits: 256 x 256 over a long K from 128 such tiles on (f16, 8 uneven experts, K
 //    1024: 4096 x 2048 32.0 against 33.4 us on 128 x 128, 2048 x 2048 26.5 against 22.6),
