@@ -32,8 +32,8 @@
  *    id is outside 0 .. experts - 1 (-1 marks a choice that a capacity limit
  *    dropped).  Those entries' rows come after every expert's.  entry_of_row is
  *    the inverse: the entry of each row, complemented for rows without an expert.
- *    Both are contiguous.  offsets[g] is the first row of expert g and
- *    offsets[experts] the number of rows that have one; they must not decrease.
+ *    Both are contiguous.  offsets[g] is the first row of expert g (offsets[0] is 0)
+ *    and offsets[experts] the number of rows that have one; they must not decrease.
  *    Tables live in device memory and are not checked on the host.  The kernels
  *    clamp what they read to the rows there are, so a wrong table gives wrong
  *    results and no access outside the operands.

@@ -19,11 +19,13 @@
 // last chunk would pass a matrix's end) goes through registers with element-exact
 // zeros in both operands, so that a NaN behind K meets none.
 //
-// Measured, 16384 rows x 4096 x 2048 bf16 over 8 experts with a bf16 result: even experts
-// 209 us forward, 203 for the rows' gradient, 202-210 for the weights' (1310-1360 TFLOP/s,
-// the rate of a large library product on this card); uneven ones 223-230, 238 and 214, where
-// part-filled tile rows and the last round show.  Bound by the matrix cores while K is
-// long; under about 1024 by the start and the stores of a tile.
+// Measured, 16384 rows x 4096 x 2048 bf16 over 8 experts with a bf16 result, inputs that
+// change from call to call: even experts 229 us forward, 229 for the rows' gradient, 219 for
+// the weights' (1200-1255 TFLOP/s); uneven ones 240-245, 259-267 and 219-223, where
+// part-filled tile rows and the last round show.  On the same inputs again, half of them in
+// the last-level cache, 214, 207 and 208 (1282-1329 TFLOP/s, the rate of a large library
+// product on this card) and 227, 234 and 211.  Bound by the matrix cores while K is long;
+// under about 1024 by the start and the stores of a tile.
 //
 // B's fragments are the matrix instruction's first operand and A's the second:
 // a lane then holds four neighbouring columns of one row of C, so that C is
