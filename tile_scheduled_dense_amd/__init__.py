@@ -36,7 +36,7 @@ LAYOUT_CFG_STRIP_N, LAYOUT_CFG_STRIP_M = 101, 102
 LAYOUT_CFG_F32_256, LAYOUT_CFG_F32_128, LAYOUT_CFG_F32_STRIP_N, LAYOUT_CFG_F32_STRIP_M = 103, 104, 105, 106
 SWZ_DEFAULT, SWZ_NONE, SWZ_PAD, SWZ_XOR = 0, 1, 2, 3
 BIAS_NONE, BIAS_PER_COLUMN, BIAS_PER_ROW = 0, 1, 2
-ACT_NONE, ACT_RELU, ACT_GELU = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3     # SiLU: tile_gemm_gated and its gradient
 
 LAYOUT_LDS_A, LAYOUT_LDS_B, LAYOUT_ACC, LAYOUT_COPY_A = range(4)
 AXIS_M, AXIS_LANE, AXIS_WAVE, AXIS_PID, AXIS_TLANE, AXIS_TCOL = range(6)
@@ -55,6 +55,11 @@ EXPORTED_EXPERTS = ["tile_gemm_experts_version", "tile_gemm_expert_sort_workspac
                     "tile_gemm_expert_gather", "tile_gemm_expert_combine", "tile_gemm_expert_combine_grad",
                     "tile_gemm_grouped", "tile_gemm_grouped_wgrad", "tile_gemm_q4_packed_size", "tile_gemm_pack_q4",
                     "tile_gemm_q4", "tile_gemm_grouped_plan", "tile_gemm_grouped_wgrad_plan", "tile_gemm_q4_plan"]
+# every symbol include/tile_gemm_ffn.h declares
+EXPORTED_FFN = ["tile_gemm_ffn_version", "tile_gemm_gated_workspace_size", "tile_gemm_gated", "tile_gemm_gated_grad",
+                "tile_gemm_adapters_workspace_size", "tile_gemm_adapters", "tile_gemm_adapters_wgrad_workspace_size",
+                "tile_gemm_adapters_wgrad"]
+FFN_VERSION = 1         # TILE_GEMM_FFN_VERSION
 EXPERTS_VERSION = 2     # TILE_GEMM_EXPERTS_VERSION
 MAX_EXPERTS = 2048      # TILE_GEMM_MAX_EXPERTS
 
@@ -176,6 +181,7 @@ def _lib():
     lib.tile_gemm_pack_b.argtypes = [i64, i64, i64, ci, vp, i64, i64, ci, vp, i64, vp]
     lib.tile_gemm_pack_b.restype = ci
     _declare_experts(lib, i64, vp, ci)
+    _declare_ffn(lib, i64, vp, ci)
     _lib_handle = lib
     return lib
 
@@ -199,6 +205,27 @@ def _declare_experts(lib, i64, vp, ci):
         "tile_gemm_grouped_plan": [i64, i64, i64, i64, ci, ci, ci, info],
         "tile_gemm_grouped_wgrad_plan": [i64, i64, i64, i64, ci, ci, info],
         "tile_gemm_q4_plan": [i64, i64, i64, i64, i64, ci, ci, info],
+    }.items():
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ci
+
+
+def _declare_ffn(lib, i64, vp, ci):
+    """Argument types of the operators of a feed-forward block (include/tile_gemm_ffn.h)."""
+    size = ctypes.POINTER(i64)
+    for name, args in {
+        "tile_gemm_ffn_version": [],
+        "tile_gemm_gated_workspace_size": [i64, i64, i64, i64, ci, ci, size],
+        "tile_gemm_gated": [i64, i64, i64, i64, ci, vp, i64, vp, vp, i64, i64, ci, ci, vp, i64, vp, vp, i64, vp, vp, i64,
+                            vp],
+        "tile_gemm_gated_grad": [i64, i64, i64, i64, ci, vp, i64, vp, i64, i64, ci, ci, vp, vp, i64, vp, vp, i64, vp, i64,
+                                 vp, vp],
+        "tile_gemm_adapters_workspace_size": [i64, i64, i64, i64, i64, ci, ci, size],
+        "tile_gemm_adapters": [i64, i64, i64, i64, i64, ci, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, ci, vp, vp, i64,
+                               vp, i64, vp, vp, vp, i64, vp],
+        "tile_gemm_adapters_wgrad_workspace_size": [i64, i64, i64, i64, i64, ci, size],
+        "tile_gemm_adapters_wgrad": [i64, i64, i64, i64, i64, ci, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp,
+                                     i64, i64, ci, ci, vp, vp, vp, i64, vp],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ci
@@ -456,6 +483,82 @@ def tile_gemm_grouped_wgrad_plan(experts, rows, M, N, dtype, c_dtype="f32") -> d
 def tile_gemm_q4_plan(experts, rows, N, K, group, dtype, c_dtype="f32") -> dict:
     """The tile and grid of a tile_gemm_q4 call."""
     return _experts_plan("tile_gemm_q4_plan", experts, rows, N, K, group, _dtype(dtype), _dtype(c_dtype))
+
+
+# ---- the operators of a feed-forward block (include/tile_gemm_ffn.h) ---------------------
+def ffn_version() -> int:
+    return int(_lib().tile_gemm_ffn_version())
+
+
+def _size(fn, *args) -> int:
+    n = ctypes.c_int64(0)
+    _check(getattr(_lib(), fn)(*args, ctypes.byref(n)), fn)
+    return int(n.value)
+
+
+def tile_gemm_gated_workspace_size(experts, rows, N, K, dtype, transposed=0) -> int:
+    """Bytes of workspace with which tile_gemm_gated splits K over more workgroups (0: none)."""
+    return _size("tile_gemm_gated_workspace_size", experts, rows, N, K, _dtype(dtype), int(transposed))
+
+
+def tile_gemm_gated(experts, rows, N, K, dtype, A, lda, B, B_up, ldb, strideB, H, ldh, offsets=None, activation=ACT_SILU,
+                    transposed=0, U=None, V=None, ldu=0, workspace=None, workspace_bytes=None, stream=None) -> None:
+    """H[r] = act(A[r] . B[g]) * (A[r] . B_up[g]) for the rows offsets[g] .. offsets[g + 1] of every expert g;
+    matrices K x N, or N x K with transposed=1.  U, V: the two products, for the gradient.  offsets None: one
+    expert with every row."""
+    if workspace_bytes is None:
+        workspace_bytes = _bytes_of(workspace)
+    _check(_lib().tile_gemm_gated(experts, rows, N, K, _dtype(dtype), _addr(A), lda, _addr(B), _addr(B_up), ldb, strideB,
+                                  int(transposed), int(activation), _addr(H), ldh, _addr(U), _addr(V), ldu,
+                                  _addr(offsets), _addr(workspace), workspace_bytes, _stream(stream)), "tile_gemm_gated")
+
+
+def tile_gemm_gated_grad(experts, rows, N, K, dtype, D, ldd, B, ldb, strideB, U, V, ldu, dU, dV, lddu, offsets=None,
+                         activation=ACT_SILU, transposed=0, H=None, ldh=0, stream=None) -> None:
+    """dU = d_h * V * act'(U), dV = d_h * act(U), and H = act(U) * V if given, for d_h = D . B[g] (B[g] K x N, or
+    N x K with transposed=1: a down projection as it is stored inputs x outputs)."""
+    _check(_lib().tile_gemm_gated_grad(experts, rows, N, K, _dtype(dtype), _addr(D), ldd, _addr(B), ldb, strideB,
+                                       int(transposed), int(activation), _addr(U), _addr(V), ldu, _addr(dU), _addr(dV),
+                                       lddu, _addr(H), ldh, _addr(offsets), _stream(stream)), "tile_gemm_gated_grad")
+
+
+def tile_gemm_adapters_workspace_size(adapters, rows, N, K, rank, dtype, transposed=0) -> int:
+    """Bytes of workspace that tile_gemm_adapters needs."""
+    return _size("tile_gemm_adapters_workspace_size", adapters, rows, N, K, rank, _dtype(dtype), int(transposed))
+
+
+def tile_gemm_adapters(adapters, rows, N, K, rank, dtype, X, ldx, W, ldw, A, lda, strideA, B, ldb, strideB, Y, ldy, offsets,
+                       workspace, order=None, scales=None, transposed=0, T=None, ldt=0, workspace_bytes=None,
+                       stream=None) -> None:
+    """Y[r] = X[r] . W + t[r] . B[g], t[r] = scales[g] * (X[r] . A[g]), g the adapter of row r: position p of the
+    adapters' order is row order[p] (None: p), adapter g has the positions offsets[g] .. offsets[g + 1], those
+    behind the last have none.  W, A[g], B[g]: K x N, K x rank, rank x N, or with transposed=1 N x K, rank x K,
+    N x rank.  T: t, for the gradients."""
+    if workspace_bytes is None:
+        workspace_bytes = _bytes_of(workspace)
+    _check(_lib().tile_gemm_adapters(adapters, rows, N, K, rank, _dtype(dtype), _addr(X), ldx, _addr(W), ldw, _addr(A), lda,
+                                     strideA, _addr(B), ldb, strideB, int(transposed), _addr(scales), _addr(Y), ldy,
+                                     _addr(T), ldt, _addr(offsets), _addr(order), _addr(workspace), workspace_bytes,
+                                     _stream(stream)), "tile_gemm_adapters")
+
+
+def tile_gemm_adapters_wgrad_workspace_size(adapters, rows, N, K, rank, dtype) -> int:
+    """Bytes of workspace that tile_gemm_adapters_wgrad needs."""
+    return _size("tile_gemm_adapters_wgrad_workspace_size", adapters, rows, N, K, rank, _dtype(dtype))
+
+
+def tile_gemm_adapters_wgrad(adapters, rows, N, K, rank, dtype, X, ldx, dY, ldy, T, ldt, dT, lddt, dA, lda, strideA, dB,
+                             ldb, strideB, offsets, workspace, order=None, c_dtype="f32", transposed=0,
+                             workspace_bytes=None, stream=None) -> None:
+    """dA[g] = X^T . dT and dB[g] = T^T . dY over the rows of every adapter g (K x rank and rank x N, or rank x K and
+    N x rank with transposed=1); T and dT: what tile_gemm_adapters stored forward and backward."""
+    if workspace_bytes is None:
+        workspace_bytes = _bytes_of(workspace)
+    _check(_lib().tile_gemm_adapters_wgrad(adapters, rows, N, K, rank, _dtype(dtype), _addr(X), ldx, _addr(dY), ldy,
+                                           _addr(T), ldt, _addr(dT), lddt, _addr(dA), lda, strideA, _addr(dB), ldb,
+                                           strideB, int(transposed), _dtype(c_dtype), _addr(offsets), _addr(order),
+                                           _addr(workspace), workspace_bytes, _stream(stream)),
+           "tile_gemm_adapters_wgrad")
 
 
 def make_layout(shape, shard, replica=(), offset=None, swizzle=None) -> Layout:

@@ -14,11 +14,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libtile_gemm.so")
 # the C ABIs and planning, the layout introspection, and one translation unit per
-# input type for the GEMM kernels and for the expert products (compiled in
-# parallel, then linked)
+# input type for the GEMM kernels, for the expert products and for each operator of a
+# feed-forward block (compiled in parallel, then linked)
 SOURCES = [os.path.join(CSRC, f) for f in ("tile_gemm.hip", "layout.hip", "launch_bf16.hip", "launch_f16.hip",
                                            "launch_f32.hip", "experts.hip", "experts_bf16.hip", "experts_f16.hip",
-                                           "experts_f32.hip")]
+                                           "experts_f32.hip", "ffn.hip", "gated_bf16.hip", "gated_f16.hip",
+                                           "gated_f32.hip", "adapters_bf16.hip", "adapters_f16.hip",
+                                           "adapters_f32.hip")]
 BUILD_DIR = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,9 @@
+// adapters_f32.hip -- the f32 kernels of a projection with adapters (ffn.hpp).
+#include "adapters_kernels.hpp"
+
+namespace tg {
+
+template tg_status launch_adapters<DT_F32>(const AdapterParams &p, bool transposed, void *workspace, hipStream_t s);
+template tg_status launch_adapters_wgrad<DT_F32>(const AdapterGradParams &p, void *workspace, hipStream_t s);
+
+}  // namespace tg

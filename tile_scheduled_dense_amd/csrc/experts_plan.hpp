@@ -55,10 +55,11 @@ inline int64_t most_tiles(int64_t rows, int64_t groups, int64_t bm) {
 
 // The grid is the most there can be: whole tiles and, with pieces, three more for each
 // tile that is split, and a row of pieces for every group.
-inline ProductPlan plan_tiles(int64_t experts, int64_t rows, int64_t N, int tile, bool pieces, bool pipeline, int copies) {
-    int64_t grid = most_tiles(rows, experts + 1, tile) * cdiv(N, tile);
-    if (pieces) grid += 3 * kSplitRound + (rows < experts + 1 ? rows : experts + 1) * cdiv(N, tile / 2);
-    ProductPlan p = plan_of(TG_EXPERTS_TILES, tile, tile, 4, grid);
+inline ProductPlan plan_tiles(int64_t experts, int64_t rows, int64_t N, int tile_m, int tile_n, bool pieces, bool pipeline,
+                              int copies) {
+    int64_t grid = most_tiles(rows, experts + 1, tile_m) * cdiv(N, tile_n);
+    if (pieces) grid += 3 * kSplitRound + (rows < experts + 1 ? rows : experts + 1) * cdiv(N, tile_n / 2);
+    ProductPlan p = plan_of(TG_EXPERTS_TILES, tile_m, tile_n, 4, grid);
     p.info.pieces = pieces;
     p.info.pipeline = pipeline;
     p.lds_copies = copies;
@@ -104,9 +105,9 @@ ProductPlan plan_grouped_as(int64_t experts, int64_t rows, int64_t N, int64_t K)
     const bool stream = weights <= (int64_t(96) << 20) && (mean <= 8 || (mean <= 128 && strips < 256));
     if (stream || N < kNarrow) return plan_stream<DT, TRANS>(experts, rows, N, K);
     const int64_t tiles = cdiv(rows, 256) * cdiv(N, 256);
-    if (K >= kLong && tiles >= (DT == DT_F32 ? 800 : 128)) return plan_tiles(experts, rows, N, 256, true, true, 4);
-    return DT == DT_F32 ? plan_tiles(experts, rows, N, 64, false, true, 4)
-                        : plan_tiles(experts, rows, N, 128, false, false, 3);
+    if (K >= kLong && tiles >= (DT == DT_F32 ? 800 : 128)) return plan_tiles(experts, rows, N, 256, 256, true, true, 4);
+    return DT == DT_F32 ? plan_tiles(experts, rows, N, 64, 64, false, true, 4)
+                        : plan_tiles(experts, rows, N, 128, 128, false, false, 3);
 }
 template <int DT>
 ProductPlan plan_grouped(bool transposed, int64_t experts, int64_t rows, int64_t N, int64_t K) {

@@ -1,0 +1,9 @@
+// gated_f32.hip -- the f32 kernels of the gated pair and its gradient (ffn.hpp).
+#include "gated_kernels.hpp"
+
+namespace tg {
+
+template tg_status launch_gated<DT_F32>(const GatedParams &p, bool transposed, void *workspace, hipStream_t s);
+template tg_status launch_gate_grad<DT_F32>(const GatedParams &p, bool transposed, hipStream_t s);
+
+}  // namespace tg

@@ -107,7 +107,7 @@ struct GemmParams {
 // |z| < 1 and runs both sides when the lanes of a wave differ.  The error is
 // relative, so the negative tail keeps its accuracy, where x / 2 * (1 + erf)
 // cancels; in fp32 the result is within 2.4e-7 |x| of x * Phi(x).
-__device__ __forceinline__ float gelu(float x) {
+__device__ __forceinline__ float normal_cdf(float x) {
     const float z = __builtin_fabsf(x) * 0.70710678118654752f;
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, z, 1.0f));
     float q = 0.17087277f;
@@ -121,8 +121,9 @@ __device__ __forceinline__ float gelu(float x) {
     q = __builtin_fmaf(q, t, 1.00002368f);
     q = __builtin_fmaf(q, t, -1.26551223f);
     const float h = 0.5f * t * __builtin_amdgcn_exp2f((q - z * z) * 1.4426950408889634f);
-    return x * (x >= 0.0f ? 1.0f - h : h);
+    return x >= 0.0f ? 1.0f - h : h;
 }
+__device__ __forceinline__ float gelu(float x) { return x * normal_cdf(x); }
 
 // The tail's activation: 1 = ReLU (x < 0 ? 0 : x, so a NaN stays NaN), 2 = GELU.
 __device__ __forceinline__ float tail_activation(float x, int act) {

@@ -149,11 +149,171 @@ struct RingOperand {
     }
 };
 
-template <class C, bool A_KS, bool B_KS, int STAGES>
+// Row p of a table of rows, clamped to the rows there are; an entry may be complemented
+// (as the token exchange's tables are, for rows without an expert).
+__device__ __forceinline__ int row_in(const int32_t *order, int p, int rows) {
+    const int r = order[p], t = r < 0 ? ~r : r;
+    return t < rows ? t : rows - 1;
+}
+
+// The store of a workgroup's tile of a result whose value v (0 .. 3: neighbouring columns)
+// of MFMA tile (i, j) of this lane is value(i, j, v) (integral constants).  C: the
+// configuration of the product; TN: column tiles of 16 a wave has of the result.
+// ORDERED: row m of the tile is row order[m] of C (of `total`), and `at` an offset in a row.
+template <class C, int TN, class F, bool ORDERED = false>
+struct TileStore {
+    const F &value;
+    const int lane, wave;
+    const int32_t *order = nullptr;
+    const int total = 0;
+    static constexpr int WTN = 16 * TN, BN = C::WAVES_N * WTN;
+
+    template <int i, int j, int v>
+    __device__ __forceinline__ float get() const {
+        return value(std::integral_constant<int, i>{}, std::integral_constant<int, j>{}, std::integral_constant<int, v>{});
+    }
+    // Rows of whole 16-byte units take straight-line code (a tile at an end of C a mask a
+    // store), that writes 128 bytes of each of eight rows at a time, whole cache lines
+    // where C's rows are aligned to them (64 or 32 bytes a row cost up to 40% more).  Of a
+    // 16-bit C a lane holds 8 bytes of each fragment, so neighbouring fragments trade
+    // halves between lane groups first (v_permlane16_swap: the odd rows of 16 lanes of
+    // one register against the even ones of the other).  Then two 64-byte neighbours P,
+    // Q of 16 rows trade their halves of 8 rows (a rotation by 8 lanes).
+    __device__ __forceinline__ static void trade_rows(const u32x4 &P, const u32x4 &Q, u32x4 &low, u32x4 &high) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            // row_ror:8, written to lanes 8-15 (banks 2, 3) or 0-7 (banks 0, 1) of each 16
+            low[c] = __builtin_amdgcn_update_dpp((int)P[c], (int)Q[c], 0x128, 0xf, 0xc, false);
+            high[c] = __builtin_amdgcn_update_dpp((int)Q[c], (int)P[c], 0x128, 0xf, 0x3, false);
+        }
+    }
+    // fragments j, j + 1 of row tile i in 16 bits: 16 bytes of lane group 0, 2 are columns
+    // 0-7, 8-15 of the even fragment, of 1, 3 those of the odd one
+    template <int i, int j>
+    __device__ __forceinline__ u32x4 pair16() const {
+        typedef typename ElemOf<C::DT>::type t2 __attribute__((ext_vector_type(2)));
+        typedef typename ElemOf<C::DT>::type T;
+        u32x4 v;
+        static_for<0, 2, 1>([&](auto hc) {
+            constexpr int h = decltype(hc)::value;
+            const t2 even = {(T)get<i, j, 2 * h>(), (T)get<i, j, 2 * h + 1>()};
+            const t2 odd = {(T)get<i, j + 1, 2 * h>(), (T)get<i, j + 1, 2 * h + 1>()};
+            const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, even),
+                                                            __builtin_bit_cast(uint32_t, odd), false, false);
+            v[h] = r[0];
+            v[2 + h] = r[1];
+        });
+        return v;
+    }
+    template <int i, int j>
+    __device__ __forceinline__ u32x4 quad32() const {
+        return __builtin_bit_cast(u32x4, f32x4{get<i, j, 0>(), get<i, j, 1>(), get<i, j, 2>(), get<i, j, 3>()});
+    }
+    // PAST: with the non-temporal hint (GroupedParams::past)
+    template <bool PAST>
+    __device__ __forceinline__ static void put(char *at, const u32x4 &v) {
+        if constexpr (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(at));
+        else *reinterpret_cast<u32x4 *>(at) = v;
+    }
+    // A store takes two fragments (fp32) or four (16 bits) of the wave's columns; a wave
+    // with two of 16 bits stores 64 bytes of each of 16 rows.
+    static constexpr bool short_rows(bool f32) { return !f32 && TN % 4 != 0; }
+    // row: this lane's first, `first` in the tile (ORDERED: of row 0 of C); half: 8 rows.
+    // MASKED: rows below `rows` and columns below `cols`, counted from this lane's first
+    // (whole units of 16 bytes: the caller's condition)
+    template <bool F32, bool PAST, bool MASKED>
+    __device__ __forceinline__ void store_whole(char *row, int64_t half, int first, int rows, int cols) const {
+        auto out = [&](char *at, const u32x4 &v, int r, int c) {
+            if (!MASKED || (r < rows && c < cols)) put<PAST>(at, v);
+        };
+        static_assert(TN % 2 == 0, "whole 64 bytes of a wave's columns");
+        char *const column = row;
+        static_for<0, C::TM, 1>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            char *second = row + half;
+            if constexpr (ORDERED) {
+                auto place = [&](int r) {
+                    if (MASKED && r >= rows) r = rows > 0 ? rows - 1 : -first;
+                    return column + row_in(order, first + r, total) * (half / 8);
+                };
+                row = place(16 * i);
+                if (!short_rows(F32)) second = place(16 * i + 8);
+            }
+            if constexpr (short_rows(F32)) {
+                static_for<0, TN, 2>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    if constexpr (C::DT != DT_F32) out(row + 32 * j, pair16<i, j>(), 16 * i, 16 * j);
+                });
+            } else if constexpr (F32) {
+                static_for<0, TN, 2>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    u32x4 low, high;
+                    trade_rows(quad32<i, j>(), quad32<i, j + 1>(), low, high);
+                    out(row + 64 * j, low, 16 * i, 16 * j);
+                    out(second + 64 * j, high, 16 * i + 8, 16 * j);
+                });
+            } else if constexpr (C::DT != DT_F32) {
+                static_for<0, TN, 4>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    u32x4 low, high;
+                    trade_rows(pair16<i, j>(), pair16<i, j + 2>(), low, high);
+                    out(row + 32 * j, low, 16 * i, 16 * j);
+                    out(second + 32 * j, high, 16 * i + 8, 16 * j);
+                });
+            }
+            if constexpr (!ORDERED) row += 2 * half;
+        });
+    }
+    __device__ __forceinline__ void store(char *Cp, int64_t at, int64_t ldc, int m_left, int n_left, bool c_f32,
+                                          bool past) const {
+        const int g = lane / 16, m = (wave / C::WAVES_N) * C::WTM + lane % 16, n = (wave % C::WAVES_N) * WTN;
+        const bool f32 = C::DT == DT_F32 || c_f32;
+        const int size = f32 ? 4 : 2;
+        char *first = Cp + at * size;
+        const bool wide = ldc * size % 16 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
+        const int unit = 16 / size;
+        if (wide && (n_left >= BN || n_left % unit == 0)) {
+            const bool is_short = short_rows(f32);
+            const int rm = (wave / C::WAVES_N) * C::WTM + (is_short ? lane % 16 : lane % 8);
+            const int rn = n + (f32 ? 4 * g : 8 * (g / 2) + 16 * (g % 2)) + (is_short ? 0 : 64 / size * (lane % 16 / 8));
+            char *row = first + ((ORDERED ? 0 : (int64_t)rm * ldc) + rn) * size;
+            const int64_t half = 8 * ldc * size;
+            if (m_left >= C::BM && n_left >= BN) {
+                if (f32 && past) store_whole<true, true, false>(row, half, rm, 0, 0);
+                else if (f32) store_whole<true, false, false>(row, half, rm, 0, 0);
+                else if (past) store_whole<false, true, false>(row, half, rm, 0, 0);
+                else store_whole<false, false, false>(row, half, rm, 0, 0);
+            } else {
+                if (f32) store_whole<true, false, true>(row, half, rm, m_left - rm, n_left - rn);
+                else store_whole<false, false, true>(row, half, rm, m_left - rm, n_left - rn);
+            }
+            return;
+        }
+        const bool wide4 = ldc % 4 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
+        static_for<0, C::TM, 1>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            if (m + 16 * i < m_left) {
+                int64_t place = m + 16 * i;
+                if constexpr (ORDERED) place = row_in(order, m + 16 * i, total);
+                const int64_t row = at + place * ldc + n + 4 * g;
+                static_for<0, TN, 1>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    const f32x4 v = {get<i, j, 0>(), get<i, j, 1>(), get<i, j, 2>(), get<i, j, 3>()};
+                    const int left = n_left - n - 4 * g - 16 * j;
+                    if (left > 0) store4<C::DT>(Cp, row + 16 * j, left, c_f32, wide4, v);
+                });
+            }
+        });
+    }
+};
+
+template <class C, bool KS> using OperandA = RingOperand<typename std::conditional<KS, typename SwapCfg<C>::type, C>::type, KS, C::TM>;
+template <class C, bool KS> using OperandB = RingOperand<typename std::conditional<KS, C, typename SwapCfg<C>::type>::type, KS, C::TN>;
+
+template <class C, bool A_KS, bool B_KS, int STAGES, class OA_ = OperandA<C, A_KS>, class OB_ = OperandB<C, B_KS>>
 struct GroupedTile {
-    using CT = typename SwapCfg<C>::type;
-    using OA = RingOperand<typename std::conditional<A_KS, CT, C>::type, A_KS, C::TM>;
-    using OB = RingOperand<typename std::conditional<B_KS, C, CT>::type, B_KS, C::TN>;
+    using OA = OA_;
+    using OB = OB_;
     static constexpr int COPIES = OA::PER + OB::PER;
     static constexpr int LDS = STAGES * (OA::REGION + OB::REGION);
     static constexpr int READS = C::TM * OA::PIECES + C::TN * OB::PIECES;
@@ -169,15 +329,18 @@ struct GroupedTile {
     int wave, lane;
     u32x4 tail[COPIES];
 
-    __device__ __forceinline__ void init(const char *A, int64_t lda, int m_left, const char *B, int64_t ldb, int n_left,
-                                         int K_, char *smem) {
+    // whole_chunks: no chunk of the last K tile that the copies bring passes a matrix's end
+    __device__ __forceinline__ void begin(int K_, bool whole_chunks) {
         lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         K = K_;
         nk = (K + C::BK - 1) / C::BK;
-        const bool whole = K % C::BK == 0 && (!A_KS || m_left >= C::BM || m_left % C::CHUNK == 0) &&
-                           (!B_KS || n_left >= C::BN || n_left % C::CHUNK == 0);
-        ndma = whole || nk == 0 ? nk : nk - 1;
+        ndma = (K % C::BK == 0 && whole_chunks) || nk == 0 ? nk : nk - 1;
+    }
+    __device__ __forceinline__ void init(const char *A, int64_t lda, int m_left, const char *B, int64_t ldb, int n_left,
+                                         int K_, char *smem) {
+        begin(K_, (!A_KS || m_left >= C::BM || m_left % C::CHUNK == 0) &&
+                      (!B_KS || n_left >= C::BN || n_left % C::CHUNK == 0));
         const uint32_t lds0 = lds_address(smem);
         b.init(B, ldb, n_left, (wave % C::WAVES_N) * C::WTN, lds0, lane, wave);
         a.init(A, lda, m_left, (wave / C::WAVES_N) * C::WTM, lds0 + STAGES * OB::REGION, lane, wave);
@@ -319,117 +482,12 @@ struct GroupedTile {
     }
 
     // C's tile: rows m < m_left, columns n < n_left, from its element `at`.
-    // Rows of whole 16-byte units take straight-line code (a tile at an end of C a mask a
-    // store), that writes 128 bytes of each of eight rows at a time, whole cache lines
-    // where C's rows are aligned to them (64 or 32 bytes a row cost up to 40% more).  Of a
-    // 16-bit C a lane holds 8 bytes of each fragment, so neighbouring fragments trade
-    // halves between lane groups first (v_permlane16_swap: the odd rows of 16 lanes of
-    // one register against the even ones of the other).  Then two 64-byte neighbours P,
-    // Q of 16 rows trade their halves of 8 rows (a rotation by 8 lanes).
-    __device__ __forceinline__ static void trade_rows(const u32x4 &P, const u32x4 &Q, u32x4 &low, u32x4 &high) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            // row_ror:8, written to lanes 8-15 (banks 2, 3) or 0-7 (banks 0, 1) of each 16
-            low[c] = __builtin_amdgcn_update_dpp((int)P[c], (int)Q[c], 0x128, 0xf, 0xc, false);
-            high[c] = __builtin_amdgcn_update_dpp((int)Q[c], (int)P[c], 0x128, 0xf, 0x3, false);
-        }
-    }
-    // fragments j, j + 1 of row tile i in 16 bits: 16 bytes of lane group 0, 2 are columns
-    // 0-7, 8-15 of the even fragment, of 1, 3 those of the odd one
-    template <int i, int j>
-    __device__ __forceinline__ u32x4 pair16() const {
-        typedef typename ElemOf<C::DT>::type t2 __attribute__((ext_vector_type(2)));
-        typedef typename ElemOf<C::DT>::type T;
-        u32x4 v;
-        static_for<0, 2, 1>([&](auto hc) {
-            constexpr int h = decltype(hc)::value;
-            const t2 even = {(T)acc.get(i, j, 2 * h), (T)acc.get(i, j, 2 * h + 1)};
-            const t2 odd = {(T)acc.get(i, j + 1, 2 * h), (T)acc.get(i, j + 1, 2 * h + 1)};
-            const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, even),
-                                                            __builtin_bit_cast(uint32_t, odd), false, false);
-            v[h] = r[0];
-            v[2 + h] = r[1];
-        });
-        return v;
-    }
-    template <int i, int j>
-    __device__ __forceinline__ u32x4 quad32() const {
-        return __builtin_bit_cast(u32x4, f32x4{acc.get(i, j, 0), acc.get(i, j, 1), acc.get(i, j, 2), acc.get(i, j, 3)});
-    }
-    // PAST: with the non-temporal hint (GroupedParams::past)
-    template <bool PAST>
-    __device__ __forceinline__ static void put(char *at, const u32x4 &v) {
-        if constexpr (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(at));
-        else *reinterpret_cast<u32x4 *>(at) = v;
-    }
-    // MASKED: rows below `rows` and columns below `cols`, counted from this lane's first
-    // (whole units of 16 bytes: the caller's condition)
-    template <bool F32, bool PAST, bool MASKED>
-    __device__ __forceinline__ void store_whole(char *row, int64_t half, int rows, int cols) const {
-        auto out = [&](char *at, const u32x4 &v, int r, int c) {
-            if (!MASKED || (r < rows && c < cols)) put<PAST>(at, v);
-        };
-        // a store takes two fragments (fp32) or four (16 bits) of the wave's columns
-        static_assert(C::TN % (C::DT == DT_F32 ? 2 : 4) == 0, "whole 128 bytes of a wave's columns");
-        static_for<0, C::TM, 1>([&](auto ic) {
-            constexpr int i = decltype(ic)::value;
-            if constexpr (F32) {
-                static_for<0, C::TN, 2>([&](auto jc) {
-                    constexpr int j = decltype(jc)::value;
-                    u32x4 low, high;
-                    trade_rows(quad32<i, j>(), quad32<i, j + 1>(), low, high);
-                    out(row + 64 * j, low, 16 * i, 16 * j);
-                    out(row + 64 * j + half, high, 16 * i + 8, 16 * j);
-                });
-            } else if constexpr (C::DT != DT_F32) {
-                static_for<0, C::TN, 4>([&](auto jc) {
-                    constexpr int j = decltype(jc)::value;
-                    u32x4 low, high;
-                    trade_rows(pair16<i, j>(), pair16<i, j + 2>(), low, high);
-                    out(row + 32 * j, low, 16 * i, 16 * j);
-                    out(row + 32 * j + half, high, 16 * i + 8, 16 * j);
-                });
-            }
-            row += 2 * half;
-        });
-    }
     __device__ __forceinline__ void store(char *Cp, int64_t at, int64_t ldc, int m_left, int n_left, bool c_f32,
                                           bool past) const {
-        const int g = lane / 16, m = (wave / C::WAVES_N) * C::WTM + lane % 16, n = (wave % C::WAVES_N) * C::WTN;
-        const bool f32 = C::DT == DT_F32 || c_f32;
-        const int size = f32 ? 4 : 2;
-        char *first = Cp + at * size;
-        const bool wide = ldc * size % 16 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
-        const int unit = 16 / size;
-        if (wide && (n_left >= C::BN || n_left % unit == 0)) {
-            const int rm = (wave / C::WAVES_N) * C::WTM + lane % 8;
-            const int rn = n + (f32 ? 4 * g : 8 * (g / 2) + 16 * (g % 2)) + 64 / size * (lane % 16 / 8);
-            char *row = first + ((int64_t)rm * ldc + rn) * size;
-            const int64_t half = 8 * ldc * size;
-            if (m_left >= C::BM && n_left >= C::BN) {
-                if (f32 && past) store_whole<true, true, false>(row, half, 0, 0);
-                else if (f32) store_whole<true, false, false>(row, half, 0, 0);
-                else if (past) store_whole<false, true, false>(row, half, 0, 0);
-                else store_whole<false, false, false>(row, half, 0, 0);
-            } else {
-                if (f32) store_whole<true, false, true>(row, half, m_left - rm, n_left - rn);
-                else store_whole<false, false, true>(row, half, m_left - rm, n_left - rn);
-            }
-            return;
-        }
-        const bool wide4 = ldc % 4 == 0 && reinterpret_cast<uintptr_t>(first) % 16 == 0;
-        static_for<0, C::TM, 1>([&](auto ic) {
-            constexpr int i = decltype(ic)::value;
-            if (m + 16 * i < m_left) {
-                const int64_t row = at + (int64_t)(m + 16 * i) * ldc + n + 4 * g;
-                static_for<0, C::TN, 1>([&](auto jc) {
-                    constexpr int j = decltype(jc)::value;
-                    const f32x4 v = {acc.get(i, j, 0), acc.get(i, j, 1), acc.get(i, j, 2), acc.get(i, j, 3)};
-                    const int left = n_left - n - 4 * g - 16 * j;
-                    if (left > 0) store4<C::DT>(Cp, row + 16 * j, left, c_f32, wide4, v);
-                });
-            }
-        });
+        const auto value = [&](auto i, auto j, auto v) {
+            return acc.get(decltype(i)::value, decltype(j)::value, decltype(v)::value);
+        };
+        TileStore<C, C::TN, decltype(value)>{value, lane, wave}.store(Cp, at, ldc, m_left, n_left, c_f32, past);
     }
 };
 
