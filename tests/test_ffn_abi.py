@@ -143,7 +143,7 @@ def test_workspace_sizes():
     n = tg.tile_gemm_gated_workspace_size(1, 1, 2816, 1024, "bf16")
     assert n % (2 * 2816 * 4) == 0                                                       # u and v of each split
     assert tg.tile_gemm_gated_workspace_size(1, 0, 2816, 1024, "bf16") == 0
-    assert tg.tile_gemm_adapters_workspace_size(4, 8192, 4096, 4096, 60, "f16") == 8192 * 64 * 2
+    assert tg.tile_gemm_adapters_workspace_size(4, 8192, 4096, 4096, 60, "f16") >= 8192 * 64 * 2 + 8192 * 60 * 4
     assert tg.tile_gemm_adapters_workspace_size(4, 8192, 4096, 4096, 0, "f16") == 0
     assert tg.tile_gemm_adapters_workspace_size(4, 16, 4096, 4096, 16, "f16") > 16 * 4096 * 4
     assert tg.tile_gemm_adapters_wgrad_workspace_size(2, 0, 64, 64, 8, "f16") == 0

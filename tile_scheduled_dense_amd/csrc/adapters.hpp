@@ -34,7 +34,7 @@ struct AdapterParams : GroupedParams {   // A: x, B: W, C: y; experts: adapters;
     const int32_t *order;
     char *T;                              // NULL: not stored
     char *low;                            // many rows: t of dtype by position, rows of ld_low
-    float *part, *part_t;                 // few rows: sums of x . W (by row), of x . A[g] (by position)
+    float *part, *part_t;                 // fp32 sums by split of K: of x . W by row, of x . A[g] by position
     int64_t ld_down, s_down, ld_up, s_up, ldt;
     int64_t ld_low;
     int rank, splits, t_splits;
@@ -80,7 +80,7 @@ __device__ __forceinline__ bool shrink_sum(const AdapterParams &p, int strip, in
 #pragma unroll
     for (int j = 0; j < S::FRAGS; ++j) acc[j] = f32x4{0, 0, 0, 0};
     int begin, end;
-    few_range(stages, p.t_splits, split, begin, end);
+    split_range(stages, p.t_splits, split, begin, end);
     few_sum<DT, TRANS>(of, row, p.K, p.K % S::PER == 0 && (TRANS || p.rank % S::PER == 0), begin + wave, waves, end, lane,
                        acc);
 #pragma unroll
@@ -89,32 +89,40 @@ __device__ __forceinline__ bool shrink_sum(const AdapterParams &p, int strip, in
     return true;
 }
 
-// ---- few rows -------------------------------------------------------------------------------
-// Workgroups below `base`: x . W (strips x splits x tiles of 16 rows); behind them x . A[g].
+// The sums of shrink_sum by split and position (few rows).
 template <int DT, bool TRANS>
-__global__ __launch_bounds__(512) void adapters_few_kernel(AdapterParams p, int base, int row_tiles, int strips_t) {
+__device__ __forceinline__ void shrink_few(const AdapterParams &p, int id, int strips, f32x4 *lds) {
+    using S = StreamShape<DT, TRANS>;
+    const int split = id % p.t_splits, strip = id / p.t_splits % strips, slot = id / p.t_splits / strips;
+    const int waves = blockDim.x >> 6, n0 = strip * S::COLS;
+    int g;
+    RowSpan span;
+    if (!shrink_sum<DT, TRANS>(p, strip, slot - (p.experts + 1), split, lds, g, span) || g == p.experts) return;
+    for (int it = threadIdx.x; it < S::FRAGS * 64; it += blockDim.x) {
+        int m, n;
+        const f32x4 v = few_item<DT, TRANS>(lds, waves, it, m, n);
+        const int left = p.rank - n0 - n;
+        if (m < span.hi - span.lo && left > 0)
+            store4<DT_F32>(reinterpret_cast<char *>(p.part_t), ((int64_t)split * p.rows + span.lo + m) * p.rank + n0 + n,
+                           left, true, p.rank % 4 == 0, v);
+    }
+}
+
+// ---- few rows -------------------------------------------------------------------------------
+// Workgroups below `low`: x . A[g] (they are the longer chains, so they start first); behind
+// them x . W, strips x splits x tiles of 16 rows.
+template <int DT, bool TRANS>
+__global__ __launch_bounds__(512) void adapters_few_kernel(AdapterParams p, int low, int row_tiles, int strips_t) {
     using S = StreamShape<DT, TRANS>;
     extern __shared__ f32x4 stream_lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
     int id = blockIdx.x;
-    if (id >= base) {
-        id -= base;
-        const int split = id % p.t_splits, strip = id / p.t_splits % strips_t, slot = id / p.t_splits / strips_t;
-        int g;
-        RowSpan span;
-        if (!shrink_sum<DT, TRANS>(p, strip, slot - (p.experts + 1), split, stream_lds, g, span) || g == p.experts) return;
-        const int n0 = strip * S::COLS;
-        for (int it = threadIdx.x; it < S::FRAGS * 64; it += blockDim.x) {
-            int m, n;
-            const f32x4 v = few_item<DT, TRANS>(stream_lds, waves, it, m, n);
-            const int left = p.rank - n0 - n;
-            if (m < span.hi - span.lo && left > 0)
-                store4<DT_F32>(reinterpret_cast<char *>(p.part_t),
-                               ((int64_t)split * p.rows + span.lo + m) * p.rank + n0 + n, left, true, p.rank % 4 == 0, v);
-        }
+    if (id < low) {
+        shrink_few<DT, TRANS>(p, id, strips_t, stream_lds);
         return;
     }
+    id -= low;
     const int z = id % p.splits, tile = id / p.splits % row_tiles, n0 = id / p.splits / row_tiles * S::COLS;
     const int r0 = 16 * tile, stages = (p.K + S::K - 1) / S::K;
     const OneStrip<DT, TRANS> of = {p.B + (TRANS ? n0 * p.ldb : (int64_t)n0) * S::E, p.ldb, p.N - n0};
@@ -123,7 +131,7 @@ __global__ __launch_bounds__(512) void adapters_few_kernel(AdapterParams p, int 
 #pragma unroll
     for (int j = 0; j < S::FRAGS; ++j) acc[j] = f32x4{0, 0, 0, 0};
     int begin, end;
-    few_range(stages, p.splits, z, begin, end);
+    split_range(stages, p.splits, z, begin, end);
     few_sum<DT, TRANS>(of, row, p.K, p.K % S::PER == 0 && (TRANS || p.N % S::PER == 0), begin + wave, waves, end, lane, acc);
 #pragma unroll
     for (int j = 0; j < S::FRAGS; ++j) stream_lds[(wave * S::FRAGS + j) * 64 + lane] = acc[j];
@@ -138,74 +146,126 @@ __global__ __launch_bounds__(512) void adapters_few_kernel(AdapterParams p, int 
     }
 }
 
-// y and t of a position from the sums (workgroups: position by position): a thread four neighbours of y.  t in LDS,
-// in fp32, 256 of the rank at a time.
+// The same where W is read in tiles of BM rows through LDS.
+template <class C, bool KS, int STAGES>
+__global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void adapters_split_kernel(AdapterParams p, int low, int strips_t) {
+    using S = StreamShape<C::DT, !KS>;
+    constexpr int TILE = GroupedTile<C, false, KS, STAGES>::LDS, SUMS = C::WAVES * S::FRAGS * 1024;
+    __shared__ __attribute__((aligned(1024))) char smem[TILE > SUMS ? TILE : SUMS];
+    int id = blockIdx.x;
+    if (id < low) {
+        shrink_few<C::DT, !KS>(p, id, strips_t, reinterpret_cast<f32x4 *>(smem));
+        return;
+    }
+    id -= low;
+    const int strips = (p.N + C::BN - 1) / C::BN;
+    const int z = id % p.splits, n0 = id / p.splits % strips * C::BN, m0 = id / p.splits / strips * C::BM;
+    int begin, end;
+    split_range((p.K + C::BK - 1) / C::BK, p.splits, z, begin, end);
+    const int k0 = begin * C::BK, K = (end * C::BK < p.K ? end * C::BK : p.K) - k0;
+    GroupedTile<C, false, KS, STAGES> tile;
+    tile.init(p.A + ((int64_t)m0 * p.lda + k0) * C::ELEM, p.lda, p.rows - m0,
+              p.B + (KS ? k0 * p.ldb + n0 : n0 * p.ldb + k0) * C::ELEM, p.ldb, p.N - n0, K > 0 ? K : 0, smem);
+    tile.run_ring();
+    tile.store(reinterpret_cast<char *>(p.part), ((int64_t)z * p.rows + m0) * p.N + n0, p.N, p.rows - m0, p.N - n0, true,
+               false);
+}
+
+// y and t of a position from the sums (workgroups: position by position): y's sums over the
+// splits, t's in fp32 through LDS, kJoinRank of the rank at a time.  A thread has COLS
+// neighbouring columns: two of B's rows as stored, one of its columns transposed (whose
+// rank is contiguous); the next STEP ranks' loads of B are in flight, the first before t
+// is there.  (As stored with four columns and eight ranks at a time: 64 rows of rank 32, 4096
+// columns, 14 us.)
 constexpr int kJoinRank = 256;
+template <bool TRANS> constexpr int join_cols() { return TRANS ? 1 : 2; }
 template <int DT, bool TRANS>
 __global__ __launch_bounds__(256) void adapters_join_kernel(AdapterParams p) {
     typedef typename ElemOf<DT>::type E;
-    __shared__ float t[kJoinRank];
-    const int parts = (p.N + 1023) / 1024, pos = blockIdx.x / parts, part = blockIdx.x % parts;
+    typedef E Two __attribute__((ext_vector_type(2)));
+    typedef Two __attribute__((aligned(sizeof(E)))) TwoAnywhere;
+    constexpr int COLS = join_cols<TRANS>(), STEP = TRANS ? Chunk<DT>::PER : 16, BYTES = (int)sizeof(E);
+    __shared__ float t[kJoinRank + STEP];
+    const int parts = (p.N + 256 * COLS - 1) / (256 * COLS), pos = blockIdx.x / parts, part = blockIdx.x % parts;
     const int g = group_of(p.offsets, p.experts, pos);
     const int64_t r = row_at(p, pos);
-    const int c = 4 * (part * 256 + (int)threadIdx.x), left = p.N - c;
-    f32x4 y = {0, 0, 0, 0};
-    if (left > 0)
-        for (int z = 0; z < p.splits; ++z)
-            y += load4<DT_F32>(reinterpret_cast<const char *>(p.part), ((int64_t)z * p.rows + r) * p.N + c, left, p.N % 4 == 0);
+    const int c = COLS * (part * 256 + (int)threadIdx.x), left = p.N - c;
     const bool has = g < p.experts;
-    const float scale = has ? (p.scales ? p.scales[g] : 1.0f) : 0.0f;
-    const E *up = reinterpret_cast<const E *>(p.up) + (has ? (int64_t)g * p.s_up : 0);
-    for (int k0 = 0; k0 < p.rank; k0 += kJoinRank) {
-        const int n = p.rank - k0 < kJoinRank ? p.rank - k0 : kJoinRank;
-        __syncthreads();
-        for (int k = threadIdx.x; k < n; k += 256) {
-            float s = 0;
-            if (has)
-                for (int z = 0; z < p.t_splits; ++z) s += p.part_t[((int64_t)z * p.rows + pos) * p.rank + k0 + k];
-            s *= scale;
-            if (!has) s = 0;
-            t[k] = s;
-            if (p.T && part == 0) reinterpret_cast<E *>(p.T)[r * p.ldt + k0 + k] = (E)s;
-        }
-        __syncthreads();
-        if (!has || left <= 0) continue;
-        for (int k = 0; k < n; ++k) {
+    const char *up = p.up + (has ? (int64_t)g * p.s_up : 0) * BYTES;
+    // B of ranks k .. k + STEP - 1
+    struct Piece {
+        Two rows[TRANS ? 1 : STEP];
+        Chunk<DT> column;
+    };
+    auto fetch = [&](int k, Piece &b) {
+        if constexpr (TRANS) {
+            b.column.load(up, (int64_t)c * p.ld_up + k, has && left > 0 ? p.rank - k : 0);
+        } else {
+            const E *at = reinterpret_cast<const E *>(up) + (int64_t)k * p.ld_up + c;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < left)
-                    y[e] = __builtin_fmaf(t[k], (float)(TRANS ? up[(int64_t)(c + e) * p.ld_up + k0 + k]
-                                                              : up[(int64_t)(k0 + k) * p.ld_up + c + e]), y[e]);
+            for (int i = 0; i < STEP; ++i) {
+                b.rows[i] = Two{};
+                if (has && k + i < p.rank) {
+                    if (left >= 2) b.rows[i] = *reinterpret_cast<const TwoAnywhere *>(at);
+                    else if (left == 1) b.rows[i][0] = at[0];
+                }
+                at += p.ld_up;
+            }
+        }
+    };
+    Piece b0, b1;
+    fetch(0, b0);
+    float y[COLS] = {};
+    if (left > 0) {
+        const float *sums = p.part + r * p.N + c;
+        const int64_t plane = (int64_t)p.rows * p.N;
+#pragma unroll 4
+        for (int z = 0; z < p.splits; ++z) {
+            y[0] += sums[z * plane];
+            if (COLS > 1 && left > 1) y[COLS - 1] += sums[z * plane + 1];
         }
     }
-    if (left > 0) store4<DT>(p.C, r * p.ldc + c, left, false, wide_rows<DT>(p.C, p.ldc), y);
+    const float scale = has ? (p.scales ? p.scales[g] : 1.0f) : 0.0f;
+    for (int base = 0; base < p.rank; base += kJoinRank) {
+        const int n = p.rank - base < kJoinRank ? p.rank - base : kJoinRank;
+        if (base) __syncthreads();
+        for (int k = threadIdx.x; k < kJoinRank + STEP; k += 256) {
+            float s = 0;
+            if (has && k < n) {
+                const float *sums = p.part_t + (int64_t)pos * p.rank + base + k;
+#pragma unroll 8
+                for (int z = 0; z < p.t_splits; ++z) s += sums[(int64_t)z * p.rows * p.rank];
+                s *= scale;
+            }
+            t[k] = s;
+            if (p.T && part == 0 && k < n) reinterpret_cast<E *>(p.T)[r * p.ldt + base + k] = (E)s;
+        }
+        __syncthreads();
+        if (!has) continue;
+        for (int k = 0; k < n; k += STEP) {
+            if (base + k + STEP < p.rank) fetch(base + k + STEP, b1);
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+                if constexpr (TRANS) {
+                    y[0] = __builtin_fmaf(t[k + i], (float)b0.column.x[i], y[0]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < COLS; ++e) y[e] = __builtin_fmaf(t[k + i], (float)b0.rows[i][e], y[e]);
+                }
+            }
+            b0 = b1;
+        }
+    }
+    E *to = reinterpret_cast<E *>(p.C) + r * p.ldc + c;
+    if (left >= COLS) {
+        if constexpr (TRANS) to[0] = (E)y[0];
+        else *reinterpret_cast<TwoAnywhere *>(to) = Two{(E)y[0], (E)y[1]};
+    } else if (left > 0) {
+        to[0] = (E)y[0];
+    }
 }
 
 // ---- many rows ------------------------------------------------------------------------------
-// t by position, of dtype, into low (its rows' rest up to ld_low zeros), and into T.
-template <int DT, bool TRANS>
-__global__ __launch_bounds__(512) void shrink_kernel(AdapterParams p) {
-    using S = StreamShape<DT, TRANS>;
-    extern __shared__ f32x4 stream_lds[];
-    const int waves = blockDim.x >> 6, n0 = blockIdx.x * S::COLS;
-    int g;
-    RowSpan span;
-    if (!shrink_sum<DT, TRANS>(p, blockIdx.x, slot_of(p.experts), 0, stream_lds, g, span)) return;
-    const bool has = g < p.experts;
-    const float scale = has && p.scales ? p.scales[g] : 1.0f;
-    for (int it = threadIdx.x; it < S::FRAGS * 64; it += blockDim.x) {
-        int m, n;
-        f32x4 v = few_item<DT, TRANS>(stream_lds, waves, it, m, n);
-        const int left = p.rank - n0 - n;
-        if (m >= span.hi - span.lo) continue;
-        v *= scale;
-        if (!has) v = f32x4{0, 0, 0, 0};
-        const int pos = span.lo + m, low_left = (int)p.ld_low - n0 - n;
-        if (low_left > 0) store4<DT>(p.low, (int64_t)pos * p.ld_low + n0 + n, low_left, false, true, v);
-        if (p.T && left > 0) store4<DT>(p.T, (int64_t)row_at(p, pos) * p.ldt + n0 + n, left, false, wide_rows<DT>(p.T, p.ldt), v);
-    }
-}
-
 // A's operand whose rows lie at order[m]: offsets from the matrix's first element.
 template <class V, int T>
 struct OrderedOperand : RingOperand<V, false, T> {
@@ -233,59 +293,104 @@ struct OrderedOperand : RingOperand<V, false, T> {
     }
 };
 
+// x's rows at positions m0 .. , in order or through the table
+template <class C, bool ORDERED>
+using OperandX = typename std::conditional<ORDERED, OrderedOperand<C, C::TM>, OperandA<C, false>>::type;
+
 template <class C, bool KS, bool ORDERED, int STAGES>
-struct AdapterTile
-    : GroupedTile<C, false, KS, STAGES,
-                  typename std::conditional<ORDERED, OrderedOperand<C, C::TM>, OperandA<C, false>>::type, OperandB<C, KS>> {
-    using OA = typename std::conditional<ORDERED, OrderedOperand<C, C::TM>, OperandA<C, false>>::type;
+struct AdapterTile : GroupedTile<C, false, KS, STAGES, OperandX<C, ORDERED>, OperandB<C, KS>> {
+    using OA = OperandX<C, ORDERED>;
     using OB = OperandB<C, KS>;
 
-    __device__ __forceinline__ void init(const AdapterParams &p, int m0, int n0, char *smem) {
-        const int m_left = p.rows - m0, n_left = p.N - n0;
-        this->begin(p.K, !KS || n_left >= C::BN || n_left % C::CHUNK == 0);
+    // positions m0 .. of which m_left exist, from k0 on K of them; B: the second operand's
+    // first element
+    __device__ __forceinline__ void init(const AdapterParams &p, int m0, int m_left, int k0, int K, const char *B, int64_t ldb,
+                                         int n_left, char *smem) {
+        this->begin(K, !KS || n_left >= C::BN || n_left % C::CHUNK == 0);
         const uint32_t lds0 = lds_address(smem);
-        this->b.init(p.B + (KS ? (int64_t)n0 : n0 * p.ldb) * C::ELEM, p.ldb, n_left, (this->wave % C::WAVES_N) * C::WTN, lds0,
-                     this->lane, this->wave);
+        this->b.init(B, ldb, n_left, (this->wave % C::WAVES_N) * C::WTN, lds0, this->lane, this->wave);
         const int w = (this->wave / C::WAVES_N) * C::WTM;
+        const char *A = p.A + (int64_t)k0 * C::ELEM;
         if constexpr (ORDERED)
-            this->a.init(p.A, p.lda, m_left, w, lds0 + STAGES * OB::REGION, this->lane, this->wave, p.order + m0, p.rows);
+            this->a.init(A, p.lda, m_left, w, lds0 + STAGES * OB::REGION, this->lane, this->wave, p.order + m0, p.rows);
         else
-            this->a.init(p.A + (int64_t)m0 * p.lda * C::ELEM, p.lda, m_left, w, lds0 + STAGES * OB::REGION, this->lane,
+            this->a.init(A + (int64_t)m0 * p.lda * C::ELEM, p.lda, m_left, w, lds0 + STAGES * OB::REGION, this->lane,
                          this->wave);
         this->acc.zero();
     }
 
+    // f(g, lo, hi) for every adapter with positions in the tile: lo .. hi, from its first
+    template <class F>
+    __device__ __forceinline__ static void each_adapter(const AdapterParams &p, int m0, const F &f) {
+        const int lane = threadIdx.x & 63, m_end = m0 + C::BM < p.rows ? m0 + C::BM : p.rows;
+        const int last = group_of(p.offsets, p.experts, m_end - 1);
+        for (int base = group_of(p.offsets, p.experts, m0); base <= last; base += 64) {
+            const int g = base + lane;
+            RowSpan s = {0, 0};
+            if (g <= last && g < p.experts) s = rows_of(p.offsets, g, p.experts, p.rows);
+            const int lo = s.lo > m0 ? s.lo - m0 : 0, hi = (s.hi < m_end ? s.hi : m_end) - m0;
+            for (uint64_t m = __ballot(lo < hi); m; m &= m - 1) {
+                const int l = __builtin_ctzll(m);
+                f(base + l, __builtin_amdgcn_readlane(lo, l), __builtin_amdgcn_readlane(hi, l));
+            }
+        }
+    }
+
+    // The K tile of B[g] at rank k0 (columns from n0), zeros past its ends; whether any of
+    // the workgroup's values is not finite.
+    __device__ __forceinline__ void load_up(const AdapterParams &p, int g, int n0, int k0, u32x4 (&tb)[OB::PER]) const {
+        const char *up = p.up + ((int64_t)g * p.s_up + (KS ? k0 * p.ld_up + n0 : n0 * p.ld_up + k0)) * C::ELEM;
+        const rsrc_t rb = make_rsrc(up);
+#pragma unroll
+        for (int d = 0; d < OB::PER; ++d) {
+            const int k_left = p.rank - k0 - this->b.k[d], x_left = this->b.left - this->b.x[d];
+            const int run = KS ? x_left : k_left, other = KS ? k_left : x_left;
+            const int n = other <= 0 || run <= 0 ? 0 : (run < C::CHUNK ? run : C::CHUNK);
+            const int at = KS ? this->b.k[d] * (int)p.ld_up + this->b.x[d] : this->b.x[d] * (int)p.ld_up + this->b.k[d];
+            tb[d] = bload16_n<C::ELEM>(rb, n > 0 ? at * C::ELEM : 0, 0, n);
+        }
+    }
+    __device__ __forceinline__ static bool not_finite(const u32x4 (&t)[OB::PER]) {
+        constexpr uint32_t E = C::DT == DT_F32 ? 0x7f800000u : (C::DT == DT_BF16 ? 0x7f80u : 0x7c00u);
+        bool bad = false;
+#pragma unroll
+        for (int d = 0; d < OB::PER; ++d)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                bad |= (t[d][w] & E) == E;
+                if (C::DT != DT_F32) bad |= (t[d][w] >> 16 & E) == E;
+            }
+        return __syncthreads_or(bad);
+    }
+
     // The contraction goes on: t . B[g] for every adapter with positions in the tile, in
     // K tiles of the rank through registers, one at a time (an adapter of 32 and less is
-    // one), other adapters' rows and what lies past the rank as zeros.
-    __device__ __forceinline__ void adapters(const AdapterParams &p, int m0, int n0) {
-        if (this->nk == 0) return;                 // t is zero too
-        const int m_end = m0 + C::BM < p.rows ? m0 + C::BM : p.rows;
-        const int last = __builtin_amdgcn_readfirstlane(group_of(p.offsets, p.experts, m_end - 1));
-        for (int g = __builtin_amdgcn_readfirstlane(group_of(p.offsets, p.experts, m0)); g <= last && g < p.experts; ++g) {
-            const RowSpan s = rows_of(p.offsets, g, p.experts, p.rows);
-            const int lo = __builtin_amdgcn_readfirstlane(s.lo) - m0, hi = __builtin_amdgcn_readfirstlane(s.hi) - m0;
-            if (hi <= 0 || lo >= C::BM || hi <= lo) continue;
-            const rsrc_t rt = make_rsrc(p.low + (int64_t)m0 * p.ld_low * C::ELEM);
-            const char *up = p.up + ((int64_t)g * p.s_up + (KS ? (int64_t)n0 : n0 * p.ld_up)) * C::ELEM;
+    // one), other adapters' rows and what lies past the rank as zeros.  Those zeros would make
+    // NaN of an infinity or NaN in B[g], in other adapters' rows: such a K tile is left
+    // out, and true is returned, unless all of the tile's positions are g's.
+    __device__ __forceinline__ bool adapters(const AdapterParams &p, int m0, int n0) {
+        if (this->nk == 0) return false;           // t is zero too
+        const int m_here = p.rows - m0 < C::BM ? p.rows - m0 : C::BM;
+        const rsrc_t rt = make_rsrc(p.low + (int64_t)m0 * p.ld_low * C::ELEM);
+        bool left_out = false;
+        each_adapter(p, m0, [&](int g, int lo, int hi) {
             for (int k0 = 0; k0 < p.rank; k0 += C::BK) {
                 u32x4 ta[OA::PER], tb[OB::PER];
 #pragma unroll
                 for (int d = 0; d < OA::PER; ++d) {
                     const int x = this->a.x[d], k = k0 + this->a.k[d];
-                    const bool in = x >= lo && x < hi && x < m_end - m0 && k < p.ld_low;
+                    const bool in = x >= lo && x < hi && k < p.ld_low;
                     ta[d] = bload16(rt, in ? (x * (int)p.ld_low + k) * C::ELEM : kOutOfRange, 0);
                 }
-                const rsrc_t rb = make_rsrc(up + (int64_t)k0 * (KS ? p.ld_up : 1) * C::ELEM);
-#pragma unroll
-                for (int d = 0; d < OB::PER; ++d) {
-                    const int k_left = p.rank - k0 - this->b.k[d], x_left = this->b.left - this->b.x[d];
-                    const int run = KS ? x_left : k_left, other = KS ? k_left : x_left;
-                    const int n = other <= 0 || run <= 0 ? 0 : (run < C::CHUNK ? run : C::CHUNK);
-                    const int at = KS ? this->b.k[d] * (int)p.ld_up + this->b.x[d] : this->b.x[d] * (int)p.ld_up + this->b.k[d];
-                    tb[d] = bload16_n<C::ELEM>(rb, n > 0 ? at * C::ELEM : 0, 0, n);
+                load_up(p, g, n0, k0, tb);
+                if (hi - lo < m_here) {
+                    if (not_finite(tb)) {
+                        left_out = true;
+                        continue;
+                    }
+                } else {
+                    block_barrier();               // the copy's last readers are done
                 }
-                block_barrier();                   // the copy's last readers are done
                 this->a.tail_store(0, ta);
                 this->b.tail_store(0, tb);
                 wait_lds();
@@ -297,8 +402,36 @@ struct AdapterTile
                     [&](auto q) { this->template mma<false, decltype(q)::value>(fa, fb); });
                 wait_lds();
             }
-        }
+        });
         this->acc.settle();
+        return left_out;
+    }
+    // What adapters() left out, element by element, onto the stored result: value(position
+    // in the tile, column, sum).
+    template <class F>
+    __device__ __forceinline__ void left_out(const AdapterParams &p, int m0, int n0, const F &add) const {
+        typedef typename ElemOf<C::DT>::type T;
+        const int n_here = p.N - n0 < C::BN ? p.N - n0 : C::BN, m_here = p.rows - m0 < C::BM ? p.rows - m0 : C::BM;
+        __threadfence_block();
+        __syncthreads();
+        each_adapter(p, m0, [&](int g, int lo, int hi) {
+            if (hi - lo == m_here) return;
+            const T *up = reinterpret_cast<const T *>(p.up) + (int64_t)g * p.s_up;
+            const T *low = reinterpret_cast<const T *>(p.low) + (int64_t)m0 * p.ld_low;
+            for (int k0 = 0; k0 < p.rank; k0 += C::BK) {
+                u32x4 tb[OB::PER];
+                load_up(p, g, n0, k0, tb);
+                if (!not_finite(tb)) continue;
+                const int k_end = k0 + C::BK < p.rank ? k0 + C::BK : p.rank;
+                for (int i = threadIdx.x; i < (hi - lo) * n_here; i += C::THREADS) {
+                    const int m = lo + i / n_here, n = i % n_here;
+                    float sum = 0;
+                    for (int k = k0; k < k_end; ++k)
+                        sum += (float)low[m * p.ld_low + k] * (float)(KS ? up[k * p.ld_up + n0 + n] : up[(n0 + n) * p.ld_up + k]);
+                    add(m, n, sum);
+                }
+            }
+        });
     }
     __device__ __forceinline__ void store_rows(const AdapterParams &p, int m0, int n0) const {
         const auto value = [&](auto i, auto j, auto v) {
@@ -313,14 +446,63 @@ struct AdapterTile
     }
 };
 
+// x . A[g] of up to 64 positions of one adapter, 64 of the rank and a split of K, times the
+// adapter's scale, into part_t.  grid: (rank x splits) x row tiles.
+template <class C, bool KS, bool ORDERED, int STAGES>
+__global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void shrink_tile_kernel(AdapterParams p) {
+    __shared__ __attribute__((aligned(1024))) char smem[AdapterTile<C, KS, ORDERED, STAGES>::LDS];
+    const int z = blockIdx.x % p.t_splits, n0 = (int)(blockIdx.x / p.t_splits) * C::BN;
+    int g;
+    RowSpan span;
+    if (!row_slot<C::BM>(p.offsets, p.experts, p.rows, slot_of(p.experts), g, span)) return;
+    const bool has = g < p.experts;
+    int begin = 0, end = 0;
+    if (has) split_range((p.K + C::BK - 1) / C::BK, p.t_splits, z, begin, end);
+    const int k0 = begin * C::BK, K = (end * C::BK < p.K ? end * C::BK : p.K) - k0, rows = span.hi - span.lo;
+    const char *B = p.down + ((has ? (int64_t)g * p.s_down : 0) + (KS ? k0 * p.ld_down + n0 : n0 * p.ld_down + k0)) * C::ELEM;
+    AdapterTile<C, KS, ORDERED, STAGES> tile;
+    tile.init(p, span.lo, rows, k0, K > 0 ? K : 0, B, p.ld_down, p.rank - n0, smem);
+    tile.run_ring();
+    const float scale = has && p.scales ? p.scales[g] : 1.0f;
+    const auto value = [&](auto i, auto j, auto v) {
+        return tile.acc.get(decltype(i)::value, decltype(j)::value, decltype(v)::value) * scale;
+    };
+    TileStore<C, C::TN, decltype(value)>{value, tile.lane, tile.wave}.store(
+        reinterpret_cast<char *>(p.part_t), ((int64_t)z * p.rows + span.lo) * p.rank + n0, p.rank, rows, p.rank - n0, true,
+        false);
+}
+
+// t of dtype from the splits' sums, into low (its rows' rest up to ld_low zeros) and T: a
+// thread four neighbours.  t is rounded once: it is the next product's operand.
+template <int DT>
+__global__ __launch_bounds__(256) void shrink_join_kernel(AdapterParams p) {
+    const int quads = (int)p.ld_low / 4;
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, plane = (int64_t)p.rows * p.rank;
+    if (at >= (int64_t)p.rows * quads) return;
+    const int pos = (int)(at / quads), k = (int)(at % quads) * 4, left = p.rank - k;
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int z = 0; z < p.t_splits; ++z)
+        v += load4<DT_F32>(reinterpret_cast<const char *>(p.part_t), z * plane + (int64_t)pos * p.rank + k, left,
+                           p.rank % 4 == 0);
+    store4<DT>(p.low, (int64_t)pos * p.ld_low + k, 4, false, true, v);
+    if (p.T && left > 0) store4<DT>(p.T, (int64_t)row_at(p, pos) * p.ldt + k, left, false, wide_rows<DT>(p.T, p.ldt), v);
+}
+
 template <class C, bool KS, bool ORDERED, bool PIPE, int STAGES>
 __device__ __forceinline__ void run_adapters(const AdapterParams &p, char *smem, int m0, int n0) {
+    typedef typename ElemOf<C::DT>::type T;
     AdapterTile<C, KS, ORDERED, STAGES> tile;
-    tile.init(p, m0, n0, smem);
+    tile.init(p, m0, p.rows - m0, 0, p.K, p.B + (KS ? (int64_t)n0 : n0 * p.ldb) * C::ELEM, p.ldb, p.N - n0, smem);
     if constexpr (PIPE) tile.run_pipe();
     else tile.run_ring();
-    tile.adapters(p, m0, n0);
+    const bool more = tile.adapters(p, m0, n0);
     tile.store_rows(p, m0, n0);
+    if (more)
+        tile.left_out(p, m0, n0, [&](int m, int n, float sum) {
+            T *y = reinterpret_cast<T *>(p.C) + (int64_t)(ORDERED ? row_in(p.order, m0 + m, p.rows) : m0 + m) * p.ldc + n0 + n;
+            *y = (T)((float)*y + sum);
+        });
 }
 
 // Tiles over positions, whatever their adapters; P: the pieces' configuration (C: none).
@@ -337,12 +519,48 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void adapters_tile_kernel
     else run_adapters<C, KS, ORDERED, PIPE, STAGES>(p, smem, t.m0, t.n0);
 }
 
+// Too few tiles for all CUs: K split over workgroups, fp32 sums by position into part; the
+// first split has the adapters too.
+template <class C, bool KS, bool ORDERED, bool PIPE, int STAGES>
+__global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void adapters_tile_split_kernel(AdapterParams p) {
+    __shared__ __attribute__((aligned(1024))) char smem[AdapterTile<C, KS, ORDERED, STAGES>::LDS];
+    const int tiles_n = (p.N + C::BN - 1) / C::BN, z = blockIdx.x % p.splits;
+    const int m0 = (int)(blockIdx.x / p.splits / tiles_n) * C::BM, n0 = (int)(blockIdx.x / p.splits % tiles_n) * C::BN;
+    if (m0 >= p.rows) return;
+    int begin, end;
+    split_range((p.K + C::BK - 1) / C::BK, p.splits, z, begin, end);
+    const int k0 = begin * C::BK, K = (end * C::BK < p.K ? end * C::BK : p.K) - k0;
+    AdapterTile<C, KS, ORDERED, STAGES> tile;
+    tile.init(p, m0, p.rows - m0, k0, K > 0 ? K : 0, p.B + (KS ? k0 * p.ldb + n0 : n0 * p.ldb + k0) * C::ELEM, p.ldb,
+              p.N - n0, smem);
+    if constexpr (PIPE) tile.run_pipe();
+    else tile.run_ring();
+    const bool more = z == 0 && tile.adapters(p, m0, n0);
+    float *part = p.part + ((int64_t)z * p.rows + m0) * p.N + n0;
+    tile.store(reinterpret_cast<char *>(part), 0, p.N, p.rows - m0, p.N - n0, true, false);
+    if (more) tile.left_out(p, m0, n0, [&](int m, int n, float sum) { part[(int64_t)m * p.N + n] += sum; });
+}
+
+// y from the splits' sums by position: a thread four neighbours of a row
+template <int DT>
+__global__ __launch_bounds__(256) void adapters_sum_kernel(AdapterParams p) {
+    const int64_t quads = (p.N + 3) / 4, at = (int64_t)blockIdx.x * 256 + threadIdx.x, plane = (int64_t)p.rows * p.N;
+    if (at >= quads * p.rows) return;
+    const int pos = (int)(at / quads), c = (int)(at % quads) * 4, left = p.N - c;
+    f32x4 y = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int z = 0; z < p.splits; ++z)
+        y += load4<DT_F32>(reinterpret_cast<const char *>(p.part), z * plane + (int64_t)pos * p.N + c, left, p.N % 4 == 0);
+    store4<DT>(p.C, (int64_t)row_at(p, pos) * p.ldc + c, left, false, wide_rows<DT>(p.C, p.ldc), y);
+}
+
 // ---- the adapters' gradients ----------------------------------------------------------------
 // C[g] = L[rows of g]^T . S[rows of g], L wide (M columns), S narrow (rank).  A workgroup
-// takes kChunk positions of one adapter and, a wave each, strips of L's columns: stages
-// of L as StreamB loads a matrix (32 or 16... rows of k by 128 or 64 columns), transposed
-// in registers; S's rows of the chunk lie transposed in LDS.  fp32 sums, rank x M of each
-// chunk, go to the workspace.
+// takes kChunk positions of one adapter and a strip of L's columns a wave: stages of L as
+// StreamB loads a matrix (32 rows by 128 columns, fp32 64), transposed in registers, the
+// next one's loads in flight during the current one's products; S's rows of the chunk lie
+// transposed in LDS, 16 JT of the rank.  fp32 sums, rank x M of each chunk, go to the
+// workspace.  Bound by the bytes of L.
 constexpr int kChunk = 256;
 constexpr int kWgradRank = 64;        // of the rank at a time
 
@@ -359,13 +577,13 @@ struct AdapterGradParams {
     int strips[2], slots, rank_tiles;
 };
 
-template <int DT>
+template <int DT, int JT>
 __global__ __launch_bounds__(256) void adapters_wgrad_kernel(AdapterGradParams p) {
     using Sh = StreamShape<DT, false>;
     typedef typename ElemOf<DT>::type T;
-    constexpr int E = Sh::E, PER = Sh::PER, PITCH = kChunk + 16 / E;      // rows of S^T off the same banks
-    constexpr int JT = kWgradRank / 16;
-    __shared__ __attribute__((aligned(16))) T st[kWgradRank * PITCH];
+    typedef Chunk<DT> X;
+    constexpr int E = Sh::E, PER = Sh::PER, PITCH = kChunk + PER, RANKS = 16 * JT;   // rows of S^T off the same banks
+    __shared__ __attribute__((aligned(16))) T st[RANKS * PITCH];
     __shared__ int32_t row_of[kChunk];
     // workgroups: (job, strips of 4 x COLS columns, rank tile, slot)
     int id = blockIdx.x;
@@ -377,39 +595,49 @@ __global__ __launch_bounds__(256) void adapters_wgrad_kernel(AdapterGradParams p
     RowSpan span;
     if (!row_slot<kChunk>(p.offsets, p.adapters, p.rows, block - (p.adapters + 1), g, span) || g == p.adapters) return;
     const int rows = span.hi - span.lo, j0 = rank_tile * kWgradRank;
-    const int ranks = p.rank - j0 < kWgradRank ? p.rank - j0 : kWgradRank;
-    for (int k = threadIdx.x; k < kChunk; k += 256)
-        row_of[k] = k < rows ? (p.order ? row_in(p.order, span.lo + k, p.rows) : span.lo + k) : 0;
+    const int ranks = p.rank - j0 < RANKS ? p.rank - j0 : RANKS;
+    for (int k = threadIdx.x; k < kChunk; k += 256) {
+        const int pos = span.lo + (k < rows ? k : 0);       // past the chunk its first again, times a zero of S
+        row_of[k] = p.order ? row_in(p.order, pos, p.rows) : pos;
+    }
     __syncthreads();
-    const T *S = reinterpret_cast<const T *>(p.S[job]);
-    for (int it = threadIdx.x; it < kChunk * kWgradRank; it += 256) {
-        const int j = it % kWgradRank, k = it / kWgradRank;
-        st[j * PITCH + k] = j < ranks && k < rows ? S[row_of[k] * p.lds[job] + j0 + j] : (T)0.0f;
+    for (int it = threadIdx.x; it < kChunk * (RANKS / PER); it += 256) {
+        const int k = it % kChunk, j = it / kChunk * PER;
+        X x;
+        x.load(p.S[job], (int64_t)row_of[k] * p.lds[job] + j0 + j, k < rows ? ranks - j : 0);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) st[(j + e) * PITCH + k] = x.x[e];
     }
     __syncthreads();
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, grp = lane / 16, c = lane % 16;
-    const int m0 = (strip * 4 + wave) * Sh::COLS, left = p.M[job] - m0 - PER * c;
+    const int m0 = (strip * 4 + wave) * Sh::COLS;
     if (m0 >= p.M[job]) return;
     f32x4 acc[JT][Sh::FRAGS];
 #pragma unroll
     for (int j = 0; j < JT; ++j)
 #pragma unroll
         for (int f = 0; f < Sh::FRAGS; ++f) acc[j][f] = f32x4{0, 0, 0, 0};
+    const int left = p.M[job] - m0 - PER * c;
     const char *L = p.L[job] + (int64_t)(m0 + PER * c) * E;
     const int64_t ldl = p.ldl[job] * E;
-    for (int k0 = 0; k0 < rows; k0 += Sh::K) {
-        u32x4 q[8];
+    // Rows past the chunk meet zeros of S, so they may hold anything finite: its first row
+    // does.  An infinity or NaN there would not stay in its own sums, so a last stage that
+    // is cut loads zeros instead.
+    auto fetch = [&](int k0, u32x4 (&q)[8], auto whole) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int k = k0 + (DT == DT_F32 ? 16 * (i / 4) + 4 * grp + i % 4 : 8 * grp + i);
-            q[i] = load_part<E, PART_ELEMENTS>(L + row_of[k < rows ? k : 0] * ldl, k < rows ? left : 0);
+            const char *at = L + row_of[k] * ldl;
+            if constexpr (decltype(whole)::value) q[i] = *reinterpret_cast<const u32x4_unaligned *>(at);
+            else q[i] = load_part<E, PART_ELEMENTS>(at, k < rows ? left : 0);
         }
+    };
+    auto multiply = [&](int k0, const u32x4 (&q)[8]) {
         if constexpr (DT == DT_F32) {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int j = 0; j < JT; ++j) {
-                    if (16 * j >= ranks) continue;
                     const f32x4 x = *reinterpret_cast<const f32x4 *>(&st[(16 * j + c) * PITCH + k0 + 16 * s + 4 * grp]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -425,12 +653,32 @@ __global__ __launch_bounds__(256) void adapters_wgrad_kernel(AdapterGradParams p
             transpose_square<2>(q, f);
 #pragma unroll
             for (int j = 0; j < JT; ++j) {
-                if (16 * j >= ranks) continue;
                 const u32x4 x = *reinterpret_cast<const u32x4 *>(&st[(16 * j + c) * PITCH + k0 + 8 * grp]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) mfma_chunk<DT>(f[i], x, acc[j][i]);
             }
         }
+    };
+    const int whole = p.M[job] - m0 >= Sh::COLS ? rows / Sh::K * Sh::K : 0;
+    int k0 = 0;
+    if (whole > 0) {
+        u32x4 q0[8], q1[8];
+        fetch(0, q0, std::true_type{});
+        for (;;) {
+            const bool more = k0 + Sh::K < whole;
+            if (more) fetch(k0 + Sh::K, q1, std::true_type{});
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(k0, q0);
+            k0 += Sh::K;
+            if (!more) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q0[i] = q1[i];
+        }
+    }
+    for (; k0 < rows; k0 += Sh::K) {
+        u32x4 q[8];
+        fetch(k0, q, std::false_type{});
+        multiply(k0, q);
     }
     // a lane holds, of rank j, the columns PER * (4 grp + v) + fragment: PER x 4 neighbours
     float *part = p.part[job] + ((int64_t)block * p.rank + j0) * p.M[job];
@@ -450,23 +698,21 @@ __global__ __launch_bounds__(256) void adapters_wgrad_kernel(AdapterGradParams p
     }
 }
 
-// C[g] from the chunks' sums, in their order; a thread an element, zeros for an adapter
-// without a row.
+// C[g] from the chunks' sums, in their order; a thread an element, threads along M (the
+// sums' rows), zeros for an adapter without a row.
 template <int DT>
 __global__ __launch_bounds__(256) void adapters_wgrad_join_kernel(AdapterGradParams p) {
     typedef typename ElemOf<DT>::type T;
     const int job = blockIdx.z, g = blockIdx.y, M = p.M[job];
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)M * p.rank;
     if (at >= n) return;
-    // consecutive threads along C's rows
-    const int j = p.wide_first[job] ? (int)(at % p.rank) : (int)(at / M), m = p.wide_first[job] ? (int)(at / p.rank) : (int)(at % M);
+    const int j = (int)(at / M), m = (int)(at % M);
     const RowSpan s = rows_of(p.offsets, g, p.adapters, p.rows);
-    const float *part = p.part[job] + (int64_t)j * M + m;
-    float sum = 0;
-    for (int k = 0; s.lo + k * kChunk < s.hi; ++k) {
-        const int block = k == 0 ? g : p.adapters + 1 + s.lo / kChunk + k - 1;
-        sum += part[(int64_t)block * n];
-    }
+    const int tiles = (s.hi - s.lo + kChunk - 1) / kChunk;
+    const float *part = p.part[job] + at, *next = part + (int64_t)(p.adapters + s.lo / kChunk) * n;
+    float sum = tiles > 0 ? part[g * n] : 0.0f;
+#pragma unroll 8
+    for (int k = 1; k < tiles; ++k) sum += next[k * n];
     const int64_t to = (int64_t)g * p.sC[job] + (p.wide_first[job] ? m * p.ldc[job] + j : j * p.ldc[job] + m);
     if (DT == DT_F32 || p.c_f32) reinterpret_cast<float *>(p.C[job])[to] = sum;
     else reinterpret_cast<T *>(p.C[job])[to] = (T)sum;

@@ -14,55 +14,77 @@ inline tg_status launched() { return hipGetLastError() == hipSuccess ? TG_OK : T
 
 template <int DT> using Tile256 = RingCfg<DT, 256, 256, 2, 2, 16>;
 template <int DT> using Tile128 = RingCfg<DT, 128, 128, 2, 2, 16>;
-using Tile64F32 = RingCfg<DT_F32, 64, 64, 2, 2, 16>;
+template <int DT> using Tile64 = RingCfg<DT, 64, 64, 2, 2, 16>;
 
-template <class C, class P, bool B_KS, bool PIPE, int STAGES>
+// Tiles: whole ones and pieces, or with K split and a second launch that adds up.
+template <class C, class P, bool KS, bool ORDERED, bool PIPE, int STAGES>
 tg_status launch_adapter_tiles(const AdapterParams &p, const ProductPlan &plan, hipStream_t s) {
     const dim3 grid((unsigned)plan.gx), block(C::THREADS);
-    if (p.order) hipLaunchKernelGGL((adapters_tile_kernel<C, P, B_KS, true, PIPE, STAGES>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((adapters_tile_kernel<C, P, B_KS, false, PIPE, STAGES>), grid, block, 0, s, p);
+    if constexpr (std::is_same<C, P>::value) {
+        if (p.splits > 1) {
+            hipLaunchKernelGGL((adapters_tile_split_kernel<C, KS, ORDERED, PIPE, STAGES>), grid, block, 0, s, p);
+            const tg_status st = launched();
+            if (st != TG_OK) return st;
+            const int64_t sums = cdiv((int64_t)p.rows * cdiv(p.N, 4), 256);
+            hipLaunchKernelGGL((adapters_sum_kernel<C::DT>), dim3((unsigned)sums), dim3(256), 0, s, p);
+            return launched();
+        }
+    }
+    hipLaunchKernelGGL((adapters_tile_kernel<C, P, KS, ORDERED, PIPE, STAGES>), grid, block, 0, s, p);
     return launched();
+}
+
+template <int DT, bool KS, bool ORDERED>
+tg_status launch_adapters_many(const AdapterParams &p, const AdapterPlan &plan, hipStream_t s) {
+    if (p.rank > 0) {
+        const dim3 grid((unsigned)plan.low.gx, plan.low.gy, plan.low.gz);
+        hipLaunchKernelGGL((shrink_tile_kernel<Tile64<DT>, KS, ORDERED, 4>), grid, dim3(256), 0, s, p);
+        tg_status st = launched();
+        if (st != TG_OK) return st;
+        const int64_t quads = cdiv((int64_t)p.rows * (p.ld_low / 4), 256);
+        if (!grid_fits(quads, 256)) return TG_ERR_UNSUPPORTED;
+        hipLaunchKernelGGL((shrink_join_kernel<DT>), dim3((unsigned)quads), dim3(256), 0, s, p);
+        st = launched();
+        if (st != TG_OK) return st;
+    }
+    if constexpr (DT == DT_F32) {
+        return launch_adapter_tiles<Tile64<DT>, Tile64<DT>, KS, ORDERED, true, 4>(p, plan.product, s);
+    } else {
+        if (plan.product.info.tile_m == 256)
+            return launch_adapter_tiles<Tile256<DT>, Tile128<DT>, KS, ORDERED, true, 4>(p, plan.product, s);
+        return launch_adapter_tiles<Tile128<DT>, Tile128<DT>, KS, ORDERED, false, 3>(p, plan.product, s);
+    }
 }
 
 template <int DT, bool TRANS>
 tg_status launch_adapters_as(AdapterParams p, void *workspace, hipStream_t s) {
     using S = StreamShape<DT, TRANS>;
-    const AdapterPlan plan = plan_adapters<DT, TRANS>(p.experts, p.rows, p.N, p.K, p.rank);
-    const ProductPlan &product = plan.product;
-    if (!product.fits()) return TG_ERR_UNSUPPORTED;
-    const int64_t strips_t = cdiv(p.rank, S::COLS);
+    const AdapterPlan plan = plan_adapters_as<DT, TRANS>(p.experts, p.rows, p.N, p.K, p.rank);
+    if (!plan.product.fits() || !plan.low.fits() ||
+        !grid_fits(plan.product.gx + plan.low.gx, 64 * plan.product.info.waves))
+        return TG_ERR_UNSUPPORTED;
     p.splits = plan.splits;
     p.t_splits = plan.t_splits;
-    if (plan.few) {
-        p.part = static_cast<float *>(workspace);
-        p.part_t = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.part_bytes);
-        const int64_t row_tiles = cdiv(p.rows, 16), base = cdiv(p.N, S::COLS) * row_tiles * plan.splits;
-        const int64_t join = cdiv(p.N, 1024) * p.rows;
-        if (!grid_fits(join, 256)) return TG_ERR_UNSUPPORTED;
-        hipLaunchKernelGGL((adapters_few_kernel<DT, TRANS>), dim3((unsigned)product.gx), dim3(64 * plan.waves),
-                           plan.waves * S::FRAGS * 1024, s, p, (int)base, (int)row_tiles, (int)strips_t);
-        const tg_status st = launched();
-        if (st != TG_OK) return st;
-        hipLaunchKernelGGL((adapters_join_kernel<DT, TRANS>), dim3((unsigned)join), dim3(256), 0, s, p);
-        return launched();
-    }
-    p.low = static_cast<char *>(workspace);
+    p.part = static_cast<float *>(workspace);
+    p.part_t = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.part_bytes);
+    p.low = static_cast<char *>(workspace) + plan.part_bytes + plan.part_t_bytes;
     p.ld_low = plan.ld_low;
-    if (p.rank > 0) {
-        const ProductPlan low = plan_of(TG_EXPERTS_STREAM, 16, S::COLS, plan.t_waves, strips_t,
-                                        tiles_and_slots(p.rows, p.experts, 16));
-        hipLaunchKernelGGL((shrink_kernel<DT, TRANS>), dim3((unsigned)low.gx, low.gy, low.gz), dim3(64 * plan.t_waves),
-                           plan.t_waves * S::FRAGS * 1024, s, p);
-        const tg_status st = launched();
-        if (st != TG_OK) return st;
-    }
-    if constexpr (DT == DT_F32) {
-        return launch_adapter_tiles<Tile64F32, Tile64F32, !TRANS, true, 4>(p, product, s);
-    } else {
-        if (product.info.tile_m == 256)
-            return launch_adapter_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true, 4>(p, product, s);
-        return launch_adapter_tiles<Tile128<DT>, Tile128<DT>, !TRANS, false, 3>(p, product, s);
-    }
+    if (plan.form == ADAPTERS_TILES)
+        return p.order ? launch_adapters_many<DT, !TRANS, true>(p, plan, s) : launch_adapters_many<DT, !TRANS, false>(p, plan, s);
+    const int64_t low = p.rank > 0 ? plan.low.gx * plan.low.gy * plan.low.gz : 0, strips_t = cdiv(p.rank, S::COLS);
+    const int64_t join = cdiv(p.N, 256 * join_cols<TRANS>()) * p.rows;
+    if (!grid_fits(join, 256)) return TG_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)(low + plan.product.gx)), block(64 * plan.product.info.waves);
+    if (plan.form == ADAPTERS_STREAM)
+        hipLaunchKernelGGL((adapters_few_kernel<DT, TRANS>), grid, block,
+                           (unsigned)(plan.product.info.waves * S::FRAGS * 1024), s, p, (int)low, (int)cdiv(p.rows, 16),
+                           (int)strips_t);
+    else
+        hipLaunchKernelGGL((adapters_split_kernel<Tile64<DT>, !TRANS, 4>), grid, block, 0, s, p, (int)low, (int)strips_t);
+    const tg_status st = launched();
+    if (st != TG_OK) return st;
+    hipLaunchKernelGGL((adapters_join_kernel<DT, TRANS>), dim3((unsigned)join), dim3(256), 0, s, p);
+    return launched();
 }
 
 }  // namespace
@@ -82,10 +104,13 @@ tg_status launch_adapters_wgrad(const AdapterGradParams &q, void *workspace, hip
     p.strips[1] = (int)plan.strips[1];
     p.slots = (int)plan.slots;
     p.rank_tiles = (int)plan.rank_tiles;
-    const int64_t longest = (int64_t)(p.M[0] > p.M[1] ? p.M[0] : p.M[1]) * p.rank, join = cdiv(longest, 256);
+    const int64_t join = cdiv((int64_t)(p.M[0] > p.M[1] ? p.M[0] : p.M[1]) * p.rank, 256);
     if (!grid_fits(plan.workgroups, 256) || !grid_fits(join, 256)) return TG_ERR_UNSUPPORTED;
     if (plan.workgroups > 0) {
-        hipLaunchKernelGGL((adapters_wgrad_kernel<DT>), dim3((unsigned)plan.workgroups), dim3(256), 0, s, p);
+        const dim3 grid((unsigned)plan.workgroups);
+        if (p.rank <= 16) hipLaunchKernelGGL((adapters_wgrad_kernel<DT, 1>), grid, dim3(256), 0, s, p);
+        else if (p.rank <= 32) hipLaunchKernelGGL((adapters_wgrad_kernel<DT, 2>), grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL((adapters_wgrad_kernel<DT, kWgradRank / 16>), grid, dim3(256), 0, s, p);
         const tg_status st = launched();
         if (st != TG_OK) return st;
     }

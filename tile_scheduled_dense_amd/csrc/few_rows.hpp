@@ -117,22 +117,25 @@ __device__ __forceinline__ void few_sum(const STRIP &strip, const char *row, int
         strip.template load<PART>(at, k_left, lane, b);
         a.template load<PART>(row, (int64_t)at * S::K, k_left, lane);
     };
-    if (s < whole) {
-        const std::integral_constant<int, PART_ALL> full;
+    // the next stage's loads in flight during the current one's products
+    auto loop = [&](int last, auto part) {
+        if (s >= last) return;
         StreamB<DT, TRANS> b0, b1;
         FewA<DT, TRANS> a0, a1;
-        fetch(s, b0, a0, full);
+        fetch(s, b0, a0, part);
         for (;;) {
             s += waves;
-            const bool more = s < whole;
-            if (more) fetch(s, b1, a1, full);
+            const bool more = s < last;
+            if (more) fetch(s, b1, a1, part);
             __builtin_amdgcn_sched_barrier(0);
             stream_mma<DT, TRANS>(b0, a0, acc);
             if (!more) break;
             b0 = b1;
             a0 = a1;
         }
-    }
+    };
+    if (strip.n_left >= STRIP::COLS) loop(whole, std::integral_constant<int, PART_ALL>{});
+    else if (chunks) loop(end, std::integral_constant<int, PART_CHUNKS>{});
     for (; s < end; s += waves) {
         StreamB<DT, TRANS> b;
         FewA<DT, TRANS> a;
@@ -168,22 +171,10 @@ __device__ __forceinline__ f32x4 few_item(const f32x4 *lds, int waves, int it, i
     return x;
 }
 
-// The stages of split z of `splits`.
-__device__ __forceinline__ void few_range(int stages, int splits, int z, int &begin, int &end) {
-    begin = (int)((int64_t)stages * z / splits);
-    end = (int)((int64_t)stages * (z + 1) / splits);
-}
-
 // ---- the gated pair -----------------------------------------------------------------
-// grid: (strips x splits) x row tiles (row_slot).  splits > 1: fp32 sums of u and v, rows x
-// N each, split by split, into part.
-struct GatedFewParams : GatedParams {
-    float *part;
-    int splits;
-};
-
+// grid: (strips x splits) x row tiles (row_slot)
 template <int DT, bool TRANS>
-__global__ __launch_bounds__(512) void gated_few_kernel(GatedFewParams p) {
+__global__ __launch_bounds__(512) void gated_few_kernel(GatedParams p) {
     using S = StreamShape<DT, TRANS>;
     using Strips = TwoStrips<DT, TRANS>;
     extern __shared__ f32x4 stream_lds[];
@@ -202,7 +193,7 @@ __global__ __launch_bounds__(512) void gated_few_kernel(GatedFewParams p) {
 #pragma unroll
     for (int j = 0; j < S::FRAGS; ++j) acc[j] = f32x4{0, 0, 0, 0};
     int begin, end;
-    few_range(stages, p.splits, z, begin, end);
+    split_range(stages, p.splits, z, begin, end);
     few_sum<DT, TRANS>(strips, row, p.K, p.K % S::PER == 0 && (TRANS || p.N % S::PER == 0), begin + wave, waves, end, lane,
                        acc);
 #pragma unroll
@@ -249,7 +240,7 @@ __global__ __launch_bounds__(512) void gated_few_kernel(GatedFewParams p) {
 
 // h, u and v from the splits' sums: a thread four neighbours of a row
 template <int DT>
-__global__ __launch_bounds__(256) void gated_join_kernel(GatedFewParams p) {
+__global__ __launch_bounds__(256) void gated_join_kernel(GatedParams p) {
     const int64_t quads = (p.N + 3) / 4, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (at >= quads * p.rows) return;
     const int64_t r = at / quads, c = at % quads * 4, plane = (int64_t)p.rows * p.N;

@@ -66,7 +66,7 @@ tg_status gated_bytes(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dt
     *bytes = 0;
     if (rows == 0 || N == 0) return TG_OK;
     const bool t = transposed != 0;
-    const FewPlan plan = dtype == TG_F32    ? plan_gated<DT_F32>(t, experts, rows, N, K)
+    const GatedPlan plan = dtype == TG_F32    ? plan_gated<DT_F32>(t, experts, rows, N, K)
                          : dtype == TG_BF16 ? plan_gated<DT_BF16>(t, experts, rows, N, K)
                                             : plan_gated<DT_F16>(t, experts, rows, N, K);
     *bytes = gated_workspace(plan, rows, N);
@@ -236,7 +236,7 @@ tg_status adapters(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t
     if (!tile_fits(ldx, esz) || !tile_fits(ldw, esz) || !tile_fits(lda, esz) || !tile_fits(ldb, esz) || !tile_fits(ldy, esz) ||
         !tile_fits(rank, esz) || (T && !tile_fits(ldt, esz)))
         return TG_ERR_UNSUPPORTED;
-    if (order && !plan.few && rows * ldx * esz >= (int64_t(1) << 31) - 65536) return TG_ERR_UNSUPPORTED;
+    if (order && plan.form == ADAPTERS_TILES && rows * ldx * esz >= (int64_t(1) << 31) - 65536) return TG_ERR_UNSUPPORTED;
     st = device_ok();
     if (st != TG_OK) return st;
     AdapterParams p = {};

@@ -24,6 +24,10 @@ struct GatedParams : GroupedParams {     // A, B (the gate's), C = H, ldc, N: co
     char *dU, *dV;                        // C NULL: h not stored
     int64_t ldu, lddu;
     int act;
+    // K split over workgroups (forward, few rows): fp32 sums of u and v, rows x N each,
+    // split by split, in part
+    float *part;
+    int splits;
 };
 
 // The pair of second operands: MFMA tiles below T are the first's, the others the second's.
@@ -78,6 +82,15 @@ struct GatedTile : GroupedTile<C, false, B_KS, STAGES, OperandA<C, false>, Opera
         this->a.init(A, lda, m_left, (this->wave / C::WAVES_N) * C::WTM, lds0 + STAGES * Base::OB::REGION, this->lane,
                      this->wave);
         this->acc.zero();
+    }
+    // u (FIRST 0) or v (TN / 2) in fp32
+    template <int FIRST>
+    __device__ __forceinline__ void store_sums(float *to, int64_t ld, int m_left, int n_left) const {
+        const auto value = [&](auto i, auto j, auto v) {
+            return this->acc.get(decltype(i)::value, FIRST + decltype(j)::value, decltype(v)::value);
+        };
+        TileStore<C, TH, decltype(value)>{value, this->lane, this->wave}.store(reinterpret_cast<char *>(to), 0, ld, m_left,
+                                                                               n_left, true, false);
     }
 };
 
@@ -177,13 +190,22 @@ struct WaveRows {
     }
 };
 
-template <class C, bool B_KS, bool PIPE, int STAGES>
+// split: of K, whose sums it stores instead (SPLIT; A, Bg, Bu and K are the split's)
+template <class C, bool B_KS, bool PIPE, int STAGES, bool SPLIT = false>
 __device__ __forceinline__ void run_gated(const GatedParams &p, char *smem, const RowTile &t, const char *A, const char *Bg,
-                                          const char *Bu, int K, int64_t row) {
+                                          const char *Bu, int K, int64_t row, int split = 0) {
     GatedTile<C, B_KS, STAGES> tile;
     tile.init(A, p.lda, t.rows, Bg, Bu, p.ldb, p.N - t.n0, K, smem);
     if constexpr (PIPE) tile.run_pipe();
     else tile.run_ring();
+    if constexpr (SPLIT) {
+        if (p.splits > 1) {
+            float *part = p.part + (2 * (int64_t)split * p.rows + row) * p.N + t.n0;
+            tile.template store_sums<0>(part, p.N, t.rows, p.N - t.n0);
+            tile.template store_sums<C::TN / 2>(part + (int64_t)p.rows * p.N, p.N, t.rows, p.N - t.n0);
+            return;
+        }
+    }
     // a lane a chunk of h's columns: u in the first half of the wave's, v in the second
     typedef Chunk<C::DT> X;
     constexpr int PER = X::PER, HALF = C::WTN / 2, ITEMS = HALF / PER;
@@ -249,6 +271,33 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void gated_tile_kernel(Ga
     const int K = dead ? 0 : p.K;
     if (PIECES && t.piece) run_gated<P, B_KS, PIPE, STAGES>(p, smem, t, A, p.B + b, p.Bu + b, K, row);
     else run_gated<C, B_KS, PIPE, STAGES>(p, smem, t, A, p.B + b, p.Bu + b, K, row);
+}
+
+// The stages (or K tiles) of split z of `splits`.
+__device__ __forceinline__ void split_range(int stages, int splits, int z, int &begin, int &end) {
+    begin = (int)((int64_t)stages * z / splits);
+    end = (int)((int64_t)stages * (z + 1) / splits);
+}
+
+// Few rows an expert, but too many to take the weights straight to registers for: tiles of
+// BM rows by row_slot, K split over workgroups.  grid: (column tiles x splits) x row tiles.
+template <class C, bool B_KS, int STAGES>
+__global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void gated_split_kernel(GatedParams p) {
+    __shared__ __attribute__((aligned(1024))) char smem[GatedTile<C, B_KS, STAGES>::LDS];
+    const int z = blockIdx.x % p.splits;
+    RowTile t;
+    RowSpan span;
+    t.n0 = (int)(blockIdx.x / p.splits) * (C::BN / 2);
+    if (!row_slot<C::BM>(p.offsets, p.experts, p.rows, slot_of(p.experts), t.g, span)) return;
+    const bool dead = t.g == p.experts;
+    const int64_t row = span.lo;
+    t.rows = span.hi - span.lo;
+    int begin = 0, end = 0;
+    if (!dead) split_range((p.K + C::BK - 1) / C::BK, p.splits, z, begin, end);
+    const int k0 = begin * C::BK, K = (end * C::BK < p.K ? end * C::BK : p.K) - k0;
+    const char *A = p.A + (row * p.lda + k0) * C::ELEM;
+    const int64_t b = ((dead ? 0 : (int64_t)t.g * p.sB) + (B_KS ? k0 * p.ldb + t.n0 : t.n0 * p.ldb + k0)) * C::ELEM;
+    run_gated<C, B_KS, false, STAGES, true>(p, smem, t, A, p.B + b, p.Bu + b, K > 0 ? K : 0, row, z);
 }
 
 // Four neighbours of a row, n of which exist.

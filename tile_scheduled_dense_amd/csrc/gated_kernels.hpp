@@ -15,7 +15,7 @@ inline tg_status launched() { return hipGetLastError() == hipSuccess ? TG_OK : T
 template <int DT> using Tile256 = RingCfg<DT, 256, 256, 2, 2, 16>;
 template <int DT> using Tile128 = RingCfg<DT, 128, 128, 2, 2, 16>;
 using Tile64F32 = RingCfg<DT_F32, 64, 64, 2, 2, 16>;
-using Tile64x128F32 = RingCfg<DT_F32, 64, 128, 2, 2, 16>;
+template <int DT> using Tile64x128 = RingCfg<DT, 64, 128, 2, 2, 16>;
 
 template <class C, class P, bool B_KS, bool PIPE, int STAGES>
 tg_status launch_gated_tiles(const GatedParams &p, const ProductPlan &plan, hipStream_t s) {
@@ -25,17 +25,19 @@ tg_status launch_gated_tiles(const GatedParams &p, const ProductPlan &plan, hipS
 
 template <int DT, bool TRANS>
 tg_status launch_gated_as(const GatedParams &p, void *workspace, hipStream_t s) {
-    const FewPlan plan = plan_gated<DT, TRANS>(p.experts, p.rows, p.N, p.K);
+    const GatedPlan plan = plan_gated_as<DT, TRANS>(p.experts, p.rows, p.N, p.K);
     const ProductPlan &product = plan.product;
     if (!product.fits()) return TG_ERR_UNSUPPORTED;
-    if (plan.few) {
-        GatedFewParams f;
-        static_cast<GatedParams &>(f) = p;
+    if (plan.splits > 0) {
+        GatedParams f = p;
         f.part = static_cast<float *>(workspace);
         f.splits = workspace ? plan.splits : 1;
-        const unsigned lds = plan.waves * StreamShape<DT, TRANS>::FRAGS * 1024;
         const dim3 grid((unsigned)(product.gx / plan.splits * f.splits), product.gy, product.gz);
-        hipLaunchKernelGGL((gated_few_kernel<DT, TRANS>), grid, dim3(64 * plan.waves), lds, s, f);
+        if (product.info.kernel == TG_EXPERTS_STREAM)
+            hipLaunchKernelGGL((gated_few_kernel<DT, TRANS>), grid, dim3(64 * product.info.waves),
+                               (unsigned)(product.info.waves * StreamShape<DT, TRANS>::FRAGS * 1024), s, f);
+        else
+            hipLaunchKernelGGL((gated_split_kernel<Tile64x128<DT>, !TRANS, 4>), grid, dim3(256), 0, s, f);
         const tg_status st = launched();
         if (st != TG_OK || f.splits == 1) return st;
         const int64_t quads = (int64_t)p.rows * cdiv(p.N, 4);
@@ -43,7 +45,7 @@ tg_status launch_gated_as(const GatedParams &p, void *workspace, hipStream_t s) 
         return launched();
     }
     if constexpr (DT == DT_F32) {
-        return launch_gated_tiles<Tile64x128F32, Tile64x128F32, !TRANS, true, 4>(p, product, s);
+        return launch_gated_tiles<Tile64x128<DT>, Tile64x128<DT>, !TRANS, true, 4>(p, product, s);
     } else {
         if (product.info.tile_m == 256)
             return launch_gated_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true, 4>(p, product, s);

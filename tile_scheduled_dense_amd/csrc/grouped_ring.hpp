@@ -355,16 +355,23 @@ struct GroupedTile {
         a.tail_load(k0, K, &tail[0]);
         b.tail_load(k0, K, &tail[OA::PER]);
     }
+    // at most `later` later tiles' copies in flight, or AHEAD if that is less
+    template <int AHEAD>
+    __device__ __forceinline__ static void wait_copies(int later) {
+        static_assert(AHEAD * COPIES < 64, "the counter's range");
+        if constexpr (AHEAD == 0) {
+            wait_vmcnt<0>();
+        } else {
+            if (later >= AHEAD) wait_vmcnt<AHEAD * COPIES>();
+            else wait_copies<AHEAD - 1>(later);
+        }
+    }
     // Wait until this wave's share of tile t is in LDS copy `stage`, at most AHEAD
     // later tiles being in flight; the last tile is stored from its registers.
     template <int AHEAD>
     __device__ __forceinline__ void land(int t, int stage) {
         if (t < ndma) {
-            const int later = ndma - 1 - t;
-            if (AHEAD >= 3 && later >= 3) wait_vmcnt<3 * COPIES>();
-            else if (AHEAD >= 2 && later >= 2) wait_vmcnt<2 * COPIES>();
-            else if (AHEAD >= 1 && later >= 1) wait_vmcnt<COPIES>();
-            else wait_vmcnt<0>();
+            wait_copies<AHEAD>(ndma - 1 - t);
         } else {
             wait_vmcnt<0>();
             a.tail_store(stage, &tail[0]);
