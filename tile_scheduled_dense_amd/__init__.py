@@ -232,12 +232,14 @@ def _declare_ffn(lib, i64, vp, ci):
 
 
 def _addr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    # tensors first and without a look for the attribute: 0.3 us an argument against 0.7
+    if x is None or type(x) is int:
         return x
-    if hasattr(x, "data_ptr"):
-        return int(x.data_ptr())
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):
+            return x
     raise TypeError(f"expected a device address or a tensor, got {type(x)!r}")
 
 
@@ -370,7 +372,7 @@ def tile_gemm_pack_b(batch, K, N, dtype, B, ldb, strideB, packed, packed_bytes=N
 
 # ---- the operators of a mixture-of-experts layer (include/tile_gemm_experts.h) ----------
 def _bytes_of(x) -> int:
-    return x.numel() * x.element_size() if hasattr(x, "numel") else 0
+    return getattr(x, "nbytes", 0)
 
 
 def experts_version() -> int:

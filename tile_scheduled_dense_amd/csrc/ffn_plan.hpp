@@ -41,8 +41,9 @@ GatedPlan plan_gated_as(int64_t experts, int64_t rows, int64_t N, int64_t K) {
         return p;
     }
     const int64_t strips = cdiv(N, 64) * used;
-    if (mean <= 64 || (DT != DT_F32 && mean <= 128 && strips <= 128)) {
-        p.splits = few_splits(strips, 256, cdiv(K, 64 / S::E), 8);
+    const bool split = mean <= 64 || (DT != DT_F32 && mean <= 128 && strips <= 128);
+    if (split || (DT != DT_F32 && cdiv(rows, 128) * cdiv(N, 64) <= 400)) {
+        p.splits = split ? few_splits(strips, 256, cdiv(K, 64 / S::E), 8) : 1;
         p.product = plan_of(TG_EXPERTS_TILES, 64, 64, 4, cdiv(N, 64) * p.splits, tiles_and_slots(rows, experts, 64));
         return p;
     }
@@ -60,7 +61,14 @@ inline int64_t gated_workspace(const GatedPlan &p, int64_t rows, int64_t N) {
     return p.splits > 1 ? p.splits * 2 * rows * N * 4 : 0;
 }
 
-// The gate's gradient: the products' own rule (plan_grouped).
+// The gate's gradient: the products' own rule (plan_grouped_as), but the smaller tiles of 16
+// bits are smaller still.
+template <int DT, bool TRANS>
+ProductPlan plan_gate_grad_as(int64_t experts, int64_t rows, int64_t N, int64_t K) {
+    const ProductPlan p = plan_grouped_as<DT, TRANS>(experts, rows, N, K);
+    if (DT == DT_F32 || p.info.kernel != TG_EXPERTS_TILES || p.info.tile_m == 256) return p;
+    return plan_tiles(experts, rows, N, 64, cdiv(rows, 64) * cdiv(N, 128) <= 512 ? 64 : 128, false, false, 4);
+}
 
 // ---- adapters -------------------------------------------------------------------------------
 // Up to so many rows a projection's columns and its adapters' share one launch, and another

@@ -371,7 +371,7 @@ __device__ __forceinline__ void run_gate_grad(const GatedParams &p, char *smem, 
     const bool whole = t.rows >= C::BM && p.N - t.n0 >= C::BN && !dead;
     auto pass = [&](int first, auto a, auto w) {
         constexpr bool WHOLE = decltype(w)::value;
-        constexpr int BATCH = WHOLE ? 4 : 1, BATCHES = rows.ROWS * ITEMS / 64 / BATCH;
+        constexpr int COUNT = rows.ROWS * ITEMS / 64, BATCH = !WHOLE ? 1 : (COUNT < 4 ? COUNT : 4), BATCHES = COUNT / BATCH;
         static_assert(BATCHES * BATCH * 64 == rows.ROWS * ITEMS, "whole batches");
         // u and v of the next four chunks in flight during the current ones' work
         X u[BATCH], v[BATCH], u1[BATCH], v1[BATCH];

@@ -14,7 +14,7 @@ inline tg_status launched() { return hipGetLastError() == hipSuccess ? TG_OK : T
 
 template <int DT> using Tile256 = RingCfg<DT, 256, 256, 2, 2, 16>;
 template <int DT> using Tile128 = RingCfg<DT, 128, 128, 2, 2, 16>;
-using Tile64F32 = RingCfg<DT_F32, 64, 64, 2, 2, 16>;
+template <int DT> using Tile64 = RingCfg<DT, 64, 64, 2, 2, 16>;
 template <int DT> using Tile64x128 = RingCfg<DT, 64, 128, 2, 2, 16>;
 
 template <class C, class P, bool B_KS, bool PIPE, int STAGES>
@@ -61,7 +61,7 @@ tg_status launch_grad_tiles(const GatedParams &p, const ProductPlan &plan, hipSt
 
 template <int DT, bool TRANS>
 tg_status launch_gate_grad_as(const GatedParams &p, hipStream_t s) {
-    const ProductPlan plan = plan_grouped_as<DT, TRANS>(p.experts, p.rows, p.N, p.K);
+    const ProductPlan plan = plan_gate_grad_as<DT, TRANS>(p.experts, p.rows, p.N, p.K);
     if (!plan.fits()) return TG_ERR_UNSUPPORTED;
     if (plan.info.kernel == TG_EXPERTS_STREAM) {
         const unsigned lds = plan.info.waves * StreamShape<DT, TRANS>::FRAGS * 1024;
@@ -70,8 +70,12 @@ tg_status launch_gate_grad_as(const GatedParams &p, hipStream_t s) {
         return launched();
     }
     if (plan.info.tile_m == 256) return launch_grad_tiles<Tile256<DT>, Tile128<DT>, !TRANS, true, 4>(p, plan, s);
-    if constexpr (DT == DT_F32) return launch_grad_tiles<Tile64F32, Tile64F32, !TRANS, true, 4>(p, plan, s);
-    else return launch_grad_tiles<Tile128<DT>, Tile128<DT>, !TRANS, false, 3>(p, plan, s);
+    if constexpr (DT == DT_F32) {
+        return launch_grad_tiles<Tile64<DT>, Tile64<DT>, !TRANS, true, 4>(p, plan, s);
+    } else {
+        if (plan.info.tile_n == 128) return launch_grad_tiles<Tile64x128<DT>, Tile64x128<DT>, !TRANS, false, 4>(p, plan, s);
+        return launch_grad_tiles<Tile64<DT>, Tile64<DT>, !TRANS, false, 4>(p, plan, s);
+    }
 }
 
 }  // namespace
