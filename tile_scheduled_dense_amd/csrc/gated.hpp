@@ -362,34 +362,44 @@ __device__ __forceinline__ void run_gate_grad(const GatedParams &p, char *smem, 
                                               const char *B, int K, int64_t row, bool dead) {
     GroupedTile<C, false, B_KS, STAGES> tile;
     tile.init(A, p.lda, t.rows, B, p.ldb, p.N - t.n0, K, smem);
-    if constexpr (PIPE) tile.run_pipe();
-    else tile.run_ring();
     typedef Chunk<C::DT> X;
     constexpr int PER = X::PER, ITEMS = C::WTN / PER;
     WaveRows<C, GroupedTile<C, false, B_KS, STAGES>> rows;
+    constexpr int COUNT = rows.ROWS * ITEMS / 64, WIDE = COUNT < 4 ? COUNT : 4;
+    static_assert(COUNT * 64 == rows.ROWS * ITEMS && COUNT % WIDE == 0, "whole batches");
     const int m = (tile.wave / C::WAVES_N) * C::WTM, n = t.n0 + (tile.wave % C::WAVES_N) * C::WTN;
     const bool whole = t.rows >= C::BM && p.N - t.n0 >= C::BN && !dead;
+    // Chunk `it` of a pass, and u and v there.  In a whole tile, without a branch, four at a
+    // time; those of the next four are in flight during the current ones' work, of the
+    // first during the product's last K tiles.
+    auto fetch = [&](int first, int it, X &u, X &v, bool all) {
+        const int r = it / ITEMS, c = it % ITEMS * PER;
+        const int left = all ? PER : (m + first + r < t.rows && !dead ? p.N - n - c : 0);
+        const int64_t at = (row + m + first + r) * p.ldu + n + c;
+        u.load(p.U, at, left);
+        v.load(p.V, at, left);
+    };
+    X u[WIDE], v[WIDE];
+    if (whole) {
+#pragma unroll
+        for (int k = 0; k < WIDE; ++k) fetch(0, k * 64 + (int)(threadIdx.x & 63), u[k], v[k], true);
+    }
+    if constexpr (PIPE) tile.run_pipe();
+    else tile.run_ring();
     auto pass = [&](int first, auto a, auto w) {
         constexpr bool WHOLE = decltype(w)::value;
-        constexpr int COUNT = rows.ROWS * ITEMS / 64, BATCH = !WHOLE ? 1 : (COUNT < 4 ? COUNT : 4), BATCHES = COUNT / BATCH;
-        static_assert(BATCHES * BATCH * 64 == rows.ROWS * ITEMS, "whole batches");
-        // u and v of the next four chunks in flight during the current ones' work
-        X u[BATCH], v[BATCH], u1[BATCH], v1[BATCH];
-        auto fetch = [&](int batch, X(&to_u)[BATCH], X(&to_v)[BATCH]) {
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int it = (batch * BATCH + k) * 64 + tile.lane, r = it / ITEMS, c = it % ITEMS * PER;
-                const int left = WHOLE ? PER : (m + first + r < t.rows && !dead ? p.N - n - c : 0);
-                const int64_t at = (row + m + first + r) * p.ldu + n + c;
-                to_u[k].load(p.U, at, left);
-                to_v[k].load(p.V, at, left);
-            }
-        };
-        fetch(0, u, v);
+        constexpr int BATCH = WHOLE ? WIDE : 1, BATCHES = COUNT / BATCH;
 #pragma unroll 1
         for (int batch = 0; batch < BATCHES; ++batch) {
-            if (batch + 1 < BATCHES) fetch(batch + 1, u1, v1);
-            X du[BATCH], dv[BATCH], h[BATCH];
+            X u1[BATCH], v1[BATCH], du[BATCH], dv[BATCH], h[BATCH];
+            if constexpr (WHOLE) {
+                if (batch + 1 < BATCHES || first + rows.ROWS < C::WTM) {       // the next pass's rows follow
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) fetch(first, ((batch + 1) * BATCH + k) * 64 + tile.lane, u1[k], v1[k], true);
+                }
+            } else {
+                fetch(first, batch * 64 + tile.lane, u[0], v[0], false);
+            }
 #pragma unroll
             for (int k = 0; k < BATCH; ++k) {
                 const int it = (batch * BATCH + k) * 64 + tile.lane, r = it / ITEMS, c = it % ITEMS * PER;
@@ -414,10 +424,12 @@ __device__ __forceinline__ void run_gate_grad(const GatedParams &p, char *smem, 
                 dv[k].store(p.dV, at * p.lddu + n + c, left, p.past);
                 if (p.C) h[k].store(p.C, at * p.ldc + n + c, left, p.past);
             }
+            if constexpr (WHOLE) {
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                u[k] = u1[k];
-                v[k] = v1[k];
+                for (int k = 0; k < BATCH; ++k) {
+                    u[k] = u1[k];
+                    v[k] = v1[k];
+                }
             }
         }
     };
