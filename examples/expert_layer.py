@@ -4,11 +4,12 @@ The layer: a router picks `top_k` of `experts` for each token, each expert is a 
 projections y = (silu(x W1) * (x W3)) W2, and the experts' results are summed with the router's
 weights.  The step below runs forward and backward through
 
-    sort -> gather -> grouped products -> combine        (tile_gemm_expert_*, tile_gemm_grouped)
-    combine's gradient -> transposed products, weights' gradients -> the gather's gradient
+    sort -> gather -> the gated pair -> the product W2 -> combine   (tile_gemm_expert_*, _gated, _grouped)
+    combine's gradient -> the gate's gradient -> transposed products, weights' gradients -> the
+    gather's gradient                                               (tile_gemm_gated_grad, _grouped_wgrad)
 
 and decoding runs the same layer with the three projections in 4 bits (tile_gemm_pack_q4 once,
-tile_gemm_q4 each step).  torch supplies memory, the router's softmax and the elementwise gate.
+tile_gemm_q4 each step, tile_gemm_gate between).  torch supplies memory and the router's softmax.
 
     python examples/expert_layer.py            # checks against plain torch, prints times
 """
@@ -70,6 +71,24 @@ class Routing:
                              self.offsets, c_dtype="bf16", transposed=int(transposed))
         return c
 
+    def gated(self, a, w1, w3):
+        """silu(a w1) * (a w3) of every expert's rows, and the two products."""
+        E, K, N = w1.shape
+        h, u, v = (torch.empty(a.shape[0], N, dtype=BF16, device=a.device) for _ in range(3))
+        size = tg.tile_gemm_gated_workspace_size(E, a.shape[0], N, K, "bf16")
+        workspace = torch.empty(size, dtype=torch.uint8, device=a.device) if size else None
+        tg.tile_gemm_gated(E, a.shape[0], N, K, "bf16", a, a.stride(0), w1, w3, w1.stride(1), w1.stride(0), h, N,
+                           self.offsets, activation=tg.ACT_SILU, U=u, V=v, ldu=N, workspace=workspace)
+        return h, u, v
+
+    def gated_grad(self, d_y, w2, u, v):
+        """The gradients of u and v from that of the rows' results."""
+        E, N, K = w2.shape
+        d_u, d_v = torch.empty_like(u), torch.empty_like(v)
+        tg.tile_gemm_gated_grad(E, d_y.shape[0], N, K, "bf16", d_y, d_y.stride(0), w2, w2.stride(1), w2.stride(0), u, v, N,
+                                d_u, d_v, N, self.offsets, activation=tg.ACT_SILU, transposed=1)
+        return d_u, d_v
+
     def weight_grad(self, a, d):
         E = self.shape[2]
         g = torch.empty(E, a.shape[1], d.shape[1], dtype=F32, device=a.device)
@@ -83,24 +102,16 @@ def route(x, router, top_k):
     return ids.to(I32).contiguous(), torch.softmax(top, dim=1).contiguous()
 
 
-def silu_grad(h):
-    s = torch.sigmoid(h)
-    return s * (1 + h * (1 - s))
-
-
 def train_step(routing, x, router, w1, w3, w2, d_out, top_k):
     """Forward and backward; returns the output and the gradients of x, the router's weights, w1, w3, w2."""
     ids, weights = route(x, router, top_k)
     routing.sort(ids)
     rows = routing.gather(x)
-    h1, h3 = routing.product(rows, w1), routing.product(rows, w3)
-    g = (torch.nn.functional.silu(h1.float()) * h3.float()).to(BF16)
+    g, h1, h3 = routing.gated(rows, w1, w3)
     y = routing.product(g, w2)
     out = routing.combine(y, weights)
     d_y, d_w = routing.combine_grad(d_out, y, weights)
-    d_g = routing.product(d_y, w2, transposed=True).float()
-    d_h1 = (d_g * h3.float() * silu_grad(h1.float())).to(BF16)
-    d_h3 = (d_g * torch.nn.functional.silu(h1.float())).to(BF16)
+    d_h1, d_h3 = routing.gated_grad(d_y, w2, h1, h3)
     d_rows = routing.product(d_h1, w1, transposed=True) + routing.product(d_h3, w3, transposed=True)
     d_x = routing.combine(d_rows)
     return out, d_x, d_w, routing.weight_grad(rows, d_h1), routing.weight_grad(rows, d_h3), routing.weight_grad(g, d_y)
@@ -142,7 +153,8 @@ def decode_step(routing, x, router, q1, q3, q2, top_k):
     routing.sort(ids)
     rows = routing.gather(x)
     h1, h3 = q1.product(rows, routing.offsets), q3.product(rows, routing.offsets)
-    g = (torch.nn.functional.silu(h1.float()) * h3.float()).to(BF16)
+    g = torch.empty_like(h1)
+    tg.tile_gemm_gate(h1.shape[0], h1.shape[1], "bf16", h1, h3, h1.stride(0), g, g.stride(0), activation=tg.ACT_SILU)
     return routing.combine(q2.product(g, routing.offsets), weights)
 
 

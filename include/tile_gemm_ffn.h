@@ -6,6 +6,7 @@
  *
  *   gated        u = A . Bg,  v = A . Bu,  h = act(u) * v, per expert or for all rows
  *   gated_grad   d_h = D . B,  d_u = d_h * v * act'(u),  d_v = d_h * act(u),  h again
+ *   gate, gate_grad   the same two from u and v (and d_h) that another call gave
  *   adapters     t = s[g] (x . A[g]),  y = x . W + t . B[g]: a projection shared by all
  *                rows, and beside it a low-rank adapter of each row's own
  *   adapters_wgrad   d_A[g] = x^T . d_t,  d_B[g] = t^T . d_y over the rows of adapter g
@@ -20,8 +21,10 @@
  * Conventions: those of tile_gemm_experts.h, and
  *  - Activations by the numbers of tile_gemm.h's fused tail: 0 none, 1 ReLU, 2 GELU (x Phi(x));
  *    3 is SiLU, x / (1 + e^-x).
- *  - Results are of dtype, except where a c_dtype is given; sums, t before its use and the
- *    activation's argument are fp32.  A NaN reaches the results of its own row only.
+ *  - Results are of dtype, except where a c_dtype is given; sums and the activation's
+ *    argument are fp32.  t enters the second product in fp32 for up to 64 rows, and rounded
+ *    once to dtype (as T is) for more.  A NaN or an infinity in a row, or in an adapter,
+ *    reaches that row's, or that adapter's rows', results only.
  *  - transposed 0: matrices are inputs x outputs (Bg, Bu, W: K x N, an adapter's A: K x rank,
  *    B: rank x N); 1: outputs x inputs (N x K, rank x K, N x rank).
  *  - Rows without an expert get zeros in h, u, v and in d_u, d_v (u and v are not read
@@ -76,12 +79,23 @@ tg_status tile_gemm_gated_grad(int64_t experts, int64_t rows, int64_t N, int64_t
                                int64_t lddu, void *H, int64_t ldh, const int32_t *offsets, void *stream);
 
 /*
+ * The gate alone, of rows that another call gave (a projection with adapters, 4-bit
+ * weights): H = act(U) * V, and from the gradient D of H (rows x N) dU = D * V * act'(U),
+ * dV = D * act(U), and H once more (NULL: not written).
+ */
+tg_status tile_gemm_gate(int64_t rows, int64_t N, tg_dtype dtype, int activation, const void *U, const void *V,
+                         int64_t ldu, void *H, int64_t ldh, void *stream);
+tg_status tile_gemm_gate_grad(int64_t rows, int64_t N, tg_dtype dtype, int activation, const void *D, int64_t ldd,
+                              const void *U, const void *V, int64_t ldu, void *dU, void *dV, int64_t lddu, void *H,
+                              int64_t ldh, void *stream);
+
+/*
  * Y[r] = X[r] . W + t[r] . B[g], t[r] = scales[g] * (X[r] . A[g]).  X: rows x K, Y: rows x N, W: K x N
  * (or N x K); A[g], B[g]: K x rank and rank x N (or rank x K and N x rank) at strideA, strideB.
  * scales: one fp32 a adapter, NULL: 1.  Adapter g has the positions offsets[g] .. offsets[g + 1] - 1
  * of the adapters' order, those from offsets[adapters] on have none; position p is row order[p]
  * of X, Y and T (order[p] or its complement: tile_gemm_expert_sort's entry_of_row, with one
- * choice a row, is such a table), or row p where order is NULL.  T (rows x rank, of dtype): t,
+ * choice a row, is such a table; it must hold every row once), or row p where order is NULL.  T (rows x rank, of dtype): t,
  * for the gradients; NULL: not stored.
  */
 tg_status tile_gemm_adapters_workspace_size(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank,
@@ -106,6 +120,35 @@ tg_status tile_gemm_adapters_wgrad(int64_t adapters, int64_t rows, int64_t N, in
                                    int64_t ldb, int64_t strideB, int transposed, tg_dtype c_dtype,
                                    const int32_t *offsets, const int32_t *order, void *workspace,
                                    int64_t workspace_bytes, void *stream);
+
+/*
+ * The kernel and grid of a call (pure host arithmetic on sizes and types; no device is
+ * needed); rows or N of 0: kernel TG_FFN_NOTHING.  tile_gemm_gated's with the workspace
+ * that its query asks for, tile_gemm_adapters' the product with W.
+ */
+typedef enum {
+    TG_FFN_NOTHING = 0,
+    TG_FFN_STREAM = 1,         /* weights streamed to registers */
+    TG_FFN_TILES = 2           /* block tiles through LDS */
+} tg_ffn_kernel;
+
+typedef struct {
+    int kernel;                /* tg_ffn_kernel */
+    int tile_m, tile_n;        /* rows and columns of the result a workgroup holds */
+    int pieces;                /* 1: short last tile rows and part-filled rounds in quarters of the tile */
+    int pipeline;              /* tiles: 1: fragments a K tile ahead in registers */
+    int waves;                 /* of a workgroup */
+    int splits;                /* of K over workgroups, whose sums a second launch adds (1: none) */
+    int pad_;
+    int64_t workgroups;
+} tg_ffn_plan_info;
+
+tg_status tile_gemm_gated_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed,
+                               tg_ffn_plan_info *out);
+tg_status tile_gemm_gated_grad_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed,
+                                    tg_ffn_plan_info *out);
+tg_status tile_gemm_adapters_plan(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, tg_dtype dtype,
+                                  int transposed, tg_ffn_plan_info *out);
 
 #ifdef __cplusplus
 }

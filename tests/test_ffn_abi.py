@@ -47,7 +47,10 @@ ADAPT = dict(adapters=4, rows=64, N=32, K=48, rank=8, dtype=1, X=P[0], ldx=48, W
 WGRAD = dict(adapters=4, rows=64, N=32, K=48, rank=8, dtype=1, X=P[0], ldx=48, dY=P[1], ldy=32, T=P[2], ldt=8, dT=P[3],
              lddt=8, dA=P[4], lda=8, strideA=384, dB=P[5], ldb=32, strideB=256, transposed=0, c_dtype=0, offsets=P[6],
              order=P[7], workspace=P[8], workspace_bytes=1 << 30, stream=0)
-ALL = [("tile_gemm_gated", GATED), ("tile_gemm_gated_grad", GRAD), ("tile_gemm_adapters", ADAPT),
+GATE = dict(rows=64, N=32, dtype=1, activation=3, U=P[0], V=P[0] + 64, ldu=64, H=P[1], ldh=32, stream=0)
+GATE_GRAD = dict(rows=64, N=32, dtype=1, activation=3, D=P[0], ldd=32, U=P[1], V=P[1] + 64, ldu=64, dU=P[2], dV=P[2] + 64,
+                 lddu=64, H=P[3], ldh=32, stream=0)
+ALL = [("tile_gemm_gate", GATE), ("tile_gemm_gate_grad", GATE_GRAD), ("tile_gemm_gated", GATED), ("tile_gemm_gated_grad", GRAD), ("tile_gemm_adapters", ADAPT),
        ("tile_gemm_adapters_wgrad", WGRAD)]
 
 
@@ -63,7 +66,7 @@ def test_valid_arguments_only_lack_the_device(fn, base):
     ("tile_gemm_gated", GATED, dict(B_up=P[1])), ("tile_gemm_gated", GATED, dict(V=P[10], ldu=32)),
     ("tile_gemm_gated", GATED, dict(transposed=1, B_up=P[1] + 32 * 48 * 2, ldb=48)),
     ("tile_gemm_gated", GATED, dict(workspace=P[0], workspace_bytes=0)),        # too small: not used, so not looked at
-    ("tile_gemm_gated_grad", GRAD, dict(H=None)), ("tile_gemm_gated_grad", GRAD, dict(dV=P[10], lddu=33)),
+    ("tile_gemm_gated_grad", GRAD, dict(H=None)), ("tile_gemm_gate_grad", GATE_GRAD, dict(H=None)), ("tile_gemm_gated_grad", GRAD, dict(dV=P[10], lddu=33)),
     ("tile_gemm_adapters", ADAPT, dict(order=None, scales=None, T=None)), ("tile_gemm_adapters", ADAPT, dict(rank=0)),
     ("tile_gemm_adapters", ADAPT, dict(transposed=1, ldw=48, lda=48, ldb=8)),
     ("tile_gemm_adapters_wgrad", WGRAD, dict(transposed=1, lda=48, ldb=8)),
@@ -88,6 +91,13 @@ REFUSED = [
         dict(D=None), dict(B=None), dict(U=None), dict(V=None), dict(dU=None), dict(dV=None), dict(ldd=47), dict(ldb=47),
         dict(ldu=31), dict(lddu=31), dict(ldh=31), dict(strideB=-1), dict(dU=P[2], dV=P[2] + 64), dict(dV=P[3] + 62),
         dict(H=P[0]), dict(H=P[2]), dict(H=P[3]), dict(H=P[5]), dict(dU=P[0]), dict(dV=P[1]), dict(D=P[0] + 1)]),
+    ("tile_gemm_gate", GATE, [
+        dict(rows=-1), dict(N=-1), dict(dtype=3), dict(activation=4), dict(U=None), dict(V=None), dict(H=None), dict(ldu=31),
+        dict(ldh=31), dict(H=P[0]), dict(H=P[0] + 64), dict(U=P[0] + 1)]),
+    ("tile_gemm_gate_grad", GATE_GRAD, [
+        dict(rows=-1), dict(N=-1), dict(dtype=-1), dict(activation=-1), dict(D=None), dict(U=None), dict(V=None), dict(dU=None),
+        dict(dV=None), dict(ldd=31), dict(ldu=31), dict(lddu=31), dict(ldh=31), dict(dU=P[0]), dict(dV=P[1]), dict(H=P[2]),
+        dict(dV=P[2] + 32), dict(H=P[0]), dict(D=P[0] + 1)]),
     ("tile_gemm_adapters", ADAPT, [
         dict(adapters=0), dict(rows=-1), dict(N=-1), dict(K=-1), dict(rank=-1), dict(dtype=3), dict(transposed=2),
         dict(X=None), dict(W=None), dict(A=None), dict(B=None), dict(Y=None), dict(offsets=None), dict(workspace=None),
@@ -120,7 +130,8 @@ def test_invalid_arguments(fn, base, kw):
     ("tile_gemm_adapters", ADAPT, dict(adapters=2049)), ("tile_gemm_adapters", ADAPT, dict(ldx=1 << 22)),
     ("tile_gemm_adapters", ADAPT, dict(ldw=1 << 22)), ("tile_gemm_adapters", ADAPT, dict(ldy=1 << 22)),
     ("tile_gemm_adapters", ADAPT, dict(rows=1 << 14, ldx=1 << 16)),                         # with an order: 2^31 bytes of x
-    ("tile_gemm_adapters_wgrad", WGRAD, dict(adapters=2049)),
+    ("tile_gemm_adapters_wgrad", WGRAD, dict(adapters=2049)), ("tile_gemm_gate", GATE, dict(ldu=1 << 22)),
+    ("tile_gemm_gate_grad", GATE_GRAD, dict(rows=(1 << 30) + 1)),
 ], ids=lambda v: str(v) if isinstance(v, dict) and len(v) < 4 else "")
 def test_unsupported(fn, base, kw):
     assert call(fn, base, **kw) == UNSUPPORTED
@@ -129,7 +140,8 @@ def test_unsupported(fn, base, kw):
 @pytest.mark.parametrize("fn,base,kw", [
     ("tile_gemm_gated", GATED, dict(rows=0, A=None, H=None, U=None, V=None)), ("tile_gemm_gated", GATED, dict(N=0)),
     ("tile_gemm_gated_grad", GRAD, dict(rows=0, D=None, U=None, V=None, dU=None, dV=None, H=None)),
-    ("tile_gemm_gated_grad", GRAD, dict(N=0)),
+    ("tile_gemm_gated_grad", GRAD, dict(N=0)), ("tile_gemm_gate", GATE, dict(rows=0, U=None, V=None, H=None)),
+    ("tile_gemm_gate_grad", GATE_GRAD, dict(N=0)),
     ("tile_gemm_adapters", ADAPT, dict(rows=0, X=None, Y=None, T=None, offsets=None, workspace=None)),
     ("tile_gemm_adapters", ADAPT, dict(N=0)), ("tile_gemm_adapters_wgrad", WGRAD, dict(rank=0)),
     ("tile_gemm_adapters_wgrad", WGRAD, dict(N=0, K=0)),

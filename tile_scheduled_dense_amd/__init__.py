@@ -58,7 +58,8 @@ EXPORTED_EXPERTS = ["tile_gemm_experts_version", "tile_gemm_expert_sort_workspac
 # every symbol include/tile_gemm_ffn.h declares
 EXPORTED_FFN = ["tile_gemm_ffn_version", "tile_gemm_gated_workspace_size", "tile_gemm_gated", "tile_gemm_gated_grad",
                 "tile_gemm_adapters_workspace_size", "tile_gemm_adapters", "tile_gemm_adapters_wgrad_workspace_size",
-                "tile_gemm_adapters_wgrad"]
+                "tile_gemm_adapters_wgrad", "tile_gemm_gated_plan", "tile_gemm_gated_grad_plan",
+                "tile_gemm_adapters_plan", "tile_gemm_gate", "tile_gemm_gate_grad"]
 FFN_VERSION = 1         # TILE_GEMM_FFN_VERSION
 EXPERTS_VERSION = 2     # TILE_GEMM_EXPERTS_VERSION
 MAX_EXPERTS = 2048      # TILE_GEMM_MAX_EXPERTS
@@ -112,6 +113,16 @@ class ExpertsPlanInfo(ctypes.Structure):
     def as_dict(self):
         d = {f: getattr(self, f) for f, _ in self._fields_ if f != "pad_"}
         d["kernel"] = EXPERTS_KERNELS[self.kernel]
+        return d
+
+
+class FfnPlanInfo(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("kernel", "tile_m", "tile_n", "pieces", "pipeline", "waves", "splits",
+                                            "pad_")] + [("workgroups", ctypes.c_int64)]
+
+    def as_dict(self):
+        d = {f: getattr(self, f) for f, _ in self._fields_ if f != "pad_"}
+        d["kernel"] = EXPERTS_KERNELS[self.kernel]      # tg_ffn_kernel: the first three of tg_experts_kernel
         return d
 
 
@@ -212,14 +223,19 @@ def _declare_experts(lib, i64, vp, ci):
 
 def _declare_ffn(lib, i64, vp, ci):
     """Argument types of the operators of a feed-forward block (include/tile_gemm_ffn.h)."""
-    size = ctypes.POINTER(i64)
+    size, info = ctypes.POINTER(i64), ctypes.POINTER(FfnPlanInfo)
     for name, args in {
         "tile_gemm_ffn_version": [],
+        "tile_gemm_gated_plan": [i64, i64, i64, i64, ci, ci, info],
+        "tile_gemm_gated_grad_plan": [i64, i64, i64, i64, ci, ci, info],
+        "tile_gemm_adapters_plan": [i64, i64, i64, i64, i64, ci, ci, info],
         "tile_gemm_gated_workspace_size": [i64, i64, i64, i64, ci, ci, size],
         "tile_gemm_gated": [i64, i64, i64, i64, ci, vp, i64, vp, vp, i64, i64, ci, ci, vp, i64, vp, vp, i64, vp, vp, i64,
                             vp],
         "tile_gemm_gated_grad": [i64, i64, i64, i64, ci, vp, i64, vp, i64, i64, ci, ci, vp, vp, i64, vp, vp, i64, vp, i64,
                                  vp, vp],
+        "tile_gemm_gate": [i64, i64, ci, ci, vp, vp, i64, vp, i64, vp],
+        "tile_gemm_gate_grad": [i64, i64, ci, ci, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp],
         "tile_gemm_adapters_workspace_size": [i64, i64, i64, i64, i64, ci, ci, size],
         "tile_gemm_adapters": [i64, i64, i64, i64, i64, ci, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, ci, vp, vp, i64,
                                vp, i64, vp, vp, vp, i64, vp],
@@ -524,6 +540,19 @@ def tile_gemm_gated_grad(experts, rows, N, K, dtype, D, ldd, B, ldb, strideB, U,
                                        lddu, _addr(H), ldh, _addr(offsets), _stream(stream)), "tile_gemm_gated_grad")
 
 
+def tile_gemm_gate(rows, N, dtype, U, V, ldu, H, ldh, activation=ACT_SILU, stream=None) -> None:
+    """H = act(U) * V, of rows that another product gave."""
+    _check(_lib().tile_gemm_gate(rows, N, _dtype(dtype), int(activation), _addr(U), _addr(V), ldu, _addr(H), ldh,
+                                 _stream(stream)), "tile_gemm_gate")
+
+
+def tile_gemm_gate_grad(rows, N, dtype, D, ldd, U, V, ldu, dU, dV, lddu, activation=ACT_SILU, H=None, ldh=0,
+                        stream=None) -> None:
+    """dU = D * V * act'(U), dV = D * act(U), and H = act(U) * V if given, from the gradient D of H."""
+    _check(_lib().tile_gemm_gate_grad(rows, N, _dtype(dtype), int(activation), _addr(D), ldd, _addr(U), _addr(V), ldu,
+                                      _addr(dU), _addr(dV), lddu, _addr(H), ldh, _stream(stream)), "tile_gemm_gate_grad")
+
+
 def tile_gemm_adapters_workspace_size(adapters, rows, N, K, rank, dtype, transposed=0) -> int:
     """Bytes of workspace that tile_gemm_adapters needs."""
     return _size("tile_gemm_adapters_workspace_size", adapters, rows, N, K, rank, _dtype(dtype), int(transposed))
@@ -561,6 +590,27 @@ def tile_gemm_adapters_wgrad(adapters, rows, N, K, rank, dtype, X, ldx, dY, ldy,
                                            strideB, int(transposed), _dtype(c_dtype), _addr(offsets), _addr(order),
                                            _addr(workspace), workspace_bytes, _stream(stream)),
            "tile_gemm_adapters_wgrad")
+
+
+def _ffn_plan(fn, *args) -> dict:
+    info = FfnPlanInfo()
+    _check(getattr(_lib(), fn)(*args, ctypes.byref(info)), fn)
+    return info.as_dict()
+
+
+def tile_gemm_gated_plan(experts, rows, N, K, dtype, transposed=0) -> dict:
+    """The kernel ("stream", "tiles") and grid of a tile_gemm_gated call with its workspace."""
+    return _ffn_plan("tile_gemm_gated_plan", experts, rows, N, K, _dtype(dtype), int(transposed))
+
+
+def tile_gemm_gated_grad_plan(experts, rows, N, K, dtype, transposed=0) -> dict:
+    """The kernel and grid of a tile_gemm_gated_grad call."""
+    return _ffn_plan("tile_gemm_gated_grad_plan", experts, rows, N, K, _dtype(dtype), int(transposed))
+
+
+def tile_gemm_adapters_plan(adapters, rows, N, K, rank, dtype, transposed=0) -> dict:
+    """The kernel and grid of the product with W of a tile_gemm_adapters call."""
+    return _ffn_plan("tile_gemm_adapters_plan", adapters, rows, N, K, rank, _dtype(dtype), int(transposed))
 
 
 def make_layout(shape, shard, replica=(), offset=None, swizzle=None) -> Layout:

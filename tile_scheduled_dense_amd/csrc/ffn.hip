@@ -59,18 +59,48 @@ Range table(const int32_t *p, int64_t n) { return p ? span(p, 1, 1, n, 0, 0, 4) 
 
 bool past_caches(int64_t bytes) { return bytes > (int64_t(256) << 20); }
 
+tg_status answer(const ProductPlan &plan, int splits, tg_ffn_plan_info *out) {
+    if (!plan.fits()) return TG_ERR_UNSUPPORTED;
+    *out = {};
+    out->kernel = plan.info.kernel == TG_EXPERTS_STREAM ? TG_FFN_STREAM : TG_FFN_TILES;
+    out->tile_m = plan.info.tile_m;
+    out->tile_n = plan.info.tile_n;
+    out->pieces = plan.info.pieces;
+    out->pipeline = plan.info.pipeline;
+    out->waves = plan.info.waves;
+    out->splits = splits < 1 ? 1 : splits;
+    out->workgroups = plan.info.workgroups;
+    return TG_OK;
+}
+
 // ---- the gated pair -------------------------------------------------------------------------
+GatedPlan gated_plan_of(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed) {
+    const bool t = transposed != 0;
+    return dtype == TG_F32    ? plan_gated<DT_F32>(t, experts, rows, N, K)
+           : dtype == TG_BF16 ? plan_gated<DT_BF16>(t, experts, rows, N, K)
+                              : plan_gated<DT_F16>(t, experts, rows, N, K);
+}
 tg_status gated_bytes(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed, int64_t *bytes) {
     const tg_status st = sizes(experts, rows, N, K, dtype, transposed);
     if (st != TG_OK) return st;
-    *bytes = 0;
-    if (rows == 0 || N == 0) return TG_OK;
-    const bool t = transposed != 0;
-    const GatedPlan plan = dtype == TG_F32    ? plan_gated<DT_F32>(t, experts, rows, N, K)
-                         : dtype == TG_BF16 ? plan_gated<DT_BF16>(t, experts, rows, N, K)
-                                            : plan_gated<DT_F16>(t, experts, rows, N, K);
-    *bytes = gated_workspace(plan, rows, N);
+    *bytes = rows == 0 || N == 0 ? 0 : gated_workspace(gated_plan_of(experts, rows, N, K, dtype, transposed), rows, N);
     return TG_OK;
+}
+tg_status gated_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed, bool grad,
+                     tg_ffn_plan_info *out) {
+    const tg_status st = sizes(experts, rows, N, K, dtype, transposed);
+    if (st == TG_ERR_INVALID_ARG || !out) return TG_ERR_INVALID_ARG;
+    if (st != TG_OK) return st;
+    *out = {};
+    if (rows == 0 || N == 0) return TG_OK;
+    if (grad) {
+        const bool t = transposed != 0;
+        return answer(dtype == TG_F32    ? plan_gate_grad<DT_F32>(t, experts, rows, N, K)
+                      : dtype == TG_BF16 ? plan_gate_grad<DT_BF16>(t, experts, rows, N, K)
+                                         : plan_gate_grad<DT_F16>(t, experts, rows, N, K), 1, out);
+    }
+    const GatedPlan plan = gated_plan_of(experts, rows, N, K, dtype, transposed);
+    return answer(plan.product, plan.splits, out);
 }
 
 tg_status gated(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, const void *A, int64_t lda,
@@ -189,6 +219,50 @@ tg_status gated_grad(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dty
     return TG_ERR_INTERNAL;
 }
 
+// grad: D, dU, dV are there, and H may be NULL
+tg_status gate(bool grad, int64_t rows, int64_t N, tg_dtype dtype, int activation, const void *D, int64_t ldd, const void *U,
+               const void *V, int64_t ldu, void *dU, void *dV, int64_t lddu, void *H, int64_t ldh, void *stream) {
+    tg_status st = sizes(1, rows, N, 0, dtype, 0);
+    if (st == TG_ERR_INVALID_ARG || activation < 0 || activation >= GATE_COUNT) return TG_ERR_INVALID_ARG;
+    if (st != TG_OK) return st;
+    const int esz = size_of(dtype);
+    if (!operand_ok(U, rows, N, ldu, esz) || !operand_ok(V, rows, N, ldu, esz) ||
+        ((!grad || H) && !operand_ok(H, rows, N, ldh, esz)) ||
+        (grad && (!operand_ok(D, rows, N, ldd, esz) || !operand_ok(dU, rows, N, lddu, esz) || !operand_ok(dV, rows, N, lddu, esz))))
+        return TG_ERR_INVALID_ARG;
+    if (rows == 0 || N == 0) return TG_OK;
+    auto range = [&](const void *p, int64_t ld) { return p ? span(p, 1, rows, N, ld, 0, esz) : Range{0, 0}; };
+    const Range out[3] = {range(dU, lddu), range(dV, lddu), range(H, ldh)};
+    const Range in[3] = {range(D, ldd), range(U, ldu), range(V, ldu)};
+    if (!none_overlap(out, 3, in, 3, false) || (grad && !side_by_side(dU, dV, rows, N, lddu, esz))) return TG_ERR_INVALID_ARG;
+    if (!tile_fits(ldu, esz) || (grad && (!tile_fits(ldd, esz) || !tile_fits(lddu, esz))) || (H && !tile_fits(ldh, esz)))
+        return TG_ERR_UNSUPPORTED;
+    st = device_ok();
+    if (st != TG_OK) return st;
+    GatedParams p = {};
+    p.A = static_cast<const char *>(D);
+    p.U = const_cast<char *>(static_cast<const char *>(U));
+    p.V = const_cast<char *>(static_cast<const char *>(V));
+    p.dU = static_cast<char *>(dU);
+    p.dV = static_cast<char *>(dV);
+    p.C = static_cast<char *>(H);
+    p.lda = ldd;
+    p.ldu = ldu;
+    p.lddu = lddu;
+    p.ldc = ldh;
+    p.rows = (int)rows;
+    p.N = (int)N;
+    p.act = activation;
+    p.past = past_caches(rows * N * (grad ? (H ? 6 : 5) : 3) * esz);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    switch (dtype) {
+        case TG_F32: return launch_gate<DT_F32>(p, grad, s);
+        case TG_BF16: return launch_gate<DT_BF16>(p, grad, s);
+        case TG_F16: return launch_gate<DT_F16>(p, grad, s);
+    }
+    return TG_ERR_INTERNAL;
+}
+
 // ---- adapters ---------------------------------------------------------------------------------
 tg_status adapter_plan(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, tg_dtype dtype, int transposed,
                        AdapterPlan &plan) {
@@ -270,6 +344,16 @@ tg_status adapters(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t
         case TG_F16: return launch_adapters<DT_F16>(p, transposed != 0, workspace, s);
     }
     return TG_ERR_INTERNAL;
+}
+
+tg_status adapters_plan(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, tg_dtype dtype, int transposed,
+                        tg_ffn_plan_info *out) {
+    AdapterPlan plan;
+    const tg_status st = adapter_plan(adapters, rows, N, K, rank, dtype, transposed, plan);
+    if (st == TG_ERR_INVALID_ARG || !out) return TG_ERR_INVALID_ARG;
+    if (st != TG_OK) return st;
+    *out = {};
+    return rows == 0 || N == 0 ? TG_OK : answer(plan.product, plan.splits, out);
 }
 
 tg_status wgrad_plan(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, tg_dtype dtype,
@@ -383,6 +467,17 @@ tg_status tile_gemm_gated_grad(int64_t experts, int64_t rows, int64_t N, int64_t
                         lddu, H, ldh, offsets, stream))
 }
 
+tg_status tile_gemm_gate(int64_t rows, int64_t N, tg_dtype dtype, int activation, const void *U, const void *V,
+                         int64_t ldu, void *H, int64_t ldh, void *stream) {
+    TG_GUARD(gate(false, rows, N, dtype, activation, nullptr, 0, U, V, ldu, nullptr, nullptr, 0, H, ldh, stream))
+}
+
+tg_status tile_gemm_gate_grad(int64_t rows, int64_t N, tg_dtype dtype, int activation, const void *D, int64_t ldd,
+                              const void *U, const void *V, int64_t ldu, void *dU, void *dV, int64_t lddu, void *H,
+                              int64_t ldh, void *stream) {
+    TG_GUARD(gate(true, rows, N, dtype, activation, D, ldd, U, V, ldu, dU, dV, lddu, H, ldh, stream))
+}
+
 tg_status tile_gemm_adapters_workspace_size(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank,
                                             tg_dtype dtype, int transposed, int64_t *bytes) {
     if (!bytes) return TG_ERR_INVALID_ARG;
@@ -418,6 +513,21 @@ tg_status tile_gemm_adapters_wgrad(int64_t n_adapters, int64_t rows, int64_t N, 
                                    int64_t workspace_bytes, void *stream) {
     TG_GUARD(adapters_wgrad(n_adapters, rows, N, K, rank, dtype, X, ldx, dY, ldy, T, ldt, dT, lddt, dA, lda, strideA, dB,
                             ldb, strideB, transposed, c_dtype, offsets, order, workspace, workspace_bytes, stream))
+}
+
+tg_status tile_gemm_gated_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed,
+                               tg_ffn_plan_info *out) {
+    TG_GUARD(gated_plan(experts, rows, N, K, dtype, transposed, false, out))
+}
+
+tg_status tile_gemm_gated_grad_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed,
+                                    tg_ffn_plan_info *out) {
+    TG_GUARD(gated_plan(experts, rows, N, K, dtype, transposed, true, out))
+}
+
+tg_status tile_gemm_adapters_plan(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, tg_dtype dtype,
+                                  int transposed, tg_ffn_plan_info *out) {
+    TG_GUARD(adapters_plan(adapters, rows, N, K, rank, dtype, transposed, out))
 }
 
 }  // extern "C"

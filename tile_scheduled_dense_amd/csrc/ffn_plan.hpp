@@ -70,6 +70,11 @@ ProductPlan plan_gate_grad_as(int64_t experts, int64_t rows, int64_t N, int64_t 
     return plan_tiles(experts, rows, N, 64, cdiv(rows, 64) * cdiv(N, 128) <= 512 ? 64 : 128, false, false, 4);
 }
 
+template <int DT>
+ProductPlan plan_gate_grad(bool transposed, int64_t experts, int64_t rows, int64_t N, int64_t K) {
+    return transposed ? plan_gate_grad_as<DT, true>(experts, rows, N, K) : plan_gate_grad_as<DT, false>(experts, rows, N, K);
+}
+
 // ---- adapters -------------------------------------------------------------------------------
 // Up to so many rows a projection's columns and its adapters' share one launch, and another
 // adds them up.
@@ -117,7 +122,9 @@ AdapterPlan plan_adapters_as(int64_t adapters, int64_t rows, int64_t N, int64_t 
         if (p.product.info.tile_m < 256) {
             p.splits = few_splits(p.product.gx, 512, k_tiles, 16);
             if (p.splits > 1) p.part_bytes = round_up(p.splits * rows * N * 4, 16);
+            const bool pipeline = p.product.info.pipeline;
             p.product = plan_of(TG_EXPERTS_TILES, p.product.info.tile_m, p.product.info.tile_n, 4, p.product.gx * p.splits);
+            p.product.info.pipeline = pipeline;
         }
     }
     p.bytes = p.part_bytes + p.part_t_bytes + rows * p.ld_low * S::E;

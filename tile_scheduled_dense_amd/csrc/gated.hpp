@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include "gate.hpp"
+#include "grid.hpp"
 #include "grouped_ring.hpp"
 
 namespace tg {
@@ -454,6 +455,42 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void gate_grad_tile_kerne
     const int K = dead ? 0 : p.K;
     if (PIECES && t.piece) run_gate_grad<P, B_KS, PIPE, STAGES>(p, smem, t, A, B, K, row, dead);
     else run_gate_grad<C, B_KS, PIPE, STAGES>(p, smem, t, A, B, K, row, dead);
+}
+
+// The gate alone, on rows that another product gave (an adapted or a 4-bit one): h from u
+// and v; d_u, d_v and h from d_h (A), u and v.  A thread 16 bytes of a row; bound by memory
+// (8192 x 5632 bf16 GATE_FWD_US and GATE_GRAD_US us).
+template <int DT, bool GRAD>
+__global__ __launch_bounds__(256) void gate_kernel(GatedParams p) {
+    typedef Chunk<DT> X;
+    const int64_t chunks = (p.N + X::PER - 1) / X::PER, at = (int64_t)wide_block() * 256 + threadIdx.x, r = at / chunks;
+    if (r >= p.rows) return;
+    const int64_t c = at % chunks * X::PER;
+    const int left = p.N - (int)c;
+    X u, v, dh, h, du, dv;
+    u.load(p.U, r * p.ldu + c, left);
+    v.load(p.V, r * p.ldu + c, left);
+    if constexpr (GRAD) dh.load(p.A, r * p.lda + c, left);
+    with_act(p.act, [&](auto a) {
+#pragma unroll
+        for (int e = 0; e < X::PER; ++e) {
+            const float ue = (float)u.x[e], ve = (float)v.x[e];
+            if constexpr (GRAD) {
+                float f, d;
+                gate_both<decltype(a)::value>(ue, f, d);
+                du.x[e] = (typename X::T)((float)dh.x[e] * ve * d);
+                dv.x[e] = (typename X::T)((float)dh.x[e] * f);
+                h.x[e] = (typename X::T)(f * ve);
+            } else {
+                h.x[e] = (typename X::T)(gate_act<decltype(a)::value>(ue) * ve);
+            }
+        }
+    });
+    if constexpr (GRAD) {
+        du.store(p.dU, r * p.lddu + c, left, p.past);
+        dv.store(p.dV, r * p.lddu + c, left, p.past);
+    }
+    if (!GRAD || p.C) h.store(p.C, r * p.ldc + c, left, p.past);
 }
 
 }  // namespace tg

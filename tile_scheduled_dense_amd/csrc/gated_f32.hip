@@ -5,5 +5,6 @@ namespace tg {
 
 template tg_status launch_gated<DT_F32>(const GatedParams &p, bool transposed, void *workspace, hipStream_t s);
 template tg_status launch_gate_grad<DT_F32>(const GatedParams &p, bool transposed, hipStream_t s);
+template tg_status launch_gate<DT_F32>(const GatedParams &p, bool grad, hipStream_t s);
 
 }  // namespace tg

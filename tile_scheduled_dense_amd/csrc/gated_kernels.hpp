@@ -90,4 +90,13 @@ tg_status launch_gate_grad(const GatedParams &p, bool transposed, hipStream_t s)
     return transposed ? launch_gate_grad_as<DT, true>(p, s) : launch_gate_grad_as<DT, false>(p, s);
 }
 
+template <int DT>
+tg_status launch_gate(const GatedParams &p, bool grad, hipStream_t s) {
+    const int64_t blocks = cdiv((int64_t)p.rows * cdiv(p.N, Chunk<DT>::PER), 256);
+    if (blocks > kGridX * 65535) return TG_ERR_UNSUPPORTED;
+    if (grad) hipLaunchKernelGGL((gate_kernel<DT, true>), wide_grid(blocks), dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((gate_kernel<DT, false>), wide_grid(blocks), dim3(256), 0, s, p);
+    return launched();
+}
+
 }  // namespace tg
