@@ -42,10 +42,14 @@ ADAPTERS = [
     (dict(tile_m=256, pieces=1, pipeline=1), "bf16", 1, 4096, 0, 2048, 1056, 100, 0, 0, 1),
     (dict(tile_m=128, splits=1), "f16", 9, 4100, 33, 1100, 264, 8, 0, 0, 0),
     (dict(tile_m=128, splits=1), "bf16", 3, 5000, 0, 1001, 131, 33, 1, 1, 1),
-    (dict(tile_m=128, splits=2), "bf16", 7, 300, 20, 520, 1100, 24, 0, 0, 1),
-    (dict(tile_m=128, splits=4), "f16", 150, 260, 0, 300, 2050, 7, 1, 0, 0),
+    (dict(tile_m=64, splits=4), "bf16", 7, 300, 20, 520, 1100, 24, 0, 0, 1),
+    (dict(tile_m=64, splits=8), "f16", 150, 260, 0, 300, 2050, 7, 1, 0, 0),
+    (dict(tile_m=64, splits=1), "f16", 30, 512, 9, 1536, 520, 17, 0, 1, 1),
+    (dict(tile_m=128, splits=4), "bf16", 7, 1025, 20, 520, 2100, 24, 0, 0, 1),
+    (dict(tile_m=128, splits=8), "f16", 150, 1060, 0, 300, 4106, 7, 1, 0, 0),
     (dict(tile_m=64, splits=1, pipeline=1), "f32", 41, 1333, 21, 771, 201, 5, 0, 0, 0),
-    (dict(tile_m=64, splits=2, pipeline=1), "f32", 6, 300, 3, 264, 520, 20, 1, 1, 1),
+    (dict(tile_m=64, splits=4, pipeline=0), "f32", 6, 300, 3, 264, 520, 20, 1, 1, 1),
+    (dict(tile_m=64, splits=4, pipeline=1), "f32", 6, 1300, 3, 264, 1030, 20, 1, 1, 1),
     (dict(kernel="tiles", tile_m=64, splits=4), "bf16", 20, 64, 7, 512, 1024, 32, 0, 0, 1),
     (dict(kernel="tiles", tile_m=64, splits=4), "f32", 5, 40, 0, 300, 520, 9, 1, 0, 0),
     (dict(kernel="stream", splits=8), "bf16", 3, 7, 1, 300, 4104, 16, 0, 0, 1),

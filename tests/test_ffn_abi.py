@@ -44,7 +44,7 @@ GRAD = dict(experts=4, rows=64, N=32, K=48, dtype=1, D=P[0], ldd=48, B=P[1], ldb
 ADAPT = dict(adapters=4, rows=64, N=32, K=48, rank=8, dtype=1, X=P[0], ldx=48, W=P[1], ldw=32, A=P[2], lda=8, strideA=384,
              B=P[3], ldb=32, strideB=256, transposed=0, scales=P[4], Y=P[5], ldy=32, T=P[6], ldt=8, offsets=P[7],
              order=P[8], workspace=P[9], workspace_bytes=1 << 30, stream=0)
-WGRAD = dict(adapters=4, rows=64, N=32, K=48, rank=8, dtype=1, X=P[0], ldx=48, dY=P[1], ldy=32, T=P[2], ldt=8, dT=P[3],
+WGRAD = dict(adapters=4, rows=300, N=32, K=48, rank=8, dtype=1, X=P[0], ldx=48, dY=P[1], ldy=32, T=P[2], ldt=8, dT=P[3],
              lddt=8, dA=P[4], lda=8, strideA=384, dB=P[5], ldb=32, strideB=256, transposed=0, c_dtype=0, offsets=P[6],
              order=P[7], workspace=P[8], workspace_bytes=1 << 30, stream=0)
 GATE = dict(rows=64, N=32, dtype=1, activation=3, U=P[0], V=P[0] + 64, ldu=64, H=P[1], ldh=32, stream=0)
@@ -70,6 +70,7 @@ def test_valid_arguments_only_lack_the_device(fn, base):
     ("tile_gemm_adapters", ADAPT, dict(order=None, scales=None, T=None)), ("tile_gemm_adapters", ADAPT, dict(rank=0)),
     ("tile_gemm_adapters", ADAPT, dict(transposed=1, ldw=48, lda=48, ldb=8)),
     ("tile_gemm_adapters_wgrad", WGRAD, dict(transposed=1, lda=48, ldb=8)),
+    ("tile_gemm_adapters_wgrad", WGRAD, dict(rows=256, workspace=None, workspace_bytes=0)),     # no sums to add up
     ("tile_gemm_adapters_wgrad", WGRAD, dict(rows=0)), ("tile_gemm_adapters_wgrad", WGRAD, dict(order=None, c_dtype=1)),
 ], ids=lambda v: str(v) if isinstance(v, dict) and len(v) < 6 else "")
 def test_forms_that_are_taken(fn, base, kw):

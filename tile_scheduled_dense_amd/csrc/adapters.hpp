@@ -8,17 +8,23 @@
 // adapter g has the positions offsets[g] .. offsets[g + 1], and those behind the last
 // adapter's have none.
 //
-//  * Few rows (the bytes of W): one launch sums x . W (its columns in strips, K split over
-//    workgroups) and x . A[g] (16 positions of one adapter a workgroup, K split) into fp32
-//    partial sums, a second one adds them and t . B[g].
-//  * Many rows: t first (16 positions a workgroup, rounded once to the inputs' type: it
-//    is the second product's operand), then the block tiles of grouped_ring.hpp over
-//    positions, whose contraction goes on through t and the B[g] of every adapter that
-//    has positions in the tile, the others' rows of t being zeros.
-//  * Gradients: 16-bit and fp32 products whose contraction is an adapter's rows, the wide
-//    operand straight from memory to registers, the narrow one transposed in LDS; a
-//    workgroup takes a chunk of an adapter's rows, a second launch adds the chunks in
-//    their order.
+//  * Few rows (the bytes of W; adapters_few): one launch sums x . W (K split over workgroups) and
+//    x . A[g] (16 positions of one adapter a workgroup, K split) into fp32 partial sums, a
+//    second one adds them and t . B[g] position by position.
+//  * More rows: t first (64 positions of one adapter a workgroup, K split, then added up and
+//    rounded once to the inputs' type: it is the second product's operand), then the
+//    block tiles of grouped_ring.hpp over positions, whose contraction goes on through
+//    t and the B[g] of every adapter that has positions in the tile, the others' rows of t
+//    being zeros.  Tiles that mix adapters keep W's product as dense as without any.
+//  * Gradients: products whose contraction is an adapter's rows, the wide operand
+//    straight from memory to registers, the narrow one transposed in LDS; a workgroup takes a
+//    chunk of an adapter's rows, a second launch adds the chunks in their order.
+//
+// Measured, inputs that change from call to call: 1 row, rank 16, 4096 x 4096 bf16 12.9 us
+// (33.8 MB; the sums 9, the join 3.5); 64 rows of 20 adapters of rank 32 16.7 us (12 and 5.6); 8192
+// rows, 4 adapters of rank 64, 4096 x 4096 f16 252 us, of which t is 28 (x from HBM while the last
+// results go there) and the product 222 (1270 TFLOP/s); gradients of two adapters of rank
+// 16, 8192 rows of 2048 and 4096, 27 us (100 MB, 3.7 TB/s) and 6 to add up.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -559,8 +565,10 @@ __global__ __launch_bounds__(256) void adapters_sum_kernel(AdapterParams p) {
 // takes kChunk positions of one adapter and a strip of L's columns a wave: stages of L as
 // StreamB loads a matrix (32 rows by 128 columns, fp32 64), transposed in registers, the
 // next one's loads in flight during the current one's products; S's rows of the chunk lie
-// transposed in LDS, 16 JT of the rank.  fp32 sums, rank x M of each chunk, go to the
-// workspace.  Bound by the bytes of L.
+// transposed in LDS, 16 JT of the rank.  An adapter of one chunk gets its result at once;
+// else fp32 sums, rank x M of each chunk, go to the workspace: an adapter's first to place
+// offsets[g] / kChunk (no other adapter of several chunks starts there), the further ones
+// to their slots behind all of those.  Bound by the bytes of L.
 constexpr int kChunk = 256;
 constexpr int kWgradRank = 64;        // of the rank at a time
 
@@ -571,11 +579,32 @@ struct AdapterGradParams {
     int64_t ldl[2], lds[2], ldc[2], sC[2];
     int M[2];
     int wide_first[2];                 // C is M x rank (1) or rank x M (0)
-    float *part[2];                    // [workgroup of kChunk][rank][M]
+    float *part[2];                    // [first chunks, then further ones][rank][M]
     const int32_t *offsets, *order;
     int adapters, rows, rank, c_f32;
     int strips[2], slots, rank_tiles;
 };
+
+// Four neighbours m .. m + 3 (left of them exist) of rank j of C[g].
+template <int DT>
+__device__ __forceinline__ void wgrad_store(const AdapterGradParams &p, int job, int g, int j, int m, int left, const f32x4 &x) {
+    typedef typename ElemOf<DT>::type T;
+    const int64_t at = (int64_t)g * p.sC[job], ld = p.ldc[job];
+    const bool f32 = DT == DT_F32 || p.c_f32;
+    if (!p.wide_first[job]) {
+        const int64_t to = at + j * ld + m;
+        const bool wide = ld % 4 == 0 && p.sC[job] % 4 == 0 && reinterpret_cast<uintptr_t>(p.C[job]) % (f32 ? 16 : 8) == 0;
+        store4<DT>(p.C[job], to, left, p.c_f32, wide, x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (e >= left) continue;
+            const int64_t to = at + (m + e) * ld + j;
+            if (f32) reinterpret_cast<float *>(p.C[job])[to] = x[e];
+            else reinterpret_cast<T *>(p.C[job])[to] = (T)x[e];
+        }
+    }
+}
 
 template <int DT, int JT>
 __global__ __launch_bounds__(256) void adapters_wgrad_kernel(AdapterGradParams p) {
@@ -671,7 +700,6 @@ __global__ __launch_bounds__(256) void adapters_wgrad_kernel(AdapterGradParams p
             multiply(k0, q0);
             k0 += Sh::K;
             if (!more) break;
-#pragma unroll
             for (int i = 0; i < 8; ++i) q0[i] = q1[i];
         }
     }
@@ -681,8 +709,11 @@ __global__ __launch_bounds__(256) void adapters_wgrad_kernel(AdapterGradParams p
         multiply(k0, q);
     }
     // a lane holds, of rank j, the columns PER * (4 grp + v) + fragment: PER x 4 neighbours
-    float *part = p.part[job] + ((int64_t)block * p.rank + j0) * p.M[job];
-    const bool wide = p.M[job] % 4 == 0;
+    const int M = p.M[job], further = block - (p.adapters + 1);
+    const RowSpan all = rows_of(p.offsets, g, p.adapters, p.rows);
+    const bool alone = all.hi - all.lo <= kChunk, wide = M % 4 == 0;
+    const int place = further < 0 ? all.lo / kChunk : (p.rows - 1) / kChunk + 1 + further;
+    char *part = reinterpret_cast<char *>(p.part[job] + ((int64_t)place * p.rank + j0) * M);
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
         if (16 * j + c >= ranks) continue;
@@ -690,16 +721,17 @@ __global__ __launch_bounds__(256) void adapters_wgrad_kernel(AdapterGradParams p
         for (int v = 0; v < 4; ++v)
 #pragma unroll
             for (int f = 0; f < Sh::FRAGS; f += 4) {
-                const int m = m0 + PER * (4 * grp + v) + f, n = p.M[job] - m;
+                const int m = m0 + PER * (4 * grp + v) + f, n = M - m;
                 const f32x4 x = {acc[j][f][v], acc[j][f + 1][v], acc[j][f + 2][v], acc[j][f + 3][v]};
-                if (n > 0)
-                    store4<DT_F32>(reinterpret_cast<char *>(part), (int64_t)(16 * j + c) * p.M[job] + m, n, true, wide, x);
+                if (n <= 0) continue;
+                if (alone) wgrad_store<DT>(p, job, g, j0 + 16 * j + c, m, n, x);
+                else store4<DT_F32>(part, (int64_t)(16 * j + c) * M + m, n, true, wide, x);
             }
     }
 }
 
-// C[g] from the chunks' sums, in their order; a thread an element, threads along M (the
-// sums' rows), zeros for an adapter without a row.
+// C[g] from the chunks' sums, in their order, for an adapter of several, and zeros for one
+// without a row; a thread an element, threads along M (the sums' rows).
 template <int DT>
 __global__ __launch_bounds__(256) void adapters_wgrad_join_kernel(AdapterGradParams p) {
     typedef typename ElemOf<DT>::type T;
@@ -708,11 +740,15 @@ __global__ __launch_bounds__(256) void adapters_wgrad_join_kernel(AdapterGradPar
     if (at >= n) return;
     const int j = (int)(at / M), m = (int)(at % M);
     const RowSpan s = rows_of(p.offsets, g, p.adapters, p.rows);
-    const int tiles = (s.hi - s.lo + kChunk - 1) / kChunk;
-    const float *part = p.part[job] + at, *next = part + (int64_t)(p.adapters + s.lo / kChunk) * n;
-    float sum = tiles > 0 ? part[g * n] : 0.0f;
+    const int tiles = (s.hi - s.lo + kChunk - 1) / kChunk, first = s.lo / kChunk;
+    if (tiles == 1) return;
+    float sum = 0;
+    if (tiles > 1) {
+        const float *part = p.part[job] + at, *next = part + (int64_t)((p.rows - 1) / kChunk + 1 + first) * n;
+        sum = part[first * n];
 #pragma unroll 8
-    for (int k = 1; k < tiles; ++k) sum += next[k * n];
+        for (int k = 0; k < tiles - 1; ++k) sum += next[k * n];
+    }
     const int64_t to = (int64_t)g * p.sC[job] + (p.wide_first[job] ? m * p.ldc[job] + j : j * p.ldc[job] + m);
     if (DT == DT_F32 || p.c_f32) reinterpret_cast<float *>(p.C[job])[to] = sum;
     else reinterpret_cast<T *>(p.C[job])[to] = (T)sum;

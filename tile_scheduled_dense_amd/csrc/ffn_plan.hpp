@@ -22,6 +22,21 @@ inline int few_splits(int64_t groups, int64_t enough, int64_t stages, int64_t le
 }
 
 // ---- the gated pair -----------------------------------------------------------------------
+// Which kernel, by rows of an expert on average, and what the other one takes:
+//  * Streamed weights, both strips of a column in a workgroup of up to 8 waves along K: up to
+//    16 rows of weights outputs x inputs (8192 x 4096 f16, 16 rows 32.0 us, tiles 37.5; 24 rows
+//    52.3 and 38.0; 2816 x 1024, 1 row 8.0 and 11.2) and in fp32 (4096 x 1024, 16 rows 12.7 and
+//    18.0; 4096 x 2048, 32 rows 38.7 and 28.7); 16 bits as stored take tiles at once (8192 x
+//    4096 f16, 1 row 28.8 us on tiles, 31.6 streamed; 16 rows 30.4 and 38.3).
+//  * Tiles of 64 x 64 with K split over workgroups up to 64 rows, in 16 bits up to 128 where
+//    the strips are few (one expert of 4096 x 2048, 65 rows 15.9 us against 25.3 on 128 x 64,
+//    128 rows 18.5 and 25.0, 256 rows 25.1 and 25.0; 8 experts of 2048 x 1024, 640 rows, 256
+//    strips, 23.6 and 19.4; fp32, 640 rows 101 and 65).
+//  * The same tile, not split, in 16 bits where tiles of 128 x 64 are up to 400 (517 x 1001, 2501
+//    rows 24.2 us against 25.8; 1024 x 512 18.1 and 18.9; 8192 rows 49.4 and 45).
+//  * 256 x 128 with the pipeline where K is long and the tiles fill half the card, as the products do.
+// The splits of K go up to 256 workgroups (48 rows f16, 128, 256, 512, 1024 workgroups: 44.1, 33.8,
+// 39.8, 47.0 us; 2816 x 1024, 1 row in 1 split 8.0, in 2 10.9), none shorter than the waves' stages.
 struct GatedPlan {
     int splits;                  // of K over workgroups; 0: block tiles, which are not split
     ProductPlan product;
@@ -62,7 +77,10 @@ inline int64_t gated_workspace(const GatedPlan &p, int64_t rows, int64_t N) {
 }
 
 // The gate's gradient: the products' own rule (plan_grouped_as), but the smaller tiles of 16
-// bits are smaller still.
+// bits are smaller still, their epilogue reads and writes four matrices: 128 x 128, 64 x 128 and
+// 64 x 64 take 32.3, 25.6, 20.8 us (2501 rows of 517 x 1001), 23, 17.7, 14.8 (1024 x 512), 44,
+// 37.9, 39.0 (8192 rows); the large tiles of 256 x 256 stay (16384 rows of 8 experts of 2048 x
+// 2048 210 us, 128 x 128 234, 64 x 64 354).
 template <int DT, bool TRANS>
 ProductPlan plan_gate_grad_as(int64_t experts, int64_t rows, int64_t N, int64_t K) {
     const ProductPlan p = plan_grouped_as<DT, TRANS>(experts, rows, N, K);
@@ -76,9 +94,17 @@ ProductPlan plan_gate_grad(bool transposed, int64_t experts, int64_t rows, int64
 }
 
 // ---- adapters -------------------------------------------------------------------------------
-// Up to so many rows a projection's columns and its adapters' share one launch, and another
-// adds them up.
-constexpr int64_t kAdapterFew = 64;
+// Few rows: a projection's columns and its adapters' share one launch, and another adds them
+// up.  So up to 64 rows, and up to 512 where that makes at most 192 tiles of 64 x 64; more
+// take three launches or four (t, its join, the tiles, their join).  20 adapters of rank 16,
+// bf16, few against many: 4096 x 4096, 65 rows 23.6 and 49.6 us, 128 rows 26.2 and 52.1, 192
+// rows (192 tiles) 39.1 and 48.3; one adapter, 256 rows (256 tiles) 41.9 and 32.8; 2048 x 8192,
+// 256 rows 39.3 and 49.3; 16384 x 4096, 128 rows (512 tiles) 104 and 82; 1024 x 4096,
+// 768 rows 43.8 and 37.6; one adapter of rank 64 of 512 x 8192, 1024 rows 54.8 and 37.0; fp32
+// 4096 x 4096, 256 rows (256 tiles) 124 and 90; 771 x 1540, 512 rows (104 tiles) 59.7 and 85.0.
+inline bool adapters_few(int64_t rows, int64_t N) {
+    return rows <= 64 || N < kNarrow || (rows <= 512 && cdiv(rows, 64) * cdiv(N, 64) <= 192);
+}
 
 enum { ADAPTERS_STREAM = 0, ADAPTERS_SPLIT = 1, ADAPTERS_TILES = 2 };
 struct AdapterPlan {
@@ -90,13 +116,21 @@ struct AdapterPlan {
     ProductPlan low;             // x . A[g]
 };
 
+// Few rows: streamed weights up to 16 rows as the gated pair has them (one row of 4096 x 4096,
+// 13.1 us; as stored in 16 bits 18.1 on tiles and 18 to 21 streamed), K split up to 512 workgroups
+// (128, 256, 512: 17.8, 13.1, 13.1 us, fp32 32.9, 25.9, 19.2) of 4 waves (8 waves 13.7 to 15);
+// tiles up to 256 (64 rows, 128, 256, 512: 21.7, 17.0, 18.9 us, as stored 29.9, 24.4, 27.3), t
+// in 8 splits (4, 8, 16: 18.6, 17.2, 17.5; as stored 8 and 16 24.5 and 28.7).
+// Many: t on tiles of 64 x 64, split up to 512 workgroups (8192 rows, up to 512 252 us, 2048 259);
+// the product as the products have it, its smaller tiles split too where a half is still 16
+// tiles of K long (fp32 771 x 1540, 1333 rows, in 1, 2, 4 splits: 121, 125, 141 us).
 template <int DT, bool TRANS>
 AdapterPlan plan_adapters_as(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank) {
     using S = StreamShape<DT, TRANS>;
     AdapterPlan p = {};
     const int64_t stages = cdiv(K, S::K), k_tiles = cdiv(K, 64 / S::E);
     p.splits = p.t_splits = 1;
-    if (rows <= kAdapterFew || N < kNarrow) {
+    if (adapters_few(rows, N)) {
         const bool stream = N < kNarrow || (rows <= 16 && (TRANS || DT == DT_F32));
         const int waves = 4;
         p.form = stream ? ADAPTERS_STREAM : ADAPTERS_SPLIT;
@@ -137,21 +171,20 @@ AdapterPlan plan_adapters(bool transposed, int64_t adapters, int64_t rows, int64
 }
 
 struct AdapterGradPlan {
-    int64_t chunk, slots, rank_tiles, strips[2], workgroups, part_bytes[2], bytes;
+    int64_t slots, rank_tiles, strips[2], workgroups, part_bytes[2], bytes;
 };
-// Positions a workgroup takes: kChunk, fewer (down to 64) while there are fewer than 512
-// workgroups.
 inline AdapterGradPlan plan_adapters_wgrad(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, bool f32) {
     AdapterGradPlan p = {};
     const int64_t cols = 4 * (f32 ? StreamShape<DT_F32, false>::COLS : StreamShape<DT_F16, false>::COLS);
-    p.chunk = kChunk;
     p.slots = rows > 0 ? tiles_and_slots(rows, adapters, kChunk) : 0;
     p.rank_tiles = cdiv(rank, kWgradRank);
     p.strips[0] = cdiv(K, cols);
     p.strips[1] = cdiv(N, cols);
     p.workgroups = (p.strips[0] + p.strips[1]) * p.rank_tiles * p.slots;
-    p.part_bytes[0] = round_up(p.slots * rank * K * 4, 16);
-    p.part_bytes[1] = p.slots * rank * N * 4;
+    // an adapter's chunks are added up where it has several
+    const int64_t places = rows > kChunk ? 2 * cdiv(rows, kChunk) : 0;
+    p.part_bytes[0] = round_up(places * rank * K * 4, 16);
+    p.part_bytes[1] = places * rank * N * 4;
     p.bytes = p.part_bytes[0] + p.part_bytes[1];
     return p;
 }

@@ -1,14 +1,25 @@
-// gated.hpp -- the gated pair of projections and the gradient of its gate, for many rows:
-// block tiles on the LDS ring of grouped_ring.hpp.
+// gated.hpp -- the gated pair of projections and the gradient of its gate, on block tiles
+// and the LDS ring of grouped_ring.hpp, and the gate alone:
 //
 //   forward    u = A . Bg,  v = A . Bu,  h = act(u) * v        (U and V stored on request)
 //   gradient   d_h = D . B,  d_u = d_h * v * act'(u),  d_v = d_h * act(u),  h = act(u) * v
 //
 // Forward: a workgroup's tile holds the same columns of both products, half of its MFMA
 // column tiles each: the second operand is a pair, staged side by side, so that u and v
-// of an element are in one lane and h costs no memory.  The tile of h is half as wide
+// of an element are in one wave and h costs no memory.  The tile of h is half as wide
 // as the product's.  Gradient: the product's own tiles; u and v are read and the results
 // written where d_h would have been.
+//
+// u, v, d_u and d_v are stored in the operands' type: they are operands of the products
+// that follow (16 bits: one rounding of what the gate's gradient reads, one of what the
+// products of the backward pass read; h is of the unrounded u and v).
+//
+// Measured, bf16, inputs that change from call to call: 8192 rows, 5632 x 2048 transposed,
+// one expert, forward 323-335 us (1130-1170 TFLOP/s; a large library product 1319), bound by the
+// matrix cores; 16384 rows of 8 uneven experts of 2048 x 2048 forward with u and v stored
+// 270-285 us, of which about 30 are the stores; the gradient 200-206 us, of which the product
+// alone is 125: u and v in, d_u and d_v out are 268 MB, 55 us at the rate of a large copy,
+// and all CUs come to them at the same time.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -459,7 +470,8 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void gate_grad_tile_kerne
 
 // The gate alone, on rows that another product gave (an adapted or a 4-bit one): h from u
 // and v; d_u, d_v and h from d_h (A), u and v.  A thread 16 bytes of a row; bound by memory
-// (8192 x 5632 bf16 GATE_FWD_US and GATE_GRAD_US us).
+// (8192 x 5632 bf16 50 us,
+// 5.5 TB/s; the gradient 86 us, 5.4, with h 102).
 template <int DT, bool GRAD>
 __global__ __launch_bounds__(256) void gate_kernel(GatedParams p) {
     typedef Chunk<DT> X;
