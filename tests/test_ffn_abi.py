@@ -165,3 +165,16 @@ def test_workspace_sizes():
                 lambda: tg.tile_gemm_adapters_wgrad_workspace_size(1, 1, 8, 8, -8, "f16")):
         with pytest.raises(tg.TileGemmError):
             bad()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_workspace_that_no_memory_holds_is_refused(dt):
+    """Extents of 2^30 are taken, but not their product, which passes 64 bits."""
+    big = 1 << 30
+    for ask in (lambda: tg.tile_gemm_adapters_workspace_size(1, big, big, 64, big, dt),
+                lambda: tg.tile_gemm_adapters_workspace_size(1, big, 4, 64, big, dt),
+                lambda: tg.tile_gemm_adapters_wgrad_workspace_size(1, big, big, big, big, dt),
+                lambda: tg.tile_gemm_adapters_wgrad_workspace_size(1, big, 1 << 10, 0, big, dt)):
+        with pytest.raises(tg.TileGemmError):
+            ask()
+    assert tg.tile_gemm_adapters_workspace_size(1, 64, 1 << 20, 64, 1 << 10, dt) > 0

@@ -84,7 +84,7 @@ tg_status gated_bytes(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dt
     const tg_status st = sizes(experts, rows, N, K, dtype, transposed);
     if (st != TG_OK) return st;
     *bytes = rows == 0 || N == 0 ? 0 : gated_workspace(gated_plan_of(experts, rows, N, K, dtype, transposed), rows, N);
-    return TG_OK;
+    return *bytes < kNoMemory ? TG_OK : TG_ERR_UNSUPPORTED;
 }
 tg_status gated_plan(int64_t experts, int64_t rows, int64_t N, int64_t K, tg_dtype dtype, int transposed, bool grad,
                      tg_ffn_plan_info *out) {
@@ -276,7 +276,7 @@ tg_status adapter_plan(int64_t adapters, int64_t rows, int64_t N, int64_t K, int
     plan = dtype == TG_F32    ? plan_adapters<DT_F32>(t, adapters, rows, N, K, rank)
            : dtype == TG_BF16 ? plan_adapters<DT_BF16>(t, adapters, rows, N, K, rank)
                               : plan_adapters<DT_F16>(t, adapters, rows, N, K, rank);
-    return TG_OK;
+    return plan.bytes < kNoMemory ? TG_OK : TG_ERR_UNSUPPORTED;
 }
 
 tg_status adapters(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, tg_dtype dtype, const void *X,
@@ -363,7 +363,7 @@ tg_status wgrad_plan(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64
     if (st != TG_OK) return st;
     if (rank > kMaxExtent) return TG_ERR_UNSUPPORTED;
     plan = plan_adapters_wgrad(adapters, rows, N, K, rank, dtype == TG_F32);
-    return TG_OK;
+    return plan.bytes < kNoMemory ? TG_OK : TG_ERR_UNSUPPORTED;
 }
 
 tg_status adapters_wgrad(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, tg_dtype dtype, const void *X,

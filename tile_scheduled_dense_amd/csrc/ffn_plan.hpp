@@ -10,6 +10,14 @@
 
 namespace tg {
 
+// Bytes of a workspace's part, a multiple of 16; kNoMemory where no memory holds them (extents
+// up to 2^30 each, so that their product may pass 64 bits).
+constexpr int64_t kNoMemory = int64_t(1) << 50;
+inline int64_t part_bytes(int64_t copies, int64_t rows, int64_t cols, int64_t element) {
+    const unsigned __int128 n = (unsigned __int128)copies * rows * element * cols;
+    return n < kNoMemory - 16 ? round_up((int64_t)n, 16) : kNoMemory;
+}
+
 // Waves of a workgroup that splits K (plan_stream).
 inline int few_waves(int64_t stages) { return stages >= 16 ? 8 : (stages >= 8 ? 4 : 2); }
 
@@ -73,7 +81,7 @@ GatedPlan plan_gated(bool transposed, int64_t experts, int64_t rows, int64_t N, 
     return transposed ? plan_gated_as<DT, true>(experts, rows, N, K) : plan_gated_as<DT, false>(experts, rows, N, K);
 }
 inline int64_t gated_workspace(const GatedPlan &p, int64_t rows, int64_t N) {
-    return p.splits > 1 ? p.splits * 2 * rows * N * 4 : 0;
+    return p.splits > 1 ? part_bytes(p.splits * 2, rows, N, 4) : 0;
 }
 
 // The gate's gradient: the products' own rule (plan_grouped_as), but the smaller tiles of 16
@@ -137,8 +145,8 @@ AdapterPlan plan_adapters_as(int64_t adapters, int64_t rows, int64_t N, int64_t 
         const int64_t strips = cdiv(N, stream ? S::COLS : 64), tiles = strips * cdiv(rows, stream ? 16 : 64);
         p.splits = stream ? few_splits(tiles, 512, stages, waves) : few_splits(tiles, 256, k_tiles, 8);
         p.t_splits = few_splits(cdiv(rank, S::COLS), 8, stages, waves);
-        p.part_bytes = round_up(p.splits * rows * N * 4, 16);
-        p.part_t_bytes = round_up(p.t_splits * rows * rank * 4, 16);
+        p.part_bytes = part_bytes(p.splits, rows, N, 4);
+        p.part_t_bytes = part_bytes(p.t_splits, rows, rank, 4);
         p.product = plan_of(stream ? TG_EXPERTS_STREAM : TG_EXPERTS_TILES, stream ? 16 : 64, stream ? S::COLS : 64, waves,
                             tiles * p.splits);
         p.low = plan_of(TG_EXPERTS_STREAM, 16, S::COLS, waves,
@@ -147,7 +155,7 @@ AdapterPlan plan_adapters_as(int64_t adapters, int64_t rows, int64_t N, int64_t 
         p.form = ADAPTERS_TILES;
         p.ld_low = round_up(rank, S::PER);
         p.t_splits = few_splits(cdiv(rows, 64) * cdiv(rank, 64), 512, k_tiles, 8);
-        p.part_t_bytes = round_up(p.t_splits * rows * rank * 4, 16);
+        p.part_t_bytes = part_bytes(p.t_splits, rows, rank, 4);
         p.low = plan_of(TG_EXPERTS_TILES, 64, 64, 4, cdiv(rank, 64) * p.t_splits, tiles_and_slots(rows, adapters, 64));
         const int64_t tiles = cdiv(rows, 256) * cdiv(N, 256);
         if (DT == DT_F32) p.product = plan_tiles(1, rows, N, 64, 64, false, true, 4);
@@ -155,13 +163,13 @@ AdapterPlan plan_adapters_as(int64_t adapters, int64_t rows, int64_t N, int64_t 
         else p.product = plan_tiles(1, rows, N, 128, 128, false, false, 3);
         if (p.product.info.tile_m < 256) {
             p.splits = few_splits(p.product.gx, 512, k_tiles, 16);
-            if (p.splits > 1) p.part_bytes = round_up(p.splits * rows * N * 4, 16);
+            if (p.splits > 1) p.part_bytes = part_bytes(p.splits, rows, N, 4);
             const bool pipeline = p.product.info.pipeline;
             p.product = plan_of(TG_EXPERTS_TILES, p.product.info.tile_m, p.product.info.tile_n, 4, p.product.gx * p.splits);
             p.product.info.pipeline = pipeline;
         }
     }
-    p.bytes = p.part_bytes + p.part_t_bytes + rows * p.ld_low * S::E;
+    p.bytes = p.part_bytes + p.part_t_bytes + part_bytes(1, rows, p.ld_low, S::E);
     return p;
 }
 template <int DT>
@@ -183,8 +191,8 @@ inline AdapterGradPlan plan_adapters_wgrad(int64_t adapters, int64_t rows, int64
     p.workgroups = (p.strips[0] + p.strips[1]) * p.rank_tiles * p.slots;
     // an adapter's chunks are added up where it has several
     const int64_t places = rows > kChunk ? 2 * cdiv(rows, kChunk) : 0;
-    p.part_bytes[0] = round_up(places * rank * K * 4, 16);
-    p.part_bytes[1] = places * rank * N * 4;
+    p.part_bytes[0] = part_bytes(places, rank, K, 4);
+    p.part_bytes[1] = part_bytes(places, rank, N, 4);
     p.bytes = p.part_bytes[0] + p.part_bytes[1];
     return p;
 }
