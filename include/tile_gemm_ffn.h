@@ -93,7 +93,7 @@ tg_status tile_gemm_gate_grad(int64_t rows, int64_t N, tg_dtype dtype, int activ
 /*
  * Y[r] = X[r] . W + t[r] . B[g], t[r] = scales[g] * (X[r] . A[g]).  X: rows x K, Y: rows x N, W: K x N
  * (or N x K); A[g], B[g]: K x rank and rank x N (or rank x K and N x rank) at strideA, strideB.
- * scales: one fp32 a adapter, NULL: 1.  Adapter g has the positions offsets[g] .. offsets[g + 1] - 1
+ * scales: one fp32 an adapter, NULL: 1.  Adapter g has the positions offsets[g] .. offsets[g + 1] - 1
  * of the adapters' order, those from offsets[adapters] on have none; position p is row order[p]
  * of X, Y and T (order[p] or its complement: tile_gemm_expert_sort's entry_of_row, with one
  * choice a row, is such a table; it must hold every row once), or row p where order is NULL.  T (rows x rank, of dtype): t,

@@ -13,6 +13,10 @@ GATED = [
     (dict(tile_m=256, tile_n=128, pieces=1, pipeline=1), "f16", [100, 4000, 4090, 60], 0, 1051, 1027, 0, 1, 1),
     (dict(tile_m=128, tile_n=64, pieces=0, pipeline=0), "bf16", UNEVEN, 5, 600, 264, 0, 0, 0),
     (dict(tile_m=128, tile_n=64, pieces=0, pipeline=0), "f16", [8000], 0, 515, 131, 1, 1, 1),
+    (dict(tile_m=128, tile_n=64, pieces=0, pipeline=0), "bf16", [1300], 0, 1032, 2056, 1, 0, 0),
+    (dict(tile_m=64, tile_n=64, splits=2), "bf16", [450, 1, 0, 261], 9, 400, 2088, 1, 0, 1),
+    (dict(tile_m=64, tile_n=64, splits=2), "f16", [257], 0, 1001, 4101, 0, 1, 0),
+    (dict(tile_m=64, tile_n=64, splits=8, pipeline=0), "f32", [325], 0, 104, 2050, 0, 0, 1),
     (dict(tile_m=64, tile_n=64, splits=1), "bf16", [300, 77, 0, 900], 9, 200, 520, 0, 0, 1),
     (dict(tile_m=64, tile_n=64, splits=4), "f16", [100], 0, 1030, 1050, 0, 0, 0),
     (dict(tile_m=64, tile_n=64, splits=2), "bf16", [30, 41, 0, 7], 3, 264, 600, 1, 0, 1),
@@ -31,6 +35,7 @@ GRAD = [
     (dict(tile_m=64, tile_n=128), "bf16", UNEVEN, 5, 600, 264, 0, 0, 1),
     (dict(tile_m=64, tile_n=128), "f16", [8000], 0, 515, 131, 1, 1, 0),
     (dict(tile_m=64, tile_n=64, pipeline=0), "bf16", [300, 77, 0, 900], 9, 200, 520, 0, 0, 0),
+    (dict(tile_m=64, tile_n=128, pipeline=0), "f16", [700], 0, 4100, 2050, 0, 1, 1),
     (dict(tile_m=64, tile_n=64, pipeline=1), "f32", [700, 0, 333], 4, 300, 129, 1, 0, 1),
     (dict(kernel="stream"), "bf16", [5, 0, 9], 1, 100, 410, 1, 0, 1),
 ]

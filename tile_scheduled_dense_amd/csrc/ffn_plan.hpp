@@ -40,9 +40,17 @@ inline int few_splits(int64_t groups, int64_t enough, int64_t stages, int64_t le
 //    the strips are few (one expert of 4096 x 2048, 65 rows 15.9 us against 25.3 on 128 x 64,
 //    128 rows 18.5 and 25.0, 256 rows 25.1 and 25.0; 8 experts of 2048 x 1024, 640 rows, 256
 //    strips, 23.6 and 19.4; fp32, 640 rows 101 and 65).
+//  * Split too for more rows where tiles are few and K is long (at most 128 tiles, fp32 64, of
+//    64 K tiles or more; a split 32, fp32 16: 256 rows of 1024 x 4096 bf16 in 1 and 4 splits 34.5 and
+//    19.7 us, 512 rows in 1 and 2 36.1 and 28.5, of 512 x 1024 in 1 and 2 11.2 and 12.1; fp32
+//    325 rows of 104 x 3320 in 1 and 8 99 and 24, 512 rows of 1024 x 1024, 128 tiles, 34.9 and 40.8).
 //  * The same tile, not split, in 16 bits where tiles of 128 x 64 are up to 400 (517 x 1001, 2501
-//    rows 24.2 us against 25.8; 1024 x 512 18.1 and 18.9; 8192 rows 49.4 and 45).
-//  * 256 x 128 with the pipeline where K is long and the tiles fill half the card, as the products do.
+//    rows 24.2 us against 25.8; 1024 x 512 18.1 and 18.9; 8192 rows 49.4 and 45), but not where K
+//    is long and tiles are more than the CUs (375 rows of 4208 x 6152 155 and 107; 13462 rows of
+//    136 x 4840 150 and 117; 1024 rows of 1024 x 4096, 256 tiles, 41.3 and 42.7).
+//  * 256 x 128 with the pipeline where K is long and the tiles fill more than half the card (256
+//    tiles, 2048 rows of 4096 x 4096, 104 us, on 128 x 64 164; 128 tiles, 512 rows of 8192 x 4096, 111
+//    and 95, 4096 rows of 1024 x 8192 174 and 163, 1024 rows of 4096 x 4096 76.8 and 79.2).
 // The splits of K go up to 256 workgroups (48 rows f16, 128, 256, 512, 1024 workgroups: 44.1, 33.8,
 // 39.8, 47.0 us; 2816 x 1024, 1 row in 1 split 8.0, in 2 10.9), none shorter than the waves' stages.
 struct GatedPlan {
@@ -63,16 +71,18 @@ GatedPlan plan_gated_as(int64_t experts, int64_t rows, int64_t N, int64_t K) {
                             tiles_and_slots(rows, experts, 16));
         return p;
     }
-    const int64_t strips = cdiv(N, 64) * used;
+    const int64_t strips = cdiv(N, 64) * used, k_tiles = cdiv(K, 64 / S::E), all = cdiv(N, 64) * (cdiv(rows, 64) + used - 1);
     const bool split = mean <= 64 || (DT != DT_F32 && mean <= 128 && strips <= 128);
-    if (split || (DT != DT_F32 && cdiv(rows, 128) * cdiv(N, 64) <= 400)) {
-        p.splits = split ? few_splits(strips, 256, cdiv(K, 64 / S::E), 8) : 1;
+    const bool deep = !split && k_tiles >= 64 && all <= (DT == DT_F32 ? 64 : 128);
+    if (split || deep || (DT != DT_F32 && cdiv(rows, 128) * cdiv(N, 64) <= 400 && (K < 2048 || all <= 256))) {
+        p.splits = split ? few_splits(strips, 256, k_tiles, 8)
+                         : (deep ? few_splits(all, 256, k_tiles, DT == DT_F32 ? 16 : 32) : 1);
         p.product = plan_of(TG_EXPERTS_TILES, 64, 64, 4, cdiv(N, 64) * p.splits, tiles_and_slots(rows, experts, 64));
         return p;
     }
     const int64_t tiles = cdiv(rows, 256) * cdiv(N, 128);
     if (DT == DT_F32) p.product = plan_tiles(experts, rows, N, 64, 64, false, true, 4);
-    else if (K >= kLong && tiles >= 128) p.product = plan_tiles(experts, rows, N, 256, 128, true, true, 4);
+    else if (K >= kLong && tiles > 128) p.product = plan_tiles(experts, rows, N, 256, 128, true, true, 4);
     else p.product = plan_tiles(experts, rows, N, 128, 64, false, false, 3);
     return p;
 }
@@ -87,13 +97,14 @@ inline int64_t gated_workspace(const GatedPlan &p, int64_t rows, int64_t N) {
 // The gate's gradient: the products' own rule (plan_grouped_as), but the smaller tiles of 16
 // bits are smaller still, their epilogue reads and writes four matrices: 128 x 128, 64 x 128 and
 // 64 x 64 take 32.3, 25.6, 20.8 us (2501 rows of 517 x 1001), 23, 17.7, 14.8 (1024 x 512), 44,
-// 37.9, 39.0 (8192 rows); the large tiles of 256 x 256 stay (16384 rows of 8 experts of 2048 x
+// 37.9, 39.0 (8192 rows); with a long K 64 x 128 and 64 x 64 take 70.6 and 61.8 (2048 rows of 1024 x
+// 8192, 256 tiles), 28.4 and 29.7 (1024 of 2816 x 2048, 352), 66 and 90 (512 of 8192 x 4096, 512); the large tiles of 256 x 256 stay (16384 rows of 8 experts of 2048 x
 // 2048 210 us, 128 x 128 234, 64 x 64 354).
 template <int DT, bool TRANS>
 ProductPlan plan_gate_grad_as(int64_t experts, int64_t rows, int64_t N, int64_t K) {
     const ProductPlan p = plan_grouped_as<DT, TRANS>(experts, rows, N, K);
     if (DT == DT_F32 || p.info.kernel != TG_EXPERTS_TILES || p.info.tile_m == 256) return p;
-    return plan_tiles(experts, rows, N, 64, cdiv(rows, 64) * cdiv(N, 128) <= 512 ? 64 : 128, false, false, 4);
+    return plan_tiles(experts, rows, N, 64, cdiv(rows, 64) * cdiv(N, 128) <= (K < 2048 ? 512 : 300) ? 64 : 128, false, false, 4);
 }
 
 template <int DT>
