@@ -45,6 +45,8 @@ ADAPTERS = [
     (dict(tile_m=256, pieces=1, pipeline=1), "bf16", 5, 4100, 100, 2060, 1024, 40, 0, 0, 0),
     (dict(tile_m=256, pieces=1, pipeline=1), "f16", 70, 4230, 0, 2059, 1031, 16, 1, 1, 1),
     (dict(tile_m=256, pieces=1, pipeline=1), "bf16", 1, 4096, 0, 2048, 1056, 100, 0, 0, 1),
+    (dict(tile_m=256, splits=2, pieces=0, pipeline=1), "bf16", 5, 2100, 100, 2060, 6200, 40, 0, 0, 0),
+    (dict(tile_m=256, splits=2, pieces=0, pipeline=1), "f16", 70, 1807, 0, 2307, 6231, 16, 1, 1, 1),
     (dict(tile_m=128, splits=1), "f16", 9, 4100, 33, 1100, 264, 8, 0, 0, 0),
     (dict(tile_m=128, splits=1), "bf16", 3, 5000, 0, 1001, 131, 33, 1, 1, 1),
     (dict(tile_m=64, splits=4), "bf16", 7, 300, 20, 520, 1100, 24, 0, 0, 1),

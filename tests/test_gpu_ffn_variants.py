@@ -141,7 +141,7 @@ def test_gate_of_large_and_special_values(kind):
 
 # ---- values that are not finite ---------------------------------------------------------------
 @pytest.mark.parametrize("rows,K,N,shuffled", [(50, 200, 136, True), (300, 200, 136, False), (300, 1100, 520, True),
-                                               (1100, 1100, 520, True), (900, 200, 520, False), (4200, 1024, 2060, True)])
+                                               (1100, 1100, 520, True), (900, 200, 520, False), (1807, 6200, 2307, True), (4200, 1024, 2060, True)])
 @pytest.mark.parametrize("transposed", [0, 1])
 @pytest.mark.parametrize("what", [float("inf"), float("nan")])
 def test_an_adapter_of_infinities_reaches_its_own_rows_only(rows, K, N, shuffled, transposed, what):

@@ -20,15 +20,13 @@ template <int DT> using Tile64 = RingCfg<DT, 64, 64, 2, 2, 16>;
 template <class C, class P, bool KS, bool ORDERED, bool PIPE, int STAGES>
 tg_status launch_adapter_tiles(const AdapterParams &p, const ProductPlan &plan, hipStream_t s) {
     const dim3 grid((unsigned)plan.gx), block(C::THREADS);
-    if constexpr (std::is_same<C, P>::value) {
-        if (p.splits > 1) {
-            hipLaunchKernelGGL((adapters_tile_split_kernel<C, KS, ORDERED, PIPE, STAGES>), grid, block, 0, s, p);
-            const tg_status st = launched();
-            if (st != TG_OK) return st;
-            const int64_t sums = cdiv((int64_t)p.rows * cdiv(p.N, 4), 256);
-            hipLaunchKernelGGL((adapters_sum_kernel<C::DT>), dim3((unsigned)sums), dim3(256), 0, s, p);
-            return launched();
-        }
+    if (p.splits > 1) {
+        hipLaunchKernelGGL((adapters_tile_split_kernel<C, KS, ORDERED, PIPE, STAGES>), grid, block, 0, s, p);
+        const tg_status st = launched();
+        if (st != TG_OK) return st;
+        const int64_t sums = cdiv((int64_t)p.rows * cdiv(p.N, 4), 256);
+        hipLaunchKernelGGL((adapters_sum_kernel<C::DT>), dim3((unsigned)sums), dim3(256), 0, s, p);
+        return launched();
     }
     hipLaunchKernelGGL((adapters_tile_kernel<C, P, KS, ORDERED, PIPE, STAGES>), grid, block, 0, s, p);
     return launched();

@@ -141,7 +141,10 @@ struct AdapterPlan {
 // tiles up to 256 (64 rows, 128, 256, 512: 21.7, 17.0, 18.9 us, as stored 29.9, 24.4, 27.3), t
 // in 8 splits (4, 8, 16: 18.6, 17.2, 17.5; as stored 8 and 16 24.5 and 28.7).
 // Many: t on tiles of 64 x 64, split up to 512 workgroups (8192 rows, up to 512 252 us, 2048 259);
-// the product as the products have it, its smaller tiles split too where a half is still 16
+// the product as the products have it, 256 x 256 in two halves of a very long K too where whole
+// ones would leave up to three quarters of the CUs idle (against 128 x 128: 796 rows of 7296 x 6632 135
+// and 197 us, 2798 of 1800 x 7568 131 and 165, 1792 of 2560 x 8192 120 and 139, x 4096 74.5 and
+// 71.4, 1280 of 4096 x 4096 77.5 and 72.2), its smaller tiles split where a half is still 16
 // tiles of K long (fp32 771 x 1540, 1333 rows, in 1, 2, 4 splits: 121, 125, 141 us).
 template <int DT, bool TRANS>
 AdapterPlan plan_adapters_as(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank) {
@@ -171,9 +174,10 @@ AdapterPlan plan_adapters_as(int64_t adapters, int64_t rows, int64_t N, int64_t 
         const int64_t tiles = cdiv(rows, 256) * cdiv(N, 256);
         if (DT == DT_F32) p.product = plan_tiles(1, rows, N, 64, 64, false, true, 4);
         else if (K >= kLong && tiles >= 128) p.product = plan_tiles(1, rows, N, 256, 256, true, true, 4);
+        else if (K >= 6144 && tiles > 64) p.product = plan_tiles(1, rows, N, 256, 256, false, true, 4), p.splits = 2;
         else p.product = plan_tiles(1, rows, N, 128, 128, false, false, 3);
-        if (p.product.info.tile_m < 256) {
-            p.splits = few_splits(p.product.gx, 512, k_tiles, 16);
+        if (p.splits > 1 || p.product.info.tile_m < 256) {
+            if (p.splits == 1) p.splits = few_splits(p.product.gx, 512, k_tiles, 16);
             if (p.splits > 1) p.part_bytes = part_bytes(p.splits, rows, N, 4);
             const bool pipeline = p.product.info.pipeline;
             p.product = plan_of(TG_EXPERTS_TILES, p.product.info.tile_m, p.product.info.tile_n, 4, p.product.gx * p.splits);
