@@ -31,6 +31,7 @@
 #include <stdint.h>
 
 #include "few_rows.hpp"
+#include "narrow.hpp"
 
 namespace tg {
 
@@ -342,6 +343,28 @@ struct AdapterTile : GroupedTile<C, false, KS, STAGES, OperandX<C, ORDERED>, Ope
         }
     }
 
+    // A K tile from registers through the first LDS copy, whose last readers are done.
+    __device__ __forceinline__ void multiply(const u32x4 (&ta)[OA::PER], const u32x4 (&tb)[OB::PER]) {
+        this->a.tail_store(0, ta);
+        this->b.tail_store(0, tb);
+        wait_lds();
+        block_barrier();
+        u32x4 fa[C::TM], fb[C::TN];
+#pragma unroll
+        for (int r = 0; r < AdapterTile::READS; ++r) this->read_piece(0, r, fa, fb);
+        static_for<0, AdapterTile::NMFMA, 1>([&](auto q) { this->template mma<false, decltype(q)::value>(fa, fb); });
+        wait_lds();
+    }
+    // The K tile at k0, behind those of the ring, of K in all.
+    __device__ __forceinline__ void cut_tile(int k0, int K) {
+        u32x4 ta[OA::PER], tb[OB::PER];
+        this->a.tail_load(k0, K, ta);
+        this->b.tail_load(k0, K, tb);
+        block_barrier();
+        multiply(ta, tb);
+        this->acc.settle();
+    }
+
     // The K tile of B[g] at rank k0 (columns from n0), zeros past its ends; whether any of
     // the workgroup's values is not finite.
     __device__ __forceinline__ void load_up(const AdapterParams &p, int g, int n0, int k0, u32x4 (&tb)[OB::PER]) const {
@@ -397,16 +420,7 @@ struct AdapterTile : GroupedTile<C, false, KS, STAGES, OperandX<C, ORDERED>, Ope
                 } else {
                     block_barrier();               // the copy's last readers are done
                 }
-                this->a.tail_store(0, ta);
-                this->b.tail_store(0, tb);
-                wait_lds();
-                block_barrier();
-                u32x4 fa[C::TM], fb[C::TN];
-#pragma unroll
-                for (int r = 0; r < AdapterTile::READS; ++r) this->read_piece(0, r, fa, fb);
-                static_for<0, AdapterTile::NMFMA, 1>(
-                    [&](auto q) { this->template mma<false, decltype(q)::value>(fa, fb); });
-                wait_lds();
+                multiply(ta, tb);
             }
         });
         this->acc.settle();
@@ -466,9 +480,11 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void shrink_tile_kernel(A
     if (has) split_range((p.K + C::BK - 1) / C::BK, p.t_splits, z, begin, end);
     const int k0 = begin * C::BK, K = (end * C::BK < p.K ? end * C::BK : p.K) - k0, rows = span.hi - span.lo;
     const char *B = p.down + ((has ? (int64_t)g * p.s_down : 0) + (KS ? k0 * p.ld_down + n0 : n0 * p.ld_down + k0)) * C::ELEM;
+    const int ring = KS ? ring_rows(K > 0 ? K : 0, p.rank, C::BK, C::CHUNK) : (K > 0 ? K : 0);
     AdapterTile<C, KS, ORDERED, STAGES> tile;
-    tile.init(p, span.lo, rows, k0, K > 0 ? K : 0, B, p.ld_down, p.rank - n0, smem);
+    tile.init(p, span.lo, rows, k0, ring, B, p.ld_down, p.rank - n0, smem);
     tile.run_ring();
+    if (KS && ring < K) tile.cut_tile(ring, K);
     const float scale = has && p.scales ? p.scales[g] : 1.0f;
     const auto value = [&](auto i, auto j, auto v) {
         return tile.acc.get(decltype(i)::value, decltype(j)::value, decltype(v)::value) * scale;

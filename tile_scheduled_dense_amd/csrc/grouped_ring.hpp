@@ -14,8 +14,8 @@
 //
 // The extents' fringe: a row or column chunk past the end is fetched from past
 // the resource, which reads 0.  A chunk that the end cuts brings what lies
-// behind, in the same matrix (the host keeps extents below one chunk away), and
-// only feeds outputs that are not stored.  A last K tile that K cuts (or whose
+// behind, in the same matrix (the host keeps extents below one chunk away; for an
+// adapter's rank narrow.hpp), and only feeds outputs that are not stored.  A last K tile that K cuts (or whose
 // last chunk would pass a matrix's end) goes through registers with element-exact
 // zeros in both operands, so that a NaN behind K meets none.
 //
