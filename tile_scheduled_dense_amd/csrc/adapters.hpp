@@ -379,24 +379,40 @@ struct AdapterTile : GroupedTile<C, false, KS, STAGES, OperandX<C, ORDERED>, Ope
             tb[d] = bload16_n<C::ELEM>(rb, n > 0 ? at * C::ELEM : 0, 0, n);
         }
     }
+    static constexpr uint32_t EXP = C::DT == DT_F32 ? 0x7f800000u : (C::DT == DT_BF16 ? 0x7f80u : 0x7c00u);
     __device__ __forceinline__ static bool not_finite(const u32x4 (&t)[OB::PER]) {
-        constexpr uint32_t E = C::DT == DT_F32 ? 0x7f800000u : (C::DT == DT_BF16 ? 0x7f80u : 0x7c00u);
         bool bad = false;
 #pragma unroll
         for (int d = 0; d < OB::PER; ++d)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                bad |= (t[d][w] & E) == E;
-                if (C::DT != DT_F32) bad |= (t[d][w] >> 16 & E) == E;
+                bad |= (t[d][w] & EXP) == EXP;
+                if (C::DT != DT_F32) bad |= (t[d][w] >> 16 & EXP) == EXP;
             }
         return __syncthreads_or(bad);
+    }
+    // the values that are not finite as zeros
+    __device__ __forceinline__ static void clear_not_finite(u32x4 (&t)[OB::PER]) {
+#pragma unroll
+        for (int d = 0; d < OB::PER; ++d)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t x = t[d][w];
+                if (C::DT == DT_F32) {
+                    x = (x & EXP) == EXP ? 0 : x;
+                } else {
+                    x = (x & EXP) == EXP ? x & 0xffff0000u : x;
+                    x = (x >> 16 & EXP) == EXP ? x & 0xffffu : x;
+                }
+                t[d][w] = x;
+            }
     }
 
     // The contraction goes on: t . B[g] for every adapter with positions in the tile, in
     // K tiles of the rank through registers, one at a time (an adapter of 32 and less is
     // one), other adapters' rows and what lies past the rank as zeros.  Those zeros would make
-    // NaN of an infinity or NaN in B[g], in other adapters' rows: such a K tile is left
-    // out, and true is returned, unless all of the tile's positions are g's.
+    // NaN of an infinity or NaN in B[g], in other adapters' rows: such values are left out,
+    // and true is returned, unless all of the tile's positions are g's.
     __device__ __forceinline__ bool adapters(const AdapterParams &p, int m0, int n0) {
         if (this->nk == 0) return false;           // t is zero too
         const int m_here = p.rows - m0 < C::BM ? p.rows - m0 : C::BM;
@@ -415,7 +431,7 @@ struct AdapterTile : GroupedTile<C, false, KS, STAGES, OperandX<C, ORDERED>, Ope
                 if (hi - lo < m_here) {
                     if (not_finite(tb)) {
                         left_out = true;
-                        continue;
+                        clear_not_finite(tb);
                     }
                 } else {
                     block_barrier();               // the copy's last readers are done
@@ -426,8 +442,8 @@ struct AdapterTile : GroupedTile<C, false, KS, STAGES, OperandX<C, ORDERED>, Ope
         this->acc.settle();
         return left_out;
     }
-    // What adapters() left out, element by element, onto the stored result: value(position
-    // in the tile, column, sum).
+    // What adapters() left out, element by element, onto the stored result: add(position in
+    // the tile, column, sum).  Such a sum is an infinity or NaN, whatever the result was rounded to.
     template <class F>
     __device__ __forceinline__ void left_out(const AdapterParams &p, int m0, int n0, const F &add) const {
         typedef typename ElemOf<C::DT>::type T;
@@ -446,9 +462,14 @@ struct AdapterTile : GroupedTile<C, false, KS, STAGES, OperandX<C, ORDERED>, Ope
                 for (int i = threadIdx.x; i < (hi - lo) * n_here; i += C::THREADS) {
                     const int m = lo + i / n_here, n = i % n_here;
                     float sum = 0;
-                    for (int k = k0; k < k_end; ++k)
-                        sum += (float)low[m * p.ld_low + k] * (float)(KS ? up[k * p.ld_up + n0 + n] : up[(n0 + n) * p.ld_up + k]);
-                    add(m, n, sum);
+                    bool any = false;
+                    for (int k = k0; k < k_end; ++k) {
+                        const float b = (float)(KS ? up[k * p.ld_up + n0 + n] : up[(n0 + n) * p.ld_up + k]);
+                        if (__builtin_isfinite(b)) continue;
+                        sum += (float)low[m * p.ld_low + k] * b;
+                        any = true;
+                    }
+                    if (any) add(m, n, sum);
                 }
             }
         });
