@@ -186,6 +186,11 @@ __global__ __launch_bounds__(C::THREADS, C::OCCUPANCY) void adapters_split_kerne
 // columns, 14 us.)
 constexpr int kJoinRank = 256;
 template <bool TRANS> constexpr int join_cols() { return TRANS ? 1 : 2; }
+// workgroups of a position; one without columns too, for T
+template <bool TRANS>
+__host__ __device__ constexpr int64_t join_parts(int64_t N) {
+    return N > 0 ? (N + 256 * join_cols<TRANS>() - 1) / (256 * join_cols<TRANS>()) : 1;
+}
 template <int DT, bool TRANS>
 __global__ __launch_bounds__(256) void adapters_join_kernel(AdapterParams p) {
     typedef typename ElemOf<DT>::type E;
@@ -193,7 +198,7 @@ __global__ __launch_bounds__(256) void adapters_join_kernel(AdapterParams p) {
     typedef Two __attribute__((aligned(sizeof(E)))) TwoAnywhere;
     constexpr int COLS = join_cols<TRANS>(), STEP = TRANS ? Chunk<DT>::PER : 16, BYTES = (int)sizeof(E);
     __shared__ float t[kJoinRank + STEP];
-    const int parts = (p.N + 256 * COLS - 1) / (256 * COLS), pos = blockIdx.x / parts, part = blockIdx.x % parts;
+    const int parts = (int)join_parts<TRANS>(p.N), pos = blockIdx.x / parts, part = blockIdx.x % parts;
     const int g = group_of(p.offsets, p.experts, pos);
     const int64_t r = row_at(p, pos);
     const int c = COLS * (part * 256 + (int)threadIdx.x), left = p.N - c;

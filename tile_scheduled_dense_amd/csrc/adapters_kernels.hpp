@@ -70,7 +70,7 @@ tg_status launch_adapters_as(AdapterParams p, void *workspace, hipStream_t s) {
     if (plan.form == ADAPTERS_TILES)
         return p.order ? launch_adapters_many<DT, !TRANS, true>(p, plan, s) : launch_adapters_many<DT, !TRANS, false>(p, plan, s);
     const int64_t low = p.rank > 0 ? plan.low.gx * plan.low.gy * plan.low.gz : 0, strips_t = cdiv(p.rank, S::COLS);
-    const int64_t join = cdiv(p.N, 256 * join_cols<TRANS>()) * p.rows;
+    const int64_t join = join_parts<TRANS>(p.N) * p.rows;
     if (!grid_fits(join, 256)) return TG_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)(low + plan.product.gx)), block(64 * plan.product.info.waves);
     if (plan.form == ADAPTERS_STREAM)
