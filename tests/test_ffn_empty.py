@@ -34,3 +34,9 @@ def test_without_a_device_there_is_no_t():
     if torch.cuda.is_available():
         pytest.skip("a GPU is visible")
     assert call("tile_gemm_adapters", ADAPT, **NONE) == OK
+
+
+def test_sums_that_no_memory_holds_matter_where_t_is_asked_for():
+    big = dict(NONE, rows=1 << 30, rank=1 << 30, lda=1 << 30, ldt=1 << 30, ldx=48)
+    assert call("tile_gemm_adapters", ADAPT, **big, workspace_bytes=1 << 60) == tg.TG_ERR_UNSUPPORTED
+    assert call("tile_gemm_adapters", ADAPT, **{**big, "T": None, "workspace": None}) == OK

@@ -271,14 +271,15 @@ tg_status gate(bool grad, int64_t rows, int64_t N, tg_dtype dtype, int activatio
 }
 
 // ---- adapters ---------------------------------------------------------------------------------
+// with_t: t is computed, where N is 0 too
 tg_status adapter_plan(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, tg_dtype dtype, int transposed,
-                       AdapterPlan &plan) {
+                       bool with_t, AdapterPlan &plan) {
     const tg_status st = sizes(adapters, rows, N, K, dtype, transposed);
     if (st == TG_ERR_INVALID_ARG || rank < 0) return TG_ERR_INVALID_ARG;
     if (st != TG_OK) return st;
     if (rank > kMaxExtent) return TG_ERR_UNSUPPORTED;
     plan = {};
-    if (rows == 0) return TG_OK;
+    if (rows == 0 || (N == 0 && !with_t)) return TG_OK;
     const bool t = transposed != 0;
     plan = dtype == TG_F32    ? plan_adapters<DT_F32>(t, adapters, rows, N, K, rank)
            : dtype == TG_BF16 ? plan_adapters<DT_BF16>(t, adapters, rows, N, K, rank)
@@ -292,7 +293,7 @@ tg_status adapters(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t
                    int64_t ldt, const int32_t *offsets, const int32_t *order, void *workspace, int64_t workspace_bytes,
                    void *stream) {
     AdapterPlan plan;
-    tg_status st = adapter_plan(adapters, rows, N, K, rank, dtype, transposed, plan);
+    tg_status st = adapter_plan(adapters, rows, N, K, rank, dtype, transposed, T != nullptr, plan);
     if (st != TG_OK) return st;
     const int esz = size_of(dtype);
     const int64_t any = rows > 0;
@@ -358,7 +359,7 @@ tg_status adapters(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t
 tg_status adapters_plan(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank, tg_dtype dtype, int transposed,
                         tg_ffn_plan_info *out) {
     AdapterPlan plan;
-    const tg_status st = adapter_plan(adapters, rows, N, K, rank, dtype, transposed, plan);
+    const tg_status st = adapter_plan(adapters, rows, N, K, rank, dtype, transposed, false, plan);
     if (st == TG_ERR_INVALID_ARG || !out) return TG_ERR_INVALID_ARG;
     if (st != TG_OK) return st;
     *out = {};
@@ -491,7 +492,7 @@ tg_status tile_gemm_adapters_workspace_size(int64_t adapters, int64_t rows, int6
                                             tg_dtype dtype, int transposed, int64_t *bytes) {
     if (!bytes) return TG_ERR_INVALID_ARG;
     AdapterPlan plan;
-    const tg_status st = adapter_plan(adapters, rows, N, K, rank, dtype, transposed, plan);
+    const tg_status st = adapter_plan(adapters, rows, N, K, rank, dtype, transposed, true, plan);
     if (st == TG_OK) *bytes = plan.bytes;
     return st;
 }
