@@ -48,3 +48,19 @@ def test_rows_of_a_broken_adapter_are_rounded_once(dt, large, transposed, shuffl
     got = y[own, 5].float()
     assert bool(torch.isnan(got).all() if what != what else (got == what).all())
     assert torch.equal(t[:, 0].float(), torch.ones(rows))
+
+
+@pytest.mark.parametrize("rows", [50, 700])
+@pytest.mark.parametrize("transposed", [0, 1])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_zero_times_infinity_without_inputs(dt, rows, transposed):
+    """K = 0: t is 0, and 0 times an adapter's infinity no number, in its own rows, whichever kernel takes them."""
+    c = AdapterCase(dt, 3, rows, 9, 3, 136, 0, 4, 0, 0, transposed, True, True, scaled=False)
+    b = c.b.transpose(-1, -2) if transposed else c.b
+    b[1, 2, 5] = float("inf")
+    y, t = c.run()
+    own = torch.zeros(rows, dtype=torch.bool)
+    own[ref.group_rows(c.offsets, 1, c.order)] = True
+    assert 0 < int(own.sum()) < rows
+    assert torch.isnan(y[own, 5]).all() and not t.any()
+    assert not y[~own].any() and not y[:, torch.arange(136) != 5].any()

@@ -419,7 +419,6 @@ struct AdapterTile : GroupedTile<C, false, KS, STAGES, OperandX<C, ORDERED>, Ope
     // NaN of an infinity or NaN in B[g], in other adapters' rows: such values are left out,
     // and true is returned, unless all of the tile's positions are g's.
     __device__ __forceinline__ bool adapters(const AdapterParams &p, int m0, int n0) {
-        if (this->nk == 0) return false;           // t is zero too
         const int m_here = p.rows - m0 < C::BM ? p.rows - m0 : C::BM;
         const rsrc_t rt = make_rsrc(p.low + (int64_t)m0 * p.ld_low * C::ELEM);
         bool left_out = false;
