@@ -22,10 +22,12 @@
  *  - Activations by the numbers of tile_gemm.h's fused tail: 0 none, 1 ReLU, 2 GELU (x Phi(x));
  *    3 is SiLU, x / (1 + e^-x).
  *  - Results are of dtype, except where a c_dtype is given; sums and the activation's
- *    argument are fp32.  t enters the second product in fp32 where rows are few (up to 64,
- *    or 512 with at most 192 tiles of 64 x 64 in y), and rounded once to dtype (as T is)
- *    where there are more.  A NaN or an infinity in a row, or in an adapter,
- *    reaches that row's, or that adapter's rows', results only.
+ *    argument are fp32.  t enters the second product in fp32 where rows are few (up to 64;
+ *    up to 512 with at most 192 tiles of 64 x 64 in y; any number with N below 8), and rounded
+ *    once to dtype (as T is) where there are more: how exact a row's y is goes by the rows and
+ *    columns of its call, and in TG_F16 a t past 65504 is an infinity there, which y gets.
+ *    A NaN or an infinity in a row, or in an adapter, reaches that row's, or that adapter's
+ *    rows', results only.
  *  - transposed 0: matrices are inputs x outputs (Bg, Bu, W: K x N, an adapter's A: K x rank,
  *    B: rank x N); 1: outputs x inputs (N x K, rank x K, N x rank).
  *  - Rows without an expert get zeros in h, u, v and in d_u, d_v (u and v are not read

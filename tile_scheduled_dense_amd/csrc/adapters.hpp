@@ -21,10 +21,10 @@
 //    chunk of an adapter's rows, a second launch adds the chunks in their order.
 //
 // Measured, inputs that change from call to call: 1 row, rank 16, 4096 x 4096 bf16 12.9 us
-// (33.8 MB; the sums 9, the join 3.5); 64 rows of 20 adapters of rank 32 16.7 us (12 and 5.6); 8192
-// rows, 4 adapters of rank 64, 4096 x 4096 f16 252 us, of which t is 28 (x from HBM while the last
-// results go there) and the product 222 (1270 TFLOP/s); gradients of two adapters of rank
-// 16, 8192 rows of 2048 and 4096, 27 us (100 MB, 3.7 TB/s) and 6 to add up.
+// (33.8 MB; under a profiler the sums 10.7, the join 3.8); 64 rows of 20 adapters of rank 32
+// 16.7 us (12 and 5.6); 8192 rows, 4 adapters of rank 64, 4096 x 4096 f16 252 us, of which t is 28
+// (x from HBM while the last results go there) and the product 222 (1270 TFLOP/s); gradients of two
+// adapters of rank 16, 8192 rows of 2048 and 4096, 27 us (100 MB, 3.7 TB/s) and 6 to add up.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -609,7 +609,10 @@ __global__ __launch_bounds__(256) void adapters_sum_kernel(AdapterParams p) {
 // transposed in LDS, 16 JT of the rank.  An adapter of one chunk gets its result at once;
 // else fp32 sums, rank x M of each chunk, go to the workspace: an adapter's first to place
 // offsets[g] / kChunk (no other adapter of several chunks starts there), the further ones
-// to their slots behind all of those.  Bound by the bytes of L.
+// to their slots behind all of those.  Bound by the bytes of L while the rank is small; the
+// sums are rank / 128 of its bytes in 16 bits, written and read again (8192 rows of 4096 and 4096
+// bf16, two adapters: rank 16 55 us, 32 67, 64 92, 128 143), and above rank 32 a wave is alone on
+// its SIMD.
 constexpr int kChunk = 256;
 constexpr int kWgradRank = 64;        // of the rank at a time
 

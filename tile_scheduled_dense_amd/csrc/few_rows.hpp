@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256) void gated_join_kernel(GatedParams p) {
     });
 }
 
-// The gate's gradient; no split (a training batch of few rows is not what it is for).
+// The gate's gradient; K is split over the waves alone (plan_gate_grad_as).
 template <int DT, bool TRANS>
 __global__ __launch_bounds__(512) void gate_grad_few_kernel(GatedParams p) {
     using S = StreamShape<DT, TRANS>;

@@ -98,8 +98,10 @@ inline int64_t gated_workspace(const GatedPlan &p, int64_t rows, int64_t N) {
 // bits are smaller still, their epilogue reads and writes four matrices: 128 x 128, 64 x 128 and
 // 64 x 64 take 32.3, 25.6, 20.8 us (2501 rows of 517 x 1001), 23, 17.7, 14.8 (1024 x 512), 44,
 // 37.9, 39.0 (8192 rows); with a long K 64 x 128 and 64 x 64 take 70.6 and 61.8 (2048 rows of 1024 x
-// 8192, 256 tiles), 28.4 and 29.7 (1024 of 2816 x 2048, 352), 66 and 90 (512 of 8192 x 4096, 512); the large tiles of 256 x 256 stay (16384 rows of 8 experts of 2048 x
-// 2048 210 us, 128 x 128 234, 64 x 64 354).
+// 8192, 256 tiles), 28.4 and 29.7 (1024 of 2816 x 2048, 352), 66 and 90 (512 of 8192 x 4096, 512);
+// the large tiles of 256 x 256 stay (16384 rows of 8 experts of 2048 x 2048 210 us, 128 x 128 234,
+// 64 x 64 354).  K is not split here, so a long one with few tiles leaves CUs idle (bf16, 100 rows
+// of 500 x 8000, streamed, 32 workgroups, 186 us, where the pair itself takes 18 in 16 splits).
 template <int DT, bool TRANS>
 ProductPlan plan_gate_grad_as(int64_t experts, int64_t rows, int64_t N, int64_t K) {
     const ProductPlan p = plan_grouped_as<DT, TRANS>(experts, rows, N, K);
@@ -121,6 +123,10 @@ ProductPlan plan_gate_grad(bool transposed, int64_t experts, int64_t rows, int64
 // 256 rows 39.3 and 49.3; 16384 x 4096, 128 rows (512 tiles) 104 and 82; 1024 x 4096,
 // 768 rows 43.8 and 37.6; one adapter of rank 64 of 512 x 8192, 1024 rows 54.8 and 37.0; fp32
 // 4096 x 4096, 256 rows (256 tiles) 124 and 90; 771 x 1540, 512 rows (104 tiles) 59.7 and 85.0.
+// The rank is not looked at, though few rows read its B again for each: 8 adapters of rank 128,
+// bf16, as stored and transposed, 65 rows of 4096 x 4096 32.4 and 39.0 us against 61.2 and 56.6 as
+// many, 192 rows 51.1 and 78.7 against 55.6 and 52.1; of rank 512, 65 rows 71.2 and 98.7 against 202
+// and 177, 192 rows 110 and 228 against 151 and 135; 512 rows of 1536 x 4096, rank 1024, 157 and 95.5.
 inline bool adapters_few(int64_t rows, int64_t N) {
     return rows <= 64 || N < kNarrow || (rows <= 512 && cdiv(rows, 64) * cdiv(N, 64) <= 192);
 }
@@ -144,7 +150,9 @@ struct AdapterPlan {
 // the product as the products have it, 256 x 256 in two halves of a very long K too where whole
 // ones would leave up to three quarters of the CUs idle (against 128 x 128: 796 rows of 7296 x 6632 135
 // and 197 us, 2798 of 1800 x 7568 131 and 165, 1792 of 2560 x 8192 120 and 139, x 4096 74.5 and
-// 71.4, 1280 of 4096 x 4096 77.5 and 72.2), its smaller tiles split where a half is still 16
+// 71.4, 1280 of 4096 x 4096 77.5 and 72.2; 512 of 8704 x 8192, 68 tiles, 128 and 173, of 8192 x 8192,
+// 64 tiles, 120 and 112, 1024 of 4096 x 8192, 64, 120 and 115, 2048 of 1536 x 8192, 48, 110 and 84.7;
+// 1792 of 2560 x 6144, 70 tiles, 100 and 111, 1024 of 4352 x 6144, 68, 105 and 98, x 5120 92 and 84), its smaller tiles split where a half is still 16
 // tiles of K long (fp32 771 x 1540, 1333 rows, in 1, 2, 4 splits: 121, 125, 141 us).
 template <int DT, bool TRANS>
 AdapterPlan plan_adapters_as(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank) {
