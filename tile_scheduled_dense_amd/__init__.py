@@ -252,7 +252,7 @@ def _addr(x) -> Optional[int]:
     if x is None or type(x) is int:
         return x
     try:
-        return int(x.data_ptr())
+        return x.data_ptr()
     except AttributeError:
         if isinstance(x, int):
             return x
