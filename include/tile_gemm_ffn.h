@@ -98,8 +98,8 @@ tg_status tile_gemm_gate_grad(int64_t rows, int64_t N, tg_dtype dtype, int activ
  * scales: one fp32 an adapter, NULL: 1.  Adapter g has the positions offsets[g] .. offsets[g + 1] - 1
  * of the adapters' order, those from offsets[adapters] on have none; position p is row order[p]
  * of X, Y and T (order[p] or its complement: tile_gemm_expert_sort's entry_of_row, with one
- * choice a row, is such a table; it must hold every row once), or row p where order is NULL.  T (rows x rank, of dtype): t,
- * for the gradients; NULL: not stored.  It is stored where N is 0, too.
+ * choice a row, is such a table; it must hold every row once), or row p where order is NULL.
+ * T (rows x rank, of dtype): t, for the gradients, where N is 0 too; NULL: not stored.
  */
 tg_status tile_gemm_adapters_workspace_size(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank,
                                             tg_dtype dtype, int transposed, int64_t *bytes);

@@ -447,7 +447,8 @@ struct AdapterTile : GroupedTile<C, false, KS, STAGES, OperandX<C, ORDERED>, Ope
         return left_out;
     }
     // What adapters() left out, element by element, onto the stored result: add(position in
-    // the tile, column, sum).  Such a sum is an infinity or NaN, whatever the result was rounded to.
+    // the tile, column, sum).  Such a sum is an infinity or NaN, so that the result's rounding
+    // does not matter (but an infinity that it made of a large value counts as one).
     template <class F>
     __device__ __forceinline__ void left_out(const AdapterParams &p, int m0, int n0, const F &add) const {
         typedef typename ElemOf<C::DT>::type T;

@@ -152,8 +152,9 @@ struct AdapterPlan {
 // and 197 us, 2798 of 1800 x 7568 131 and 165, 1792 of 2560 x 8192 120 and 139, x 4096 74.5 and
 // 71.4, 1280 of 4096 x 4096 77.5 and 72.2; 512 of 8704 x 8192, 68 tiles, 128 and 173, of 8192 x 8192,
 // 64 tiles, 120 and 112, 1024 of 4096 x 8192, 64, 120 and 115, 2048 of 1536 x 8192, 48, 110 and 84.7;
-// 1792 of 2560 x 6144, 70 tiles, 100 and 111, 1024 of 4352 x 6144, 68, 105 and 98, x 5120 92 and 84), its smaller tiles split where a half is still 16
-// tiles of K long (fp32 771 x 1540, 1333 rows, in 1, 2, 4 splits: 121, 125, 141 us).
+// 1792 of 2560 x 6144, 70 tiles, 100 and 111, 1024 of 4352 x 6144, 68, 105 and 98, x 5120 92 and 84),
+// its smaller tiles split where a half is still 16 tiles of K long (fp32 771 x 1540, 1333 rows, in
+// 1, 2, 4 splits: 121, 125, 141 us).
 template <int DT, bool TRANS>
 AdapterPlan plan_adapters_as(int64_t adapters, int64_t rows, int64_t N, int64_t K, int64_t rank) {
     using S = StreamShape<DT, TRANS>;

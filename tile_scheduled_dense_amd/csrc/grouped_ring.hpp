@@ -15,9 +15,9 @@
 // The extents' fringe: a row or column chunk past the end is fetched from past
 // the resource, which reads 0.  A chunk that the end cuts brings what lies
 // behind, in the same matrix (the host keeps extents below one chunk away; for an
-// adapter's rank narrow.hpp), and only feeds outputs that are not stored.  A last K tile that K cuts (or whose
-// last chunk would pass a matrix's end) goes through registers with element-exact
-// zeros in both operands, so that a NaN behind K meets none.
+// adapter's rank narrow.hpp), and only feeds outputs that are not stored.  A last K
+// tile that K cuts (or whose last chunk would pass a matrix's end) goes through
+// registers with element-exact zeros in both operands, so that a NaN behind K meets none.
 //
 // Measured, 16384 rows x 4096 x 2048 bf16 over 8 experts with a bf16 result, inputs that
 // change from call to call: even experts 229 us forward, 229 for the rows' gradient, 219 for
